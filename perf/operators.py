@@ -1,8 +1,8 @@
 """The layer operators around the linear-attention forwards, as measured cases.
 
-short_conv_fwd / short_conv_step   depthwise short causal convolution with SiLU, prompts and one token
-s6_chunk_fwd / s6_recurrent_step   selective state space scan (diagonal A per channel), prompts and one token
-rms_norm_fwd                       RMS norm with the residual's addition or an output gate, 16-bit or e4m3 out
+gdn_short_conv_fwd / gdn_short_conv_step   depthwise short causal convolution with SiLU, prompts and one token
+gdn_s6_chunk_fwd / gdn_s6_recurrent_step   selective state space scan (diagonal A per channel), prompts and one token
+gdn_rms_norm_fwd                           RMS norm with the residual's addition or an output gate, 16-bit or e4m3 out
 
 ``run`` computes them from elementary torch operations in 32 bits, or, where ``own`` is true, by
 the calls of the package.  Packed batches carry sequence borders in an int32 ``cu`` as everywhere
@@ -308,23 +308,23 @@ def _own(s):
     import linear_attention_prefill_gb300 as lap
     case, op = s["case"], s["case"]["op"]
     if op == "conv":
-        y, sT = lap.short_conv_fwd(s["x"], s["weight"], s["bias"], s["s0"],
-                                   activation="silu" if case["silu"] else None, cu_seqlens=s["cu"])
+        y, sT = lap.gdn_short_conv_fwd(s["x"], s["weight"], s["bias"], s["s0"],
+                                       activation="silu" if case["silu"] else None, cu_seqlens=s["cu"])
         return y, sT
     if op == "conv_step":
-        y = lap.short_conv_step(s["x"], s["weight"], s["s0"], s["bias"],
-                                activation="silu" if case["silu"] else None)
+        y = lap.gdn_short_conv_step(s["x"], s["weight"], s["s0"], s["bias"],
+                                    activation="silu" if case["silu"] else None)
         return y, s["s0"]
     if op == "scan":
-        return lap.s6_chunk_fwd(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], s["dt_bias"], s["h0"],
-                                dt_softplus=case["softplus"], cu_seqlens=s["cu"])
+        return lap.gdn_s6_chunk_fwd(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], s["dt_bias"],
+                                    s["h0"], dt_softplus=case["softplus"], cu_seqlens=s["cu"])
     if op == "scan_step":
-        y = lap.s6_recurrent_step(s["x"], s["dt"], s["A"], s["B"], s["C"], s["h0"], s["D"], s["z"], s["dt_bias"],
-                                  dt_softplus=case["softplus"])
+        y = lap.gdn_s6_recurrent_step(s["x"], s["dt"], s["A"], s["B"], s["C"], s["h0"], s["D"], s["z"],
+                                      s["dt_bias"], dt_softplus=case["softplus"])
         return y, s["h0"]
-    y, scale, res = lap.rms_norm_fwd(s["x"], s["weight"], s["residual"], s["gate"], eps=EPS,
-                                     out_dtype=torch.float8_e4m3fn if case["fp8"] else None,
-                                     group=case["group"] or None)
+    y, scale, res = lap.gdn_rms_norm_fwd(s["x"], s["weight"], s["residual"], s["gate"], eps=EPS,
+                                         out_dtype=torch.float8_e4m3fn if case["fp8"] else None,
+                                         group=case["group"] or None)
     return [t for t in (y, scale, res) if t is not None]
 
 
