@@ -342,6 +342,161 @@ gdn_status kda_recurrent_step(const void* q, const void* k, const void* v, const
                               int dk, int dv, float scale, gdn_stream_t stream);
 
 /*
+ * ---- The layer around the forwards -------------------------------------------------
+ *
+ * The operators a linear-attention layer runs before and after gdn_chunk_fwd,
+ * kda_chunk_fwd and ssd_chunk_fwd, and the Mamba-1 member of the family.  The
+ * pages name the projection side only as fused operators ("Empowering Hybrid
+ * Attention Models on NPUs", §7 Implementation); the formulas are the
+ * published ones of these layers.  The conventions at the top hold, except:
+ *  - Row operands that a layer slices out of a wider projection take a stride
+ *    in elements from token to token (>= the row's length; rows of a batch
+ *    follow each other, so token t of row b is at (b T + t) * stride) and need
+ *    only their element's alignment; outputs are dense.  Rows of 16-byte
+ *    aligned, 8-element multiples run on wide accesses, others element by
+ *    element with the same results.
+ *  - cu_seqlens [N + 1]: sequences of a packed row of T tokens.  cu[N] may be
+ *    below T: rows behind the last sequence are left as they were.  The borders
+ *    are clamped to [0, T] on the device; a table that is not ordered gives
+ *    wrong results, never an access outside the tensors.
+ *  - Outputs must not overlap inputs (GDN_ERR_INVALID_ARG), except a state
+ *    output that is exactly the state input: updated in place.
+ *  - Results do not depend on the launch: the same call gives the same bits.
+ */
+
+/* Activations of the short convolution. */
+enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 };
+
+/*
+ * gdn_short_conv_fwd - short causal convolution, one filter per channel, over
+ * the projections before a forward (q, k, v; or x, B, C).  Per channel d:
+ *
+ *   y_t = act(bias[d] + sum_{j < W} w[d, j] x_{t - W + 1 + j})
+ *
+ *   x     N rows of T tokens (or one packed row) of D channels, x_stride, bf16
+ *   w     [D, W] fp32, 16-byte aligned, W in {2, 3, 4}; the last tap meets x_t
+ *   bias  [D] fp32 or NULL
+ *   s0    [N, W - 1, D] bf16: the inputs before each sequence, oldest first, or
+ *         NULL for zeros
+ *   y     [tokens, D] bf16 (fp32 sums, rounded once)
+ *   sT    [N, W - 1, D] bf16: the last W - 1 inputs of each sequence (with s0's
+ *         where it is shorter), or NULL; may equal s0
+ *
+ * gdn_short_conv_step: one token per sequence; x [N, D] (x_stride), s
+ * [N, W - 1, D] shifted in place, y [N, D].  The _f32 forms take fp32 x, y and
+ * states.
+ */
+gdn_status gdn_short_conv_fwd(const void* x, const float* w, const float* bias, const void* s0,
+                              void* y, void* sT, int N, int T, int D, int W, long long x_stride,
+                              int activation, const int32_t* cu_seqlens, gdn_stream_t stream);
+gdn_status gdn_short_conv_fwd_f32(const float* x, const float* w, const float* bias,
+                                  const float* s0, float* y, float* sT, int N, int T, int D, int W,
+                                  long long x_stride, int activation, const int32_t* cu_seqlens,
+                                  gdn_stream_t stream);
+gdn_status gdn_short_conv_step(const void* x, const float* w, const float* bias, void* s, void* y,
+                               int N, int D, int W, long long x_stride, int activation,
+                               gdn_stream_t stream);
+gdn_status gdn_short_conv_step_f32(const float* x, const float* w, const float* bias, float* s,
+                                   float* y, int N, int D, int W, long long x_stride,
+                                   int activation, gdn_stream_t stream);
+
+/*
+ * gdn_s6_chunk_fwd - the selective state space scan with a diagonal A (S6,
+ * Mamba-1): a state of Ns numbers per channel, each with its own decay.  Per
+ * sequence and channel d, tokens in order, D_t = softplus(dt_t + dt_bias) (or
+ * dt_t + dt_bias without dt_softplus):
+ *
+ *   h_t[n] = exp(D_t A[d, n]) h_{t-1}[n] + D_t x_t B_t[n]
+ *   y_t    = (sum_n C_t[n] h_t[n] + D[d] x_t) silu(z_t)
+ *
+ *   x, dt    N rows of T tokens (or one packed row) of dim channels, bf16
+ *   A        [dim, Ns] fp32 (negative: a decay), 16-byte aligned; Ns in 1..64
+ *   B, C     rows of Ns, bf16, shared by every channel
+ *   D        [dim] fp32 or NULL (no skip);  dt_bias  [dim] fp32 or NULL
+ *   z        rows of dim channels, bf16, or NULL (no gate)
+ *   h0, hT   [N, dim, Ns] fp32, NULL for zeros / to skip, 16-byte aligned; hT may
+ *            equal h0
+ *   y        [tokens, dim] bf16
+ *
+ * The state, the steps and every sum are fp32.  Few channels over many tokens
+ * are split over time (exact, in fp32), which needs a device workspace of
+ * gdn_s6_chunk_fwd_workspace_size(...) bytes (0: none), 256-byte aligned; with
+ * workspace NULL the call takes it from the stream-ordered pool.  Calls that
+ * share a workspace must be ordered on one stream.
+ * gdn_s6_recurrent_step: one token per sequence, h [N, dim, Ns] in place, no
+ * workspace.  The _f32 forms take fp32 x, dt, B, C, z and y.
+ */
+size_t gdn_s6_chunk_fwd_workspace_size(int N, int T, int dim, int Ns, int has_cu_seqlens);
+gdn_status gdn_s6_chunk_fwd(const void* x, const void* dt, const float* A, const void* B,
+                            const void* C, const float* D, const void* z, const float* dt_bias,
+                            const float* h0, void* y, float* hT, int N, int T, int dim, int Ns,
+                            long long x_stride, long long dt_stride, long long b_stride,
+                            long long c_stride, long long z_stride, int dt_softplus,
+                            const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes,
+                            gdn_stream_t stream);
+gdn_status gdn_s6_chunk_fwd_f32(const float* x, const float* dt, const float* A, const float* B,
+                                const float* C, const float* D, const float* z,
+                                const float* dt_bias, const float* h0, float* y, float* hT, int N,
+                                int T, int dim, int Ns, long long x_stride, long long dt_stride,
+                                long long b_stride, long long c_stride, long long z_stride,
+                                int dt_softplus, const int32_t* cu_seqlens, void* workspace,
+                                size_t workspace_bytes, gdn_stream_t stream);
+gdn_status gdn_s6_recurrent_step(const void* x, const void* dt, const float* A, const void* B,
+                                 const void* C, const float* D, const void* z,
+                                 const float* dt_bias, float* h, void* y, int N, int dim, int Ns,
+                                 long long x_stride, long long dt_stride, long long b_stride,
+                                 long long c_stride, long long z_stride, int dt_softplus,
+                                 gdn_stream_t stream);
+gdn_status gdn_s6_recurrent_step_f32(const float* x, const float* dt, const float* A,
+                                     const float* B, const float* C, const float* D,
+                                     const float* z, const float* dt_bias, float* h, float* y,
+                                     int N, int dim, int Ns, long long x_stride,
+                                     long long dt_stride, long long b_stride, long long c_stride,
+                                     long long z_stride, int dt_softplus, gdn_stream_t stream);
+
+/*
+ * gdn_rms_norm_fwd - RMS norm of rows of D columns, before a layer's projections
+ * (with the residual) or of each head of a forward's output (with its gate):
+ *
+ *   r = x + residual,   y = r / sqrt(mean(r^2) + eps) * w * silu(gate)
+ *
+ *   x, gate       tokens of `heads` rows of D, x_stride / gate_stride elements
+ *                 from token to token (the rows of a token follow each other);
+ *                 gate may be NULL
+ *   w             [D] fp32
+ *   residual      [tokens, heads, D], or NULL; residual_out (given exactly with
+ *                 it, may equal it) takes r, rounded once
+ *   y             [tokens, heads, D]
+ *   D             at most 32768;  eps >= 0
+ *
+ * x, residual, gate, y and residual_out are bf16 (_f32: fp32).  r, the sum of
+ * squares and y are fp32 up to their rounding on the way out; the norm sees r
+ * before it is rounded.
+ * gdn_rms_norm_fwd_e4m3(_f32): y in 8 bits (e4m3, saturating at 448) with fp32
+ * scales [tokens, heads, ceil(D / group)], one per `group` columns (32, 64 or
+ * 128), or per row with group = 0: scale = max|y| / 448, at least 2^-126, and 1
+ * where every y is 0; the stored value is y / scale rounded to nearest.
+ */
+gdn_status gdn_rms_norm_fwd(const void* x, const float* w, const void* residual, const void* gate,
+                            void* y, void* residual_out, long long tokens, int heads, int D,
+                            long long x_stride, long long gate_stride, float eps,
+                            gdn_stream_t stream);
+gdn_status gdn_rms_norm_fwd_f32(const float* x, const float* w, const float* residual,
+                                const float* gate, float* y, float* residual_out, long long tokens,
+                                int heads, int D, long long x_stride, long long gate_stride,
+                                float eps, gdn_stream_t stream);
+gdn_status gdn_rms_norm_fwd_e4m3(const void* x, const float* w, const void* residual,
+                                 const void* gate, void* y, float* scales, void* residual_out,
+                                 long long tokens, int heads, int D, long long x_stride,
+                                 long long gate_stride, int group, float eps,
+                                 gdn_stream_t stream);
+gdn_status gdn_rms_norm_fwd_e4m3_f32(const float* x, const float* w, const float* residual,
+                                     const float* gate, void* y, float* scales,
+                                     float* residual_out, long long tokens, int heads, int D,
+                                     long long x_stride, long long gate_stride, int group,
+                                     float eps, gdn_stream_t stream);
+
+/*
  * gdn_device_status - waits for `stream`, then reads and clears the device
  * error word.  The kernels record there (the first record stays until read):
  * a bounded device-side wait that gave up (GDN_ERR_TIMEOUT); a KDA log-decay

@@ -29,6 +29,13 @@ _FWD_ARGS = [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P,
 _STEP_ARGS = [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P]
 _SZ = ctypes.c_size_t
 _U = ctypes.c_uint
+_L = ctypes.c_longlong
+_CONV_ARGS = [_P] * 6 + [_I] * 4 + [_L, _I, _P, _P]
+_CONV_STEP_ARGS = [_P] * 5 + [_I] * 3 + [_L, _I, _P]
+_S6_ARGS = [_P] * 11 + [_I] * 4 + [_L] * 5 + [_I, _P, _P, _SZ, _P]
+_S6_STEP_ARGS = [_P] * 10 + [_I] * 3 + [_L] * 5 + [_I, _P]
+_NORM_ARGS = [_P] * 6 + [_L, _I, _I, _L, _L, _F, _P]
+_NORM8_ARGS = [_P] * 7 + [_L, _I, _I, _L, _L, _I, _F, _P]
 SIGNATURES = {
     "gdn_chunk_fwd": (_I, _FWD_ARGS),
     "gdn_chunk_fwd_ex": (_I, _FWD_ARGS[:-1] + [_U, _P, _SZ, _P]),
@@ -56,6 +63,19 @@ SIGNATURES = {
     "gdn_last_error": (ctypes.c_char_p, []),
     "gdn_abi_version": (_I, []),
     "gdn_chunk_fwd_chain_kind": (_I, [_I, _I, _I, _I, _I, _U]),
+    "gdn_short_conv_fwd": (_I, _CONV_ARGS),
+    "gdn_short_conv_fwd_f32": (_I, _CONV_ARGS),
+    "gdn_short_conv_step": (_I, _CONV_STEP_ARGS),
+    "gdn_short_conv_step_f32": (_I, _CONV_STEP_ARGS),
+    "gdn_s6_chunk_fwd": (_I, _S6_ARGS),
+    "gdn_s6_chunk_fwd_f32": (_I, _S6_ARGS),
+    "gdn_s6_chunk_fwd_workspace_size": (_SZ, [_I] * 5),
+    "gdn_s6_recurrent_step": (_I, _S6_STEP_ARGS),
+    "gdn_s6_recurrent_step_f32": (_I, _S6_STEP_ARGS),
+    "gdn_rms_norm_fwd": (_I, _NORM_ARGS),
+    "gdn_rms_norm_fwd_f32": (_I, _NORM_ARGS),
+    "gdn_rms_norm_fwd_e4m3": (_I, _NORM8_ARGS),
+    "gdn_rms_norm_fwd_e4m3_f32": (_I, _NORM8_ARGS),
 }
 
 _lib = None

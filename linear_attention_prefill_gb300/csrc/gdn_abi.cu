@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include "../../include/gdn.h"
+#include "abi_common.h"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
 
@@ -83,11 +84,9 @@ cudaError_t launch_check_inputs(const FwdParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-}  // namespace gdn
-
 namespace {
-
 thread_local char t_last_error[512] = "";
+}  // namespace
 
 gdn_status fail(gdn_status s, const char* fmt, ...) {
   va_list ap;
@@ -101,7 +100,15 @@ gdn_status cuda_fail(cudaError_t e, const char* what) {
   return fail(GDN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+const char* last_error() { return t_last_error; }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::aligned;
+using gdn::cuda_fail;
+using gdn::fail;
 
 bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
@@ -670,7 +677,7 @@ const char* gdn_status_string(gdn_status s) {
   return "GDN_ERR_UNKNOWN";
 }
 
-const char* gdn_last_error(void) { return t_last_error; }
+const char* gdn_last_error(void) { return gdn::last_error(); }
 
 int gdn_abi_version(void) { return 2; }
 

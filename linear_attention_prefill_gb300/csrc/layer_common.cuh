@@ -1,0 +1,181 @@
+// layer_common.cuh - device helpers of the layer operators around the forwards (short
+// convolution, S6 scan, RMS norm): 8-element rows of bf16 or fp32, packed fp32 pairs,
+// and the activations in fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---- element types ---------------------------------------------------------------
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Eight consecutive elements as they are stored: 16 bytes of bf16, 32 of fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(w[i] << 16);
+      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&o)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(o[2 * i + 1]), "f"(o[2 * i]));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = *reinterpret_cast<const uint4*>(p);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  // element by element, the first n of 8 (n <= 0: none); the others read as zero
+  __device__ __forceinline__ void load_n(const __nv_bfloat16* p, int n) {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = 2 * i < n ? q[2 * i] : 0u, hi = 2 * i + 1 < n ? q[2 * i + 1] : 0u;
+      w[i] = lo | (hi << 16);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store_n(__nv_bfloat16* p, int n) const {
+    uint16_t* q = reinterpret_cast<uint16_t*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) q[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+  }
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+    o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&o)[8]) {
+    a = make_float4(o[0], o[1], o[2], o[3]);
+    b = make_float4(o[4], o[5], o[6], o[7]);
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void load_n(const float* p, int n) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = i < n ? p[i] : 0.f;
+    set(o);
+  }
+  __device__ __forceinline__ void store_n(float* p, int n) const {
+    float o[8];
+    get(o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = o[i];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+};
+// The first n of 8 elements at p, by one wide access where the caller's `vec` says that p
+// is 16-byte aligned and n >= 8.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int n, bool vec) {
+  Raw8<T> r;
+  if (vec) r.load(p); else r.load_n(p, n);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int n, bool vec) {
+  if (vec) r.store(p); else r.store_n(p, n);
+}
+
+// ---- fp32 arithmetic ---------------------------------------------------------------
+__device__ __forceinline__ float ex2(float x) {  // 2^x: max 1.4e-7 relative, subnormals flushed
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// x sigmoid(x) = x / (1 + 2^(-x log2 e)); x -> -inf gives -inf * 0 = NaN as the quotient does
+__device__ __forceinline__ float silu(float x) { return x * rcp(1.f + ex2(-kLog2e * x)); }
+
+// Two fp32 values in one 64-bit register, the operand of the packed fp32 instructions.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 dup2(float x) { return pack2(x, x); }
+
+// softplus(x) = max(x, 0) + log1p(u), u = exp(-|x|) in (0, 1], of two values at once.
+// log1p(u) = 2 atanh(s) with s = u / (2 + u) <= 1/3, by the odd series of atanh up to
+// s^13: the first term left out is below s^15 / 7.5 = 1e-8 of the sum, and a small u keeps
+// its relative accuracy, which log(1 + u) does not.
+__device__ __forceinline__ f32x2 softplus2(f32x2 x) {
+  float x0, x1, u0, u1, d0, d1;
+  unpack2(x, x0, x1);
+  u0 = ex2(-kLog2e * fabsf(x0));
+  u1 = ex2(-kLog2e * fabsf(x1));
+  const f32x2 u = pack2(u0, u1);
+  unpack2(add2(u, dup2(2.f)), d0, d1);
+  const f32x2 s = mul2(u, pack2(rcp(d0), rcp(d1)));
+  const f32x2 q = mul2(s, s);
+  f32x2 r = dup2(2.f / 13.f);
+  r = fma2(r, q, dup2(2.f / 11.f));
+  r = fma2(r, q, dup2(2.f / 9.f));
+  r = fma2(r, q, dup2(2.f / 7.f));
+  r = fma2(r, q, dup2(2.f / 5.f));
+  r = fma2(r, q, dup2(2.f / 3.f));
+  r = fma2(r, q, dup2(2.f));
+  return fma2(r, s, pack2(fmaxf(x0, 0.f), fmaxf(x1, 0.f)));
+}
+__device__ __forceinline__ float softplus(float x) {
+  float lo, hi;
+  unpack2(softplus2(dup2(x)), lo, hi);
+  return lo;
+}
+
+}  // namespace gdn

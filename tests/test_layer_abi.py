@@ -1,0 +1,147 @@
+"""The layer operators' C entry points on the CPU: bad arguments are rejected before any
+CUDA call, calls without work return GDN_OK, and the workspace size follows its layout."""
+import pytest
+
+A = 0x10000          # aligned fake addresses, far apart: never dereferenced
+STEP = 0x100000000
+
+
+def at(i, off=0):
+    return A + i * STEP + off
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from linear_attention_prefill_gb300 import _build, binding
+    _build.build()
+    return binding.load_library()
+
+
+def conv(lib, x=at(0), w=at(1), bias=None, s0=None, y=at(2), sT=None, N=1, T=8, D=16, W=4, stride=16,
+         act=1, cu=None, f32=False):
+    fn = lib.gdn_short_conv_fwd_f32 if f32 else lib.gdn_short_conv_fwd
+    return fn(x, w, bias, s0, y, sT, N, T, D, W, stride, act, cu, None)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("case,status", [
+    (dict(x=None), 1), (dict(w=None), 1), (dict(y=None), 1), (dict(N=-1), 1), (dict(T=-1), 1),
+    (dict(D=0), 1), (dict(W=1), 2), (dict(W=5), 2), (dict(act=2), 1), (dict(stride=15), 1),
+    (dict(x=at(0, 1)), 1), (dict(w=at(1, 4)), 1), (dict(bias=at(3, 2)), 1), (dict(s0=at(3, 1)), 1),
+    (dict(sT=at(3, 1)), 1), (dict(cu=at(4, 2)), 1), (dict(cu=at(4), N=0), 1),
+    (dict(y=at(0)), 1), (dict(y=at(0, 128)), 1), (dict(s0=at(3), sT=at(3, 16)), 1),
+    (dict(sT=at(0, 64)), 1), (dict(sT=at(2)), 1), (dict(s0=at(2)), 1),
+    (dict(N=1 << 30, T=1 << 30), 1),
+])
+def test_conv_rejects(lib, case, status, f32):
+    assert conv(lib, f32=f32, **case) == status
+    assert lib.gdn_last_error() != b""
+
+
+def test_conv_without_work(lib):
+    assert conv(lib, N=0, T=0, x=None, y=None, w=None) == 0
+    assert conv(lib, N=3, T=0, x=None, y=None, w=None) == 0
+
+
+@pytest.mark.parametrize("case,status", [
+    (dict(x=None), 1), (dict(s=None), 1), (dict(y=None), 1), (dict(N=-1), 1), (dict(W=6), 2),
+    (dict(stride=4), 1), (dict(y=at(3)), 1), (dict(act=-1), 1),
+])
+def test_conv_step_rejects(lib, case, status):
+    a = dict(x=at(0), w=at(1), s=at(3), y=at(2), N=2, D=16, W=4, stride=16, act=1)
+    a.update(case)
+    for fn in (lib.gdn_short_conv_step, lib.gdn_short_conv_step_f32):
+        assert fn(a["x"], a["w"], None, a["s"], a["y"], a["N"], a["D"], a["W"], a["stride"], a["act"],
+                  None) == status
+    assert lib.gdn_short_conv_step(None, None, None, None, None, 0, 16, 4, 16, 1, None) == 0
+
+
+S6 = dict(x=at(0), dt=at(1), A=at(2), B=at(3), C=at(4), D=at(5), z=at(6), bias=at(7), h0=at(8), y=at(9),
+          hT=at(10), N=1, T=8, dim=32, Ns=16, xs=32, ds=32, bs=16, cs=16, zs=32, cu=None, ws=None, nws=0)
+
+
+def s6(lib, f32=False, **kw):
+    a = dict(S6, **kw)
+    fn = lib.gdn_s6_chunk_fwd_f32 if f32 else lib.gdn_s6_chunk_fwd
+    return fn(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], a["z"], a["bias"], a["h0"], a["y"], a["hT"],
+              a["N"], a["T"], a["dim"], a["Ns"], a["xs"], a["ds"], a["bs"], a["cs"], a["zs"], 1, a["cu"],
+              a["ws"], a["nws"], None)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("case,status", [
+    (dict(x=None), 1), (dict(dt=None), 1), (dict(A=None), 1), (dict(B=None), 1), (dict(C=None), 1),
+    (dict(y=None), 1), (dict(N=-1), 1), (dict(T=-1), 1), (dict(dim=0), 1), (dict(Ns=0), 1), (dict(Ns=65), 2),
+    (dict(xs=31), 1), (dict(ds=1), 1), (dict(bs=15), 1), (dict(cs=0), 1), (dict(zs=-32), 1),
+    (dict(x=at(0, 1)), 1), (dict(A=at(2, 8)), 1), (dict(h0=at(8, 4)), 1), (dict(hT=at(10, 8)), 1),
+    (dict(D=at(5, 2)), 1), (dict(bias=at(7, 1)), 1), (dict(cu=at(11, 1)), 1), (dict(cu=at(11), N=0), 1),
+    (dict(y=at(0)), 1), (dict(y=at(1, 64)), 1), (dict(y=at(8)), 1), (dict(hT=at(9)), 1), (dict(hT=at(2)), 1),
+    (dict(hT=at(8, 16)), 1),
+    (dict(T=4096, ws=at(12), nws=16), 1), (dict(T=4096, ws=at(12, 16), nws=1 << 40), 1),
+])
+def test_s6_rejects(lib, case, status, f32):
+    assert s6(lib, f32=f32, **case) == status
+    assert lib.gdn_last_error() != b""
+
+
+def test_s6_without_work(lib):
+    assert s6(lib, N=0, T=0) == 0
+    assert s6(lib, N=2, T=0, hT=None, h0=None) == 0
+
+
+@pytest.mark.parametrize("case,status", [(dict(h=None), 1), (dict(x=None), 1), (dict(Ns=100), 2),
+                                         (dict(h=at(8, 4)), 1), (dict(y=at(8)), 1), (dict(N=-2), 1)])
+def test_s6_step_rejects(lib, case, status):
+    a = dict(S6, h=at(8), N=2)
+    a.update(case)
+    for fn in (lib.gdn_s6_recurrent_step, lib.gdn_s6_recurrent_step_f32):
+        assert fn(a["x"], a["dt"], a["A"], a["B"], a["C"], a["D"], a["z"], a["bias"], a["h"], a["y"], a["N"],
+                  a["dim"], a["Ns"], a["xs"], a["ds"], a["bs"], a["cs"], a["zs"], 1, None) == status
+
+
+def test_s6_workspace_size(lib):
+    size = lib.gdn_s6_chunk_fwd_workspace_size
+    assert size(1, 4096, 5120, 16, 0) == 0 and size(64, 64, 64, 16, 0) == 0  # whole sequences
+    for N, T, dim, Ns, packed in ((1, 65536, 2048, 16, 0), (2, 3000, 33, 7, 0), (3, 9001, 100, 16, 1)):
+        got = size(N, T, dim, Ns, packed)
+        # slots x (steps' sum, states) and a copy of the states, each piece 256-byte aligned
+        up = lambda v: -(-v // 64) * 64  # noqa: E731
+        assert got % 4 == 0 and any(
+            got == 4 * (up(s * dim) + up(s * dim * Ns) + N * dim * Ns) for s in range(N, 32 * N + N + 2))
+    assert size(-1, 64, 64, 16, 0) == 0 and size(1, 4096, 64, 65, 0) == 0
+
+
+NORM = dict(x=at(0), w=at(1), res=None, gate=None, y=at(2), out=None, scales=at(3), tokens=4, heads=1, D=64,
+            xs=64, gs=64, group=32, eps=1e-6)
+
+
+def norm(lib, fp8=False, f32=False, **kw):
+    a = dict(NORM, **kw)
+    head = (a["x"], a["w"], a["res"], a["gate"], a["y"])
+    size = (a["tokens"], a["heads"], a["D"], a["xs"], a["gs"])
+    if fp8:
+        fn = lib.gdn_rms_norm_fwd_e4m3_f32 if f32 else lib.gdn_rms_norm_fwd_e4m3
+        return fn(*head, a["scales"], a["out"], *size, a["group"], a["eps"], None)
+    fn = lib.gdn_rms_norm_fwd_f32 if f32 else lib.gdn_rms_norm_fwd
+    return fn(*head, a["out"], *size, a["eps"], None)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("case,status", [
+    (dict(x=None), 1), (dict(w=None), 1), (dict(y=None), 1), (dict(tokens=-1), 1), (dict(heads=0), 1),
+    (dict(D=0), 1), (dict(D=32769, xs=32769), 2), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(xs=63), 1), (dict(gate=at(5), gs=10), 1), (dict(res=at(4)), 1), (dict(out=at(4)), 1),
+    (dict(x=at(0, 1)), 1), (dict(w=at(1, 2)), 1), (dict(res=at(4, 1), out=at(5)), 1),
+    (dict(y=at(0)), 1), (dict(res=at(4), out=at(4, 32)), 1), (dict(res=at(4), out=at(0)), 1),
+    (dict(res=at(2), out=at(2)), 1), (dict(tokens=1 << 40), 1), (dict(heads=1 << 20, D=32768), 1),
+])
+def test_norm_rejects(lib, case, status, fp8, f32):
+    assert norm(lib, fp8, f32, **case) == status
+    assert lib.gdn_last_error() != b""
+
+
+def test_norm_e4m3_rejects(lib):
+    assert norm(lib, True, scales=None) == 1 and norm(lib, True, group=48) == 2
+    assert norm(lib, True, scales=at(2)) == 1 and norm(lib, True, scales=at(3, 2)) == 1
+    assert norm(lib, True, tokens=0) == 0 and norm(lib, tokens=0, x=None, w=None, y=None) == 0
