@@ -155,13 +155,14 @@ gdn_status check_s6(const void* x, const void* dt, const float* A, const void* B
   p->N = N; p->T = T; p->dim = dim; p->Ns = Ns;
   p->softplus = dt_softplus != 0;
   const bool one = tokens <= 1;
-  const int pair = 2 * elem, four = 4 * elem;
-  p->vec2 = dim % 2 == 0 && aligned(x, pair) && aligned(dt, pair) && aligned(z, pair) &&
-            aligned(y, pair) && (one || (x_stride % 2 == 0 && dt_stride % 2 == 0)) &&
-            (one || !z || z_stride % 2 == 0);
+  const int pair = 2 * elem, four = 4 * elem, piece = 16 / elem;
+  p->vec = dim % piece == 0 && aligned(x, 16) && aligned(dt, 16) && aligned(z, 16) &&
+           (one || (x_stride % piece == 0 && dt_stride % piece == 0)) &&
+           (one || !z || z_stride % piece == 0);
+  p->vec2 = dim % 2 == 0 && aligned(y, pair);
   p->vec_bc = Ns % 4 == 0 && aligned(B, four) && aligned(C, four) &&
               (one || (b_stride % 4 == 0 && c_stride % 4 == 0));
-  p->chunk = 0; p->slots = 0;
+  p->whole = 0; p->chunk = 0; p->slots = 0;
   p->ws_sum = nullptr; p->ws_h = nullptr; p->ws_h0 = nullptr;
   return GDN_OK;
 }
@@ -170,13 +171,14 @@ gdn_status run_s6(gdn::S6Params p, bool f32, void* ws, size_t ws_bytes, gdn_stre
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const long long tokens = p.cu ? (long long)p.T : (long long)p.N * p.T;
   if (p.N == 0 || (tokens == 0 && !p.hT)) return GDN_OK;
-  const bool packed = p.cu != nullptr;
-  p.chunk = gdn::s6_chunk(p.N, p.T, p.dim, p.Ns, packed);
-  const long long slots = gdn::s6_slots(p.N, p.T, p.chunk, packed);
-  if (slots * ((p.dim + 31) / 32) > kMaxGrid)
+  const gdn::S6Split split = gdn::s6_split(p.N, p.T, p.dim, p.Ns, p.cu != nullptr);
+  const long long tiles = (p.dim + 31) / 32;
+  if ((split.slots + p.N) * tiles > kMaxGrid)
     return fail(GDN_ERR_INVALID_ARG, "problem too large: N=%d T=%d D=%d", p.N, p.T, p.dim);
-  p.slots = (int)slots;
-  const size_t need = gdn::s6_ws_bytes(p.N, p.T, p.dim, p.Ns, packed);
+  p.whole = split.whole;
+  p.chunk = split.chunk;
+  p.slots = (int)split.slots;
+  const size_t need = split.ws_bytes;
   void* pool = nullptr;
   if (need) {
     if (ws) {
@@ -188,11 +190,9 @@ gdn_status run_s6(gdn::S6Params p, bool f32, void* ws, size_t ws_bytes, gdn_stre
       if (e != cudaSuccess) return cuda_fail(e, "allocating the workspace");
       ws = pool;
     }
-    const size_t up = 63;
     p.ws_sum = static_cast<float*>(ws);
-    p.ws_h = p.ws_sum + (((size_t)slots * p.dim + up) & ~up);
-    if (p.h0 && p.h0 == p.hT)
-      p.ws_h0 = p.ws_h + (((size_t)slots * p.dim * p.Ns + up) & ~up);
+    p.ws_h = p.ws_sum + split.sum_floats;
+    if (p.h0 && p.h0 == p.hT) p.ws_h0 = p.ws_h + split.h_floats;
   }
   const cudaError_t e = gdn::launch_s6(p, f32, st);
   const cudaError_t ef = pool ? cudaFreeAsync(pool, st) : cudaSuccess;
@@ -306,7 +306,7 @@ gdn_status gdn_short_conv_step_f32(const float* x, const float* w, const float* 
 
 size_t gdn_s6_chunk_fwd_workspace_size(int N, int T, int dim, int Ns, int has_cu_seqlens) {
   if (N < 0 || T < 0 || dim <= 0 || Ns < 1 || Ns > 64 || (has_cu_seqlens && N < 1)) return 0;
-  return gdn::s6_ws_bytes(N, T, dim, Ns, has_cu_seqlens != 0);
+  return gdn::s6_split(N, T, dim, Ns, has_cu_seqlens != 0).ws_bytes;
 }
 
 gdn_status gdn_s6_chunk_fwd(const void* x, const void* dt, const float* A, const void* B,

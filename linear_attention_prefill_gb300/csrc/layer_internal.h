@@ -37,21 +37,25 @@ struct S6Params {
   long long x_stride, dt_stride, b_stride, c_stride, z_stride;  // elements from token to token
   int N, T, dim, Ns;
   int softplus;
-  int vec2;                         // channel pairs of x, dt, z, y are aligned, dim is even
+  int vec;                          // 8-channel (fp32: 4) pieces of x, dt, z are 16-byte aligned
+  int vec2;                         // channel pairs of y are aligned, dim is even
   int vec_bc;                       // four states of B and of C are aligned, Ns % 4 == 0
-  // the split over time: chunks of `chunk` tokens (a multiple of 32) per sequence, their
-  // summaries in the workspace; chunk = 0: whole sequences
-  int chunk;
-  int slots;                        // chunk slots (chunk > 0)
-  float* ws_sum;                    // [slots, dim]: the chunk's sum of steps
-  float* ws_h;                      // [slots, dim, Ns]: the state after it, from zero (first: from h0)
-  float* ws_h0;                     // [N, dim, Ns]: h0 kept for the scan when hT == h0, else nullptr
+  // the split over time (s6_split): channels from 32 * whole on run in chunks of `chunk`
+  // tokens per sequence, with summaries in the workspace; chunk = 0: no channel does
+  int whole, chunk, slots;
+  float* ws_sum;                    // [slots, split channels]: the chunk's sum of steps
+  float* ws_h;                      // [slots, split channels, Ns]: the state after it, from zero
+                                    // (a first chunk: from h0)
+  float* ws_h0;                     // [N, split channels, Ns]: h0 kept where hT == h0, else nullptr
 };
-// Chunk length the scan takes for these sizes (0: no split), and the slots it has then.
-int s6_chunk(int N, int T, int dim, int Ns, bool packed);
-long long s6_slots(int N, int T, int chunk, bool packed);
-// Workspace bytes of that split, the copy of h0 included; 0 without one.
-size_t s6_ws_bytes(int N, int T, int dim, int Ns, bool packed);
+// How the scan runs for these sizes: 32-channel tiles that walk whole sequences, and the
+// chunks, slots and workspace (256-byte aligned pieces) of the others; chunk = 0 without.
+struct S6Split {
+  int whole, chunk;
+  long long slots;
+  size_t sum_floats, h_floats, ws_bytes;
+};
+S6Split s6_split(int N, int T, int dim, int Ns, bool packed);
 cudaError_t launch_s6(const S6Params& p, bool f32, cudaStream_t stream);
 cudaError_t launch_s6_step(const S6Params& p, bool f32, cudaStream_t stream);
 
