@@ -12,45 +12,90 @@ from typing import Optional
 
 import torch
 
-from .binding import _check, _need, _ptr, _stream_handle, load_library
+from .binding import _check, _need, load_library
 
-_ACT = {None: 0, "silu": 1}
-_SUFFIX = {torch.bfloat16: "", torch.float32: "_f32"}
-_E4M3 = torch.float8_e4m3fn
+# A decode step takes a few microseconds on the GPU, and so do its checks here: they are
+# written for the call that passes, one expression a tensor, with the reasons in _refuse.
+_Tensor = torch.Tensor
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+_FN = {}  # (C name, type of the rows) -> library function
 
 
-def _call(name: str, dev: torch.device, stream, *args):
-    """One library call with ``dev`` as the current device, on ``stream`` or dev's current one."""
-    fn = getattr(load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, _stream_handle(stream, dev)))
+def _function(name: str, dtype):
+    fn = _FN[name, dtype] = getattr(load_library(), name + ("_f32" if dtype is _F32 else ""))
+    return fn
+
+
+def _call(name: str, dtype, index: int, stream, args):
+    """One library call with device ``index`` current, on ``stream`` or its current one."""
+    fn = _FN.get((name, dtype)) or _function(name, dtype)
+    if stream is None:
+        handle = _current_stream(index)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, _stream_handle(stream, dev)))
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if _current_device() == index:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
+    if status:
+        _check(status)
 
 
-def _kind(x, name: str) -> str:
-    """The C name's suffix for x's type; x must live on a GPU."""
-    if not isinstance(x, torch.Tensor):
+def _kind(x, name: str, dims: int):
+    """(type, device index) of the operand that sets them: bf16 or fp32, on a GPU."""
+    if not isinstance(x, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
+    dtype, index = x.dtype, x.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a CUDA device")
-    try:
-        return _SUFFIX[x.dtype]
-    except KeyError:
-        raise TypeError(f"{name} must be bf16 or fp32, got {x.dtype}") from None
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"{name} must be bf16 or fp32, got {dtype}")
+    if x.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(x.shape)}")
+    return dtype, index
 
 
-def _typed(t, name: str, dtype, device, shape):
-    """Checks type, device and shape of an operand that need not be contiguous."""
-    if not isinstance(t, torch.Tensor):
+def _refuse(t, name: str, dtype, index: int, shape, dense: bool = True):
+    """Raises what is wrong with ``t``."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous" if dense else
+                     f"{name} with strides {t.stride()}: the last dimension must be dense and tokens "
+                     "a constant stride apart")
+
+
+def _dense(t, name: str, dtype, index: int, shape) -> int:
+    """Address of a contiguous operand of that type, device and shape."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape and t.is_contiguous()):
+        _refuse(t, name, dtype, index, shape)
+    return t.data_ptr()
+
+
+def _maybe(t, name: str, dtype, index: int, shape):
+    return None if t is None else _dense(t, name, dtype, index, shape)
+
+
+def _rows(t, name: str, dtype, index: int, shape):
+    """(address, elements from token to token) of a row operand [..., cols]."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape):
+        _refuse(t, name, dtype, index, shape)
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    stride = _stride_of(t)
+    if stride is None:
+        _refuse(t, name, dtype, index, shape, dense=False)
+    return t.data_ptr(), stride
 
 
 def _stride_of(t, inner: int = 1):
@@ -75,38 +120,33 @@ def _stride_of(t, inner: int = 1):
     return stride if stride >= cols or seen <= 1 else None
 
 
-def _rows(t, name: str, dtype, device, shape) -> int:
-    """Checks a row operand [..., cols] and returns its elements from token to token."""
-    _typed(t, name, dtype, device, shape)
-    stride = _stride_of(t)
-    if stride is None:
-        raise ValueError(f"{name} with strides {t.stride()}: the last dimension must be dense and "
-                         "tokens a constant stride apart")
-    return stride
-
-
-def _param(t, name: str, device, shape):
-    if t is not None:
-        _need(t, name, torch.float32, device, shape)
-
-
-def _sequences(lead, cu_seqlens, device):
-    """(N, T) of a batch whose tensors have the leading dimensions ``lead`` = (B, T)."""
+def _sequences(shape, cu_seqlens, device):
+    """(N, T, address of cu_seqlens) of a batch of shape [B, T, ...]."""
     if cu_seqlens is None:
-        return lead
+        return shape[0], shape[1], None
     _need(cu_seqlens, "cu_seqlens", torch.int32, device)
-    if lead[0] != 1:
+    if shape[0] != 1:
         raise ValueError("with cu_seqlens the batch must be one packed row (B == 1)")
-    if cu_seqlens.numel() < 2:
+    n = cu_seqlens.numel() - 1
+    if n < 1:
         raise ValueError("cu_seqlens needs at least one sequence")
-    return cu_seqlens.numel() - 1, lead[1]
+    return n, shape[1], cu_seqlens.data_ptr()
 
 
 def _act(activation) -> int:
-    try:
-        return _ACT[activation]
-    except (KeyError, TypeError):
-        raise ValueError(f"activation must be 'silu' or None, got {activation!r}") from None
+    if activation == "silu":
+        return 1
+    if activation is None:
+        return 0
+    raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
+
+
+def _taps(weight, index: int, D: int):
+    """(address, W) of the filters [D, W]."""
+    if not isinstance(weight, _Tensor) or weight.dim() != 2:
+        raise (ValueError if isinstance(weight, _Tensor) else TypeError)("weight must be a tensor [D, W]")
+    W = weight.shape[1]
+    return _dense(weight, "weight", _F32, index, (D, W)), W
 
 
 def gdn_short_conv_fwd(x, weight, bias=None, s0=None, y=None, sT=None, *,
@@ -121,27 +161,21 @@ def gdn_short_conv_fwd(x, weight, bias=None, s0=None, y=None, sT=None, *,
     packed row, B = 1; rows behind cu_seqlens[N] are left as they were.  sT [N, W-1, D] may
     be s0 (in place).
     """
-    suffix = _kind(x, "x")
-    if x.dim() != 3 or weight.dim() != 2:
-        raise ValueError("x must be [B, T, D] and weight [D, W]")
-    dev, dt, D, W = x.device, x.dtype, x.shape[2], weight.shape[1]
-    N, T = _sequences(x.shape[:2], cu_seqlens, dev)
-    stride = _rows(x, "x", dt, dev, x.shape)
-    _param(weight, "weight", dev, (D, W))
-    _param(bias, "bias", dev, (D,))
+    dtype, index = _kind(x, "x", 3)
+    shape = x.shape
+    D = shape[2]
+    w, W = _taps(weight, index, D)
+    N, T, cu = _sequences(shape, cu_seqlens, x.device)
+    xp, stride = _rows(x, "x", dtype, index, shape)
     states = (N, W - 1, D)
-    if s0 is not None:
-        _need(s0, "s0", dt, dev, states)
     if y is None:
-        y = torch.empty(x.shape, dtype=dt, device=dev)
-    else:
-        _need(y, "y", dt, dev, x.shape)
-    if sT is not None:
-        _need(sT, "sT", dt, dev, states)
-    elif output_final_state and W > 1:
-        sT = torch.empty(states, dtype=dt, device=dev)
-    _call("gdn_short_conv_fwd" + suffix, dev, stream, _ptr(x), _ptr(weight), _ptr(bias), _ptr(s0),
-          _ptr(y), _ptr(sT), N, T, D, W, stride, _act(activation), _ptr(cu_seqlens))
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    if sT is None and output_final_state and W > 1:
+        sT = torch.empty(states, dtype=dtype, device=x.device)
+    _call("gdn_short_conv_fwd", dtype, index, stream,
+          (xp, w, _maybe(bias, "bias", _F32, index, (D,)), _maybe(s0, "s0", dtype, index, states),
+           _dense(y, "y", dtype, index, shape), _maybe(sT, "sT", dtype, index, states), N, T, D, W,
+           stride, _act(activation), cu))
     return y, sT
 
 
@@ -152,22 +186,17 @@ def gdn_short_conv_step(x, weight, s, bias=None, y=None, *, activation: Optional
     x [N, D] (may be a slice of a wider projection); weight, bias and activation as in
     gdn_short_conv_fwd.
     """
-    suffix = _kind(x, "x")
-    if x.dim() != 2 or weight.dim() != 2:
-        raise ValueError("x must be [N, D] and weight [D, W]")
-    dev, dt = x.device, x.dtype
-    N, D = x.shape
-    W = weight.shape[1]
-    stride = _rows(x, "x", dt, dev, x.shape)
-    _param(weight, "weight", dev, (D, W))
-    _param(bias, "bias", dev, (D,))
-    _need(s, "s", dt, dev, (N, W - 1, D))
+    dtype, index = _kind(x, "x", 2)
+    shape = x.shape
+    N, D = shape
+    w, W = _taps(weight, index, D)
+    xp, stride = _rows(x, "x", dtype, index, shape)
+    sp = _dense(s, "s", dtype, index, (N, W - 1, D))
     if y is None:
-        y = torch.empty((N, D), dtype=dt, device=dev)
-    else:
-        _need(y, "y", dt, dev, (N, D))
-    _call("gdn_short_conv_step" + suffix, dev, stream, _ptr(x), _ptr(weight), _ptr(bias), _ptr(s),
-          _ptr(y), N, D, W, stride, _act(activation))
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    _call("gdn_short_conv_step", dtype, index, stream,
+          (xp, w, _maybe(bias, "bias", _F32, index, (D,)), sp, _dense(y, "y", dtype, index, shape),
+           N, D, W, stride, _act(activation)))
     return y
 
 
@@ -176,23 +205,24 @@ def gdn_s6_chunk_fwd_workspace_size(N, T, dim, Ns, varlen=False) -> int:
     return int(load_library().gdn_s6_chunk_fwd_workspace_size(N, T, dim, Ns, int(bool(varlen))))
 
 
-def _s6_rows(x, dt, A, B, C, D, z, dt_bias):
-    """Checks what the scan and its step share; returns (suffix, dim, Ns, strides)."""
-    suffix = _kind(x, "x")
-    if A.dim() != 2:
-        raise ValueError("A must be [D, Ns]")
-    dev, ty = x.device, x.dtype
-    dim, Ns = x.shape[-1], A.shape[1]
-    lead = tuple(x.shape[:-1])
-    xs = _rows(x, "x", ty, dev, x.shape)
-    ds = _rows(dt, "dt", ty, dev, x.shape)
-    bs = _rows(B, "B", ty, dev, lead + (Ns,))
-    cs = _rows(C, "C", ty, dev, lead + (Ns,))
-    zs = 0 if z is None else _rows(z, "z", ty, dev, x.shape)
-    _param(A, "A", dev, (dim, Ns))
-    _param(D, "D", dev, (dim,))
-    _param(dt_bias, "dt_bias", dev, (dim,))
-    return suffix, dim, Ns, (xs, ds, bs, cs, zs)
+def _s6_rows(x, dt, A, B, C, D, z, dt_bias, dims: int):
+    """Checks what the scan and its step share; returns (type, device, dim, Ns, addresses
+    x, dt, A, B, C, D, z, dt_bias, strides x, dt, B, C, z)."""
+    dtype, index = _kind(x, "x", dims)
+    shape = x.shape
+    dim = shape[-1]
+    if not isinstance(A, _Tensor) or A.dim() != 2:
+        raise (ValueError if isinstance(A, _Tensor) else TypeError)("A must be a tensor [D, Ns]")
+    Ns = A.shape[1]
+    states = shape[:-1] + (Ns,)
+    xp, xs = _rows(x, "x", dtype, index, shape)
+    dp, ds = _rows(dt, "dt", dtype, index, shape)
+    bp, bs = _rows(B, "B", dtype, index, states)
+    cp, cs = _rows(C, "C", dtype, index, states)
+    zp, zs = (None, 0) if z is None else _rows(z, "z", dtype, index, shape)
+    return dtype, index, dim, Ns, (
+        xp, dp, _dense(A, "A", _F32, index, (dim, Ns)), bp, cp, _maybe(D, "D", _F32, index, (dim,)), zp,
+        _maybe(dt_bias, "dt_bias", _F32, index, (dim,))), (xs, ds, bs, cs, zs)
 
 
 def gdn_s6_chunk_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, y=None, hT=None, *,
@@ -209,31 +239,24 @@ def gdn_s6_chunk_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, y=No
     place).  ``workspace``: a uint8 device tensor of at least
     gdn_s6_chunk_fwd_workspace_size bytes, or None for a fresh one where the sizes need one.
     """
-    if x.dim() != 3:
-        raise ValueError("x must be [B, T, D]")
-    suffix, dim, Ns, strides = _s6_rows(x, dt, A, B, C, D, z, dt_bias)
-    dev = x.device
-    N, T = _sequences(x.shape[:2], cu_seqlens, dev)
+    dtype, index, dim, Ns, ptrs, strides = _s6_rows(x, dt, A, B, C, D, z, dt_bias, 3)
+    N, T, cu = _sequences(x.shape, cu_seqlens, x.device)
     states = (N, dim, Ns)
-    _param(h0, "h0", dev, states)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    else:
-        _need(y, "y", x.dtype, dev, x.shape)
-    if hT is not None:
-        _need(hT, "hT", torch.float32, dev, states)
-    elif output_final_state:
-        hT = torch.empty(states, dtype=torch.float32, device=dev)
+        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    if hT is None and output_final_state:
+        hT = torch.empty(states, dtype=_F32, device=x.device)
     if workspace is None:
-        need = gdn_s6_chunk_fwd_workspace_size(N, T, dim, Ns, cu_seqlens is not None)
+        need = gdn_s6_chunk_fwd_workspace_size(N, T, dim, Ns, cu is not None)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     else:
-        _need(workspace, "workspace", torch.uint8, dev)
-    _call("gdn_s6_chunk_fwd" + suffix, dev, stream, _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
-          _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(y), _ptr(hT), N, T, dim, Ns, *strides,
-          int(bool(dt_softplus)), _ptr(cu_seqlens), _ptr(workspace),
-          0 if workspace is None else workspace.numel())
+        _need(workspace, "workspace", torch.uint8, x.device)
+    _call("gdn_s6_chunk_fwd", dtype, index, stream,
+          (*ptrs, _maybe(h0, "h0", _F32, index, states), _dense(y, "y", dtype, index, x.shape),
+           _maybe(hT, "hT", _F32, index, states), N, T, dim, Ns, *strides, int(bool(dt_softplus)), cu,
+           None if workspace is None else workspace.data_ptr(),
+           0 if workspace is None else workspace.numel()))
     return y, hT
 
 
@@ -243,18 +266,15 @@ def gdn_s6_recurrent_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, y=Non
 
     x, dt, z [N, D]; B, C [N, Ns]; the rest as in gdn_s6_chunk_fwd.
     """
-    if x.dim() != 2:
-        raise ValueError("x must be [N, D]")
-    suffix, dim, Ns, strides = _s6_rows(x, dt, A, B, C, D, z, dt_bias)
-    dev, N = x.device, x.shape[0]
-    _need(h, "h", torch.float32, dev, (N, dim, Ns))
+    dtype, index, dim, Ns, ptrs, strides = _s6_rows(x, dt, A, B, C, D, z, dt_bias, 2)
+    shape = x.shape
+    N = shape[0]
+    hp = _dense(h, "h", _F32, index, (N, dim, Ns))
     if y is None:
-        y = torch.empty((N, dim), dtype=x.dtype, device=dev)
-    else:
-        _need(y, "y", x.dtype, dev, (N, dim))
-    _call("gdn_s6_recurrent_step" + suffix, dev, stream, _ptr(x), _ptr(dt), _ptr(A), _ptr(B),
-          _ptr(C), _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h), _ptr(y), N, dim, Ns, *strides,
-          int(bool(dt_softplus)))
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    _call("gdn_s6_recurrent_step", dtype, index, stream,
+          (*ptrs, hp, _dense(y, "y", dtype, index, shape), N, dim, Ns, *strides,
+           int(bool(dt_softplus))))
     return y
 
 
@@ -269,60 +289,57 @@ def gdn_rms_norm_fwd(x, weight, residual=None, gate=None, y=None, residual_out=N
     scales [..., ceil(D / group)], one per ``group`` (32, 64, 128) columns or one a row (None):
     scale = max|y| / 448 (1 for zeros).  scales and residual_out are None where there are none.
     """
-    suffix = _kind(x, "x")
-    if x.dim() < 1:
-        raise ValueError("x must be [..., D]")
-    dev, dt, D = x.device, x.dtype, x.shape[-1]
-    fp8 = out_dtype == _E4M3
-    if not fp8 and out_dtype not in (None, dt):
-        raise TypeError(f"out_dtype must be {dt} or {_E4M3}, got {out_dtype}")
-    if group is not None and not fp8:
-        raise ValueError("group applies to the e4m3 output")
-    if fp8 and group not in (None, 32, 64, 128):
-        raise ValueError(f"group must be 32, 64, 128 or None, got {group!r}")
-    _param(weight, "weight", dev, (D,))
-    _typed(x, "x", dt, dev, x.shape)
-    if gate is not None:
-        _typed(gate, "gate", dt, dev, x.shape)
-    # rows a constant stride apart, or [..., H, D] whose tokens (H D dense) are
-    heads, inner = 1, 1
-    xs, gs = _stride_of(x), 0 if gate is None else _stride_of(gate)
-    if (xs is None or gs is None) and x.dim() > 1:
-        heads, inner = x.shape[-2], 2
-        xs, gs = _stride_of(x, 2), 0 if gate is None else _stride_of(gate, 2)
-    for s, t, name in ((xs, x, "x"), (gs, gate, "gate")):
-        if s is None:
-            raise ValueError(f"{name} with strides {t.stride()}: tokens must be dense and a constant "
-                             "stride apart")
-    tokens = 1
-    for n in x.shape[:-inner]:
-        tokens *= n
-    if x.numel() == 0:
-        tokens, heads = 0, 1
-    if y is None:
-        y = torch.empty(x.shape, dtype=_E4M3 if fp8 else dt, device=dev)
+    dtype, index = _kind(x, "x", x.dim() if isinstance(x, _Tensor) and x.dim() else 1)
+    shape = x.shape
+    D = shape[-1]
+    fp8 = out_dtype is _E4M3
+    if fp8:
+        if group not in (None, 32, 64, 128):
+            raise ValueError(f"group must be 32, 64, 128 or None, got {group!r}")
     else:
-        _need(y, "y", _E4M3 if fp8 else dt, dev, x.shape)
+        if out_dtype is not None and out_dtype != dtype:
+            raise TypeError(f"out_dtype must be {dtype} or {_E4M3}, got {out_dtype}")
+        if group is not None or scales is not None:
+            raise ValueError("group and scales belong to the e4m3 output")
+    wp = _dense(weight, "weight", _F32, index, (D,))
+    # rows a constant stride apart, or [..., H, D] whose tokens (H D dense) are
+    heads, xs, gs, gp = 1, D, D, None
+    strided = not x.is_contiguous()
+    if gate is not None:
+        if not (isinstance(gate, _Tensor) and gate.dtype is dtype and gate.get_device() == index
+                and gate.shape == shape):
+            _refuse(gate, "gate", dtype, index, shape)
+        gp = gate.data_ptr()
+        strided = strided or not gate.is_contiguous()
+    rows = x.numel() // D if D else 0
+    if strided and rows:
+        xs, gs = _stride_of(x), 0 if gate is None else _stride_of(gate)
+        if (xs is None or gs is None) and x.dim() > 1:
+            heads = shape[-2]
+            xs, gs = _stride_of(x, 2), 0 if gate is None else _stride_of(gate, 2)
+        if xs is None:
+            _refuse(x, "x", dtype, index, shape, dense=False)
+        if gs is None:
+            _refuse(gate, "gate", dtype, index, shape, dense=False)
+    if y is None:
+        y = torch.empty(shape, dtype=_E4M3 if fp8 else dtype, device=x.device)
+    yp = _dense(y, "y", _E4M3 if fp8 else dtype, index, shape)
+    rp = op = None
     if residual is not None:
-        _need(residual, "residual", dt, dev, x.shape)
+        rp = _dense(residual, "residual", dtype, index, shape)
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=dt, device=dev)
-        else:
-            _need(residual_out, "residual_out", dt, dev, x.shape)
+            residual_out = torch.empty(shape, dtype=dtype, device=x.device)
+        op = _dense(residual_out, "residual_out", dtype, index, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    args = (_ptr(x), _ptr(weight), _ptr(residual), _ptr(gate), _ptr(y))
     if fp8:
-        parts = x.shape[:-1] + (-(-D // group) if group else 1,)
+        parts = shape[:-1] + (-(-D // group) if group else 1,)
         if scales is None:
-            scales = torch.empty(parts, dtype=torch.float32, device=dev)
-        else:
-            _need(scales, "scales", torch.float32, dev, parts)
-        _call("gdn_rms_norm_fwd_e4m3" + suffix, dev, stream, *args, _ptr(scales),
-              _ptr(residual_out), tokens, heads, D, xs, gs, group or 0, float(eps))
+            scales = torch.empty(parts, dtype=_F32, device=x.device)
+        _call("gdn_rms_norm_fwd_e4m3", dtype, index, stream,
+              (x.data_ptr(), wp, rp, gp, yp, _dense(scales, "scales", _F32, index, parts), op,
+               rows // heads, heads, D, xs, gs, group or 0, eps))
     else:
-        if scales is not None:
-            raise ValueError("scales belong to the e4m3 output")
-        _call("gdn_rms_norm_fwd" + suffix, dev, stream, *args, _ptr(residual_out), tokens, heads, D,
-              xs, gs, float(eps))
+        _call("gdn_rms_norm_fwd", dtype, index, stream,
+              (x.data_ptr(), wp, rp, gp, yp, op, rows // heads, heads, D, xs, gs, eps))
     return y, scales, residual_out
