@@ -3,6 +3,8 @@
 //
 // Validates arguments, maps them onto launch parameters and enqueues the kernels on the
 // caller's stream.
+#include <initializer_list>
+
 #include "abi_common.h"
 #include "layer_internal.h"
 
@@ -78,15 +80,16 @@ gdn_status check_conv(const void* x, const float* w, const float* bias, const vo
   if (overlap(ry, rx) || overlap(ry, r0) || overlap(ry, rT) || overlap(rT, rx) ||
       (s0 != sT && overlap(r0, rT)))
     return fail(GDN_ERR_INVALID_ARG, "y and sT must not overlap the inputs (sT may be s0)");
-  // one block per 32 tokens and one per state, 8 channels a thread
-  if (tokens / 32 + N + 1 > kMaxGrid || D > 65535 * 1024)
+  // blocks of 4 or more tokens, one per state; 512 channels a block
+  if (tokens / 4 + N + 1 > kMaxGrid || D > 65535 * 512)
     return fail(GDN_ERR_INVALID_ARG, "problem too large: %lld tokens, D=%d", tokens, D);
   p->x = x; p->w = w; p->bias = bias; p->s0 = s0; p->y = y; p->sT = sT; p->cu = cu;
   p->x_stride = x_stride;
   p->N = N; p->T = T; p->D = D; p->W = W;
   p->silu = activation == GDN_ACT_SILU;
-  p->vec = D % 8 == 0 && (tokens <= 1 || x_stride * elem % 16 == 0) && aligned(x, 16) &&
-           aligned(y, 16) && aligned(s0, 16) && aligned(sT, 16);
+  const int four = 4 * elem;
+  p->vec = D % 4 == 0 && (tokens <= 1 || x_stride % 4 == 0) && aligned(x, four) &&
+           aligned(y, four) && aligned(s0, four) && aligned(sT, four);
   return GDN_OK;
 }
 
@@ -103,7 +106,7 @@ gdn_status conv_step(const void* x, const float* w, const float* bias, void* s, 
   gdn::ConvParams p;
   GDN_TRY(check_conv(x, w, bias, s, y, s, N, 1, D, W, x_stride, activation, nullptr, f32 ? 4 : 2, &p));
   if (N > 0 && !s) return fail(GDN_ERR_INVALID_ARG, "s must be non-NULL");
-  if ((long long)N * ((D + 7) / 8) / 64 > kMaxGrid)
+  if ((long long)N * ((D + 3) / 4) / 64 > kMaxGrid)
     return fail(GDN_ERR_INVALID_ARG, "N=%d, D=%d too large", N, D);
   if (N == 0) return GDN_OK;
   const cudaError_t e = gdn::launch_conv_step(p, f32, reinterpret_cast<cudaStream_t>(stream));
@@ -154,14 +157,22 @@ gdn_status check_s6(const void* x, const void* dt, const float* A, const void* B
   p->c_stride = c_stride; p->z_stride = z_stride;
   p->N = N; p->T = T; p->dim = dim; p->Ns = Ns;
   p->softplus = dt_softplus != 0;
+  // How wide rows can be copied: their first elements, strides and lengths decide.
   const bool one = tokens <= 1;
-  const int pair = 2 * elem, four = 4 * elem, piece = 16 / elem;
-  p->vec = dim % piece == 0 && aligned(x, 16) && aligned(dt, 16) && aligned(z, 16) &&
-           (one || (x_stride % piece == 0 && dt_stride % piece == 0)) &&
-           (one || !z || z_stride % piece == 0);
-  p->vec2 = dim % 2 == 0 && aligned(y, pair);
-  p->vec_bc = Ns % 4 == 0 && aligned(B, four) && aligned(C, four) &&
-              (one || (b_stride % 4 == 0 && c_stride % 4 == 0));
+  const auto rows_are = [&](int n, std::initializer_list<const void*> ptrs,
+                            std::initializer_list<long long> strides, int cols) {
+    bool ok = cols % n == 0;
+    for (const void* q : ptrs) ok = ok && aligned(q, n * elem);
+    for (const long long st : strides) ok = ok && (one || st % n == 0);
+    return ok;
+  };
+  const long long zst = z ? z_stride : 0;
+  p->copy = rows_are(16 / elem, {x, dt, z}, {x_stride, dt_stride, zst}, dim) ? 16
+            : rows_are(4 / elem, {x, dt, z}, {x_stride, dt_stride, zst}, dim) ? 4 : 2;
+  p->vec_bc = rows_are(4, {B, C}, {b_stride, c_stride}, Ns);
+  p->copy_bc = p->vec_bc ? 4 * elem : rows_are(4 / elem, {B, C}, {b_stride, c_stride}, Ns) ? 4 : 2;
+  p->vec2 = dim % 2 == 0 && aligned(y, 2 * elem);
+  p->lone = 0;
   p->whole = 0; p->chunk = 0; p->slots = 0;
   p->ws_sum = nullptr; p->ws_h = nullptr; p->ws_h0 = nullptr;
   return GDN_OK;
@@ -177,6 +188,7 @@ gdn_status run_s6(gdn::S6Params p, bool f32, void* ws, size_t ws_bytes, gdn_stre
     return fail(GDN_ERR_INVALID_ARG, "problem too large: N=%d T=%d D=%d", p.N, p.T, p.dim);
   p.whole = split.whole;
   p.chunk = split.chunk;
+  p.lone = split.lone;
   p.slots = (int)split.slots;
   const size_t need = split.ws_bytes;
   void* pool = nullptr;

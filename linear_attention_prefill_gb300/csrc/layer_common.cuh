@@ -96,6 +96,65 @@ struct Raw8<float> {
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
 };
+// Four consecutive elements as they are stored: 8 bytes of bf16, 16 of fp32.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int n, bool vec) {
+    if (vec) {
+      v = *reinterpret_cast<const uint2*>(p);
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+      v.x = (n > 0 ? q[0] : 0u) | (n > 1 ? (uint32_t)q[1] << 16 : 0u);
+      v.y = (n > 2 ? q[2] : 0u) | (n > 3 ? (uint32_t)q[3] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p, int n, bool vec) const {
+    if (vec) {
+      *reinterpret_cast<uint2*>(p) = v;
+    } else {
+      uint16_t* q = reinterpret_cast<uint16_t*>(p);
+      if (n > 0) q[0] = (uint16_t)v.x;
+      if (n > 1) q[1] = (uint16_t)(v.x >> 16);
+      if (n > 2) q[2] = (uint16_t)v.y;
+      if (n > 3) q[3] = (uint16_t)(v.y >> 16);
+    }
+  }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+  __device__ __forceinline__ void set(float a, float b, float c, float d) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(b), "f"(a));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(d), "f"(c));
+  }
+};
+template <>
+struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p, int n, bool vec) {
+    if (vec) v = *reinterpret_cast<const float4*>(p);
+    else v = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+  }
+  __device__ __forceinline__ void store(float* p, int n, bool vec) const {
+    if (vec) {
+      *reinterpret_cast<float4*>(p) = v;
+    } else {
+      if (n > 0) p[0] = v.x;
+      if (n > 1) p[1] = v.y;
+      if (n > 2) p[2] = v.z;
+      if (n > 3) p[3] = v.w;
+    }
+  }
+  __device__ __forceinline__ float4 get() const { return v; }
+  __device__ __forceinline__ void set(float a, float b, float c, float d) {
+    v = make_float4(a, b, c, d);
+  }
+};
 // The first n of 8 elements at p, by one wide access where the caller's `vec` says that p
 // is 16-byte aligned and n >= 8.
 template <typename T>
@@ -107,6 +166,23 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int n, bool vec) {
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int n, bool vec) {
   if (vec) r.store(p); else r.store_n(p, n);
+}
+
+// Four states of the recurrence (n of them exist): rows of Ns floats, 16-byte aligned bases.
+__device__ __forceinline__ float4 load_h(const float* p, int n, int Ns) {
+  if ((Ns & 3) == 0) return n > 0 ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f,
+                     n > 3 ? p[3] : 0.f);
+}
+__device__ __forceinline__ void store_h(float* p, float4 v, int n, int Ns) {
+  if ((Ns & 3) == 0) {
+    if (n > 0) *reinterpret_cast<float4*>(p) = v;
+    return;
+  }
+  if (n > 0) p[0] = v.x;
+  if (n > 1) p[1] = v.y;
+  if (n > 2) p[2] = v.z;
+  if (n > 3) p[3] = v.w;
 }
 
 // ---- fp32 arithmetic ---------------------------------------------------------------
@@ -149,6 +225,14 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 __device__ __forceinline__ f32x2 dup2(float x) { return pack2(x, x); }
+
+// x sigmoid(x) of two values
+__device__ __forceinline__ f32x2 silu2(f32x2 x) {
+  float e0, e1;
+  unpack2(mul2(x, dup2(-kLog2e)), e0, e1);
+  unpack2(add2(pack2(ex2(e0), ex2(e1)), dup2(1.f)), e0, e1);
+  return mul2(x, pack2(rcp(e0), rcp(e1)));
+}
 
 // softplus(x) = max(x, 0) + log1p(u), u = exp(-|x|) in (0, 1], of two values at once.
 // log1p(u) = u P(u), P the polynomial of degree 8 with the least relative error on (0, 1]

@@ -8,6 +8,8 @@
 
 namespace gdn {
 
+constexpr int kSms = 152;
+
 // Short causal convolution over tokens, one filter per channel.
 struct ConvParams {
   const void* x;      // rows of D channels, x_stride elements from token to token
@@ -20,7 +22,7 @@ struct ConvParams {
   long long x_stride;
   int N, T, D, W;
   int silu;
-  int vec;            // every 8-channel access is 16-byte aligned and D is a multiple of 8
+  int vec;            // 4-channel pieces are aligned (8 bytes of bf16, 16 of fp32), D % 4 == 0
 };
 cudaError_t launch_conv(const ConvParams& p, bool f32, cudaStream_t stream);
 // One token per sequence: s0 == sT, updated in place; T = 1, cu = nullptr.
@@ -37,9 +39,11 @@ struct S6Params {
   long long x_stride, dt_stride, b_stride, c_stride, z_stride;  // elements from token to token
   int N, T, dim, Ns;
   int softplus;
-  int vec;                          // 8-channel (fp32: 4) pieces of x, dt, z are 16-byte aligned
+  int copy;                         // x, dt, z rows: 16-byte pieces, 4-byte words or 2-byte elements
+  int copy_bc;                      // four states of B and of C: 16 (fp32) or 8 bytes, words, elements
   int vec2;                         // channel pairs of y are aligned, dim is even
   int vec_bc;                       // four states of B and of C are aligned, Ns % 4 == 0
+  int lone;                         // the variant for one CTA an SM (s6_split)
   // the split over time (s6_split): channels from 32 * whole on run in chunks of `chunk`
   // tokens per sequence, with summaries in the workspace; chunk = 0: no channel does
   int whole, chunk, slots;
@@ -51,7 +55,7 @@ struct S6Params {
 // How the scan runs for these sizes: 32-channel tiles that walk whole sequences, and the
 // chunks, slots and workspace (256-byte aligned pieces) of the others; chunk = 0 without.
 struct S6Split {
-  int whole, chunk;
+  int whole, chunk, lone;
   long long slots;
   size_t sum_floats, h_floats, ws_bytes;
 };

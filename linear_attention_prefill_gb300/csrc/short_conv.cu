@@ -7,37 +7,75 @@
 // where the W - 1 inputs before the sequence come from its state s0 (zeros without one) and
 // the last W - 1 inputs become the state sT.  Sums in fp32, one rounding at the end.
 //
-// HBM bandwidth bounds it: 2 bytes in and 2 out per element against ~12 instructions.  A
-// thread keeps 8 channels (one 16-byte access) and walks a run of tokens with the window in
-// registers, so that each input is loaded once except for the W - 1 rows before a run.
+// HBM bandwidth bounds it: 2 bytes in and 2 out per element against ~8 instructions.  A
+// thread has 4 channels (8 bytes of bf16) and walks a run of tokens with the window in
+// registers as packed fp32 pairs, so that each input is loaded once except for the W - 1 rows
+// before a run; four tokens are loaded while the four before them are computed.
 #include "layer_common.cuh"
 #include "layer_internal.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kVec = 8;       // channels per thread
+constexpr int kVec = 4;       // channels per thread
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;    // tokens whose loads are in flight together
+constexpr int kAhead = 4;     // tokens whose loads are in flight together
 
-// The filters of channels c..c+7: w is [D, W] and c a multiple of 8, so the 8 W floats are
-// whole 16-byte pieces.
+// Four channels of a row in fp32.
+struct Four {
+  f32x2 lo, hi;
+};
+template <typename T>
+__device__ __forceinline__ Four four(const Raw4<T>& r) {
+  const float4 v = r.get();
+  return {pack2(v.x, v.y), pack2(v.z, v.w)};
+}
+
+// The filters of channels c..c+3, tap by tap: w is [D, W] and c a multiple of 4, so the 4 W
+// floats are whole 16-byte pieces.
 template <int W>
-__device__ __forceinline__ void load_filter(const float* w, int c, int n, float (&f)[kVec][W]) {
+__device__ __forceinline__ void load_filter(const float* w, int c, int n, Four (&f)[W]) {
+  float v[kVec * W];
   if (n >= kVec) {
     const float4* p = reinterpret_cast<const float4*>(w + (long long)c * W);
-    float* o = &f[0][0];
 #pragma unroll
-    for (int i = 0; i < kVec * W / 4; ++i) {
-      const float4 v = p[i];
-      o[4 * i] = v.x, o[4 * i + 1] = v.y, o[4 * i + 2] = v.z, o[4 * i + 3] = v.w;
+    for (int i = 0; i < W; ++i) {
+      const float4 q = p[i];
+      v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-#pragma unroll
-      for (int j = 0; j < W; ++j) f[i][j] = i < n ? w[(long long)(c + i) * W + j] : 0.f;
+    for (int i = 0; i < kVec * W; ++i) v[i] = i / W < n ? w[(long long)c * W + i] : 0.f;
   }
+#pragma unroll
+  for (int j = 0; j < W; ++j) f[j] = {pack2(v[j], v[W + j]), pack2(v[2 * W + j], v[3 * W + j])};
+}
+__device__ __forceinline__ Four load_bias(const float* bias, int c, int n) {
+  float b[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) b[i] = bias && i < n ? bias[c + i] : 0.f;
+  return {pack2(b[0], b[1]), pack2(b[2], b[3])};
+}
+// act(bias + sum of taps), rounded
+template <typename T, int W>
+__device__ __forceinline__ Raw4<T> filter(const Four (&f)[W], const Four& bias, const Four (&win)[W],
+                                          int act) {
+  Four a = bias;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    a.lo = fma2(f[j].lo, win[j].lo, a.lo);
+    a.hi = fma2(f[j].hi, win[j].hi, a.hi);
+  }
+  if (act) {
+    a.lo = silu2(a.lo);
+    a.hi = silu2(a.hi);
+  }
+  float v0, v1, v2, v3;
+  unpack2(a.lo, v0, v1);
+  unpack2(a.hi, v2, v3);
+  Raw4<T> o;
+  o.set(v0, v1, v2, v3);
+  return o;
 }
 
 // A sequence's tokens in the packed (or row-major) batch, clamped to the batch so that no
@@ -51,17 +89,20 @@ __device__ __forceinline__ Span span_of(const ConvParams& p, int n) {
   return {b, max(b, e)};
 }
 
-// Row of the window of token t (of the sequence `s`), j tokens back: an input, or the state.
+// Row of the window of a token of sequence n, t = an absolute row: an input, or the state.
 template <typename T, int W>
-__device__ __forceinline__ Raw8<T> tap(const ConvParams& p, const Span& s, int n, long long t,
+__device__ __forceinline__ Raw4<T> tap(const ConvParams& p, const Span& s, int n, long long t,
                                        int c, int left, bool vec) {
-  if (t >= s.begin) return load8(static_cast<const T*>(p.x) + t * p.x_stride + c, left, vec);
-  Raw8<T> r;
-  r.zero();
-  if (p.s0)
-    r = load8(static_cast<const T*>(p.s0) +
-                  ((long long)n * (W - 1) + (W - 1) + (t - s.begin)) * p.D + c,
-              left, vec);
+  Raw4<T> r;
+  if (t >= s.begin) {
+    r.load(static_cast<const T*>(p.x) + t * p.x_stride + c, left, vec);
+  } else if (p.s0) {
+    r.load(static_cast<const T*>(p.s0) +
+               ((long long)n * (W - 1) + (W - 1) + (t - s.begin)) * p.D + c,
+           left, vec);
+  } else {
+    r.zero();
+  }
   return r;
 }
 
@@ -69,16 +110,16 @@ __device__ __forceinline__ Raw8<T> tap(const ConvParams& p, const Span& s, int n
 template <typename T, int W>
 __device__ __forceinline__ void write_state(const ConvParams& p, int n, int c, int left, bool vec) {
   const Span s = span_of(p, n);
-  Raw8<T> r[W - 1];
+  Raw4<T> r[W - 1];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) r[j] = tap<T, W>(p, s, n, s.end - (W - 1) + j, c, left, vec);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j)
-    store8(static_cast<T*>(p.sT) + ((long long)n * (W - 1) + j) * p.D + c, r[j], left, vec);
+    r[j].store(static_cast<T*>(p.sT) + ((long long)n * (W - 1) + j) * p.D + c, left, vec);
 }
 
 // blockIdx.x: run of `run` tokens, then (with `states`) one sequence's state each;
-// blockIdx.y: 128 threads of 8 channels.
+// blockIdx.y: 128 threads of 4 channels.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int run, int runs,
                                                         long long tokens) {
@@ -91,8 +132,12 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
     return;
   }
   const long long t0 = (long long)blockIdx.x * run, t1 = min(t0 + run, tokens);
-  const T* x = static_cast<const T*>(p.x) + c;
-  T* y = static_cast<T*>(p.y) + c;
+  const T* x = static_cast<const T*>(p.x) + t0 * p.x_stride + c;
+  T* y = static_cast<T*>(p.y) + t0 * p.D + c;
+  Raw4<T> ahead[kAhead];  // the tokens of the next round
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (t0 + u < t1) ahead[u].load(x + u * p.x_stride, left, vec);
 
   // the sequence of token t0: the first one that ends behind it
   int n = 0;
@@ -109,56 +154,51 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   if (n >= p.N) return;  // behind the last sequence: left as it was
   Span s = span_of(p, n);
 
-  float f[kVec][W], bias[kVec], win[W - 1][kVec];
+  Four f[W], win[W];  // the filter, and the inputs under it
   load_filter<W>(p.w, c, left, f);
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) bias[i] = p.bias && i < left ? p.bias[c + i] : 0.f;
+  const Four bias = load_bias(p.bias, c, left);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j)
-    tap<T, W>(p, s, n, max(t0, s.begin) - (W - 1) + j, c, left, vec).get(win[j]);
+    win[j] = four(tap<T, W>(p, s, n, max(t0, s.begin) - (W - 1) + j, c, left, vec));
 
-  for (long long t = t0; t < t1; t += kUnroll) {
-    Raw8<T> raw[kUnroll];
+  for (long long t = t0; t < t1; t += kAhead) {
+    Raw4<T> raw[kAhead];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (t + u < t1) raw[u] = load8(x + (t + u) * p.x_stride, left, vec);
+    for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
+    x += kAhead * p.x_stride;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const long long tt = t + u;
-      if (tt >= t1) return;
-      if (tt >= s.end) {  // the next sequence that has tokens begins
-        do {
-          if (++n >= p.N) return;
-          s = span_of(p, n);
-        } while (tt >= s.end);
+    for (int u = 0; u < kAhead; ++u)
+      if (t + kAhead + u < t1) ahead[u].load(x + u * p.x_stride, left, vec);
+    if (t >= s.begin && t + kAhead <= min(t1, s.end)) {  // one sequence's tokens
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-          tap<T, W>(p, s, n, max(tt, s.begin) - (W - 1) + j, c, left, vec).get(win[j]);
+      for (int u = 0; u < kAhead; ++u) {
+        win[W - 1] = four(raw[u]);
+        filter<T, W>(f, bias, win, p.silu).store(y + (long long)u * p.D, left, vec);
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
       }
-      if (tt < s.begin) continue;
-      float in[kVec], out[kVec];
-      raw[u].get(in);
+    } else {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        float a = bias[i];
+      for (int u = 0; u < kAhead; ++u) {
+        const long long tt = t + u;
+        if (tt >= t1) return;
+        if (tt >= s.end) {  // the next sequence that has tokens begins
+          do {
+            if (++n >= p.N) return;
+            s = span_of(p, n);
+          } while (tt >= s.end);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) a = fmaf(f[i][j], win[j][i], a);
-        out[i] = fmaf(f[i][W - 1], in[i], a);
+          for (int j = 0; j < W - 1; ++j)
+            win[j] = four(tap<T, W>(p, s, n, max(tt, s.begin) - (W - 1) + j, c, left, vec));
+        }
+        if (tt < s.begin) continue;
+        win[W - 1] = four(raw[u]);
+        filter<T, W>(f, bias, win, p.silu).store(y + (long long)u * p.D, left, vec);
+#pragma unroll
+        for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
       }
-      if (p.silu) {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) out[i] = silu(out[i]);
-      }
-      Raw8<T> o;
-      o.set(out);
-      store8(y + tt * p.D, o, left, vec);
-#pragma unroll
-      for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) win[j][i] = win[j + 1][i];
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) win[W - 2][i] = in[i];
     }
+    y += kAhead * (long long)p.D;
   }
 }
 
@@ -170,40 +210,41 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(const ConvParams p
   if (c < p.D) write_state<T, W>(p, blockIdx.x, c, p.D - c, p.vec);
 }
 
-// One token per sequence: a thread holds the window of 8 channels, s is shifted in place.
-template <typename T, int W>
+// One token per sequence: a thread holds the windows of 4 channels of kSeqs sequences and
+// shifts their states in place.  kSeqs > 1 shares the filter, which is as many bytes as the
+// window and the output of one sequence.
+template <typename T, int W, int kSeqs>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p, int per_row) {
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long n = id / per_row;
-  if (n >= p.N) return;
+  const long long first = id / per_row * kSeqs;
+  if (first >= p.N) return;
   const int c = (int)(id % per_row) * kVec;
   const int left = p.D - c;
   const bool vec = p.vec;
-  T* s = static_cast<T*>(p.sT) + n * (W - 1) * p.D + c;
-  Raw8<T> r[W];
+  Raw4<T> r[kSeqs][W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) r[j] = load8(s + (long long)j * p.D, left, vec);
-  r[W - 1] = load8(static_cast<const T*>(p.x) + n * p.x_stride + c, left, vec);
-  float f[kVec][W], out[kVec];
+  for (int i = 0; i < kSeqs; ++i) {
+    if (first + i >= p.N) break;
+    const T* s = static_cast<const T*>(p.sT) + (first + i) * (W - 1) * p.D + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) r[i][j].load(s + (long long)j * p.D, left, vec);
+    r[i][W - 1].load(static_cast<const T*>(p.x) + (first + i) * p.x_stride + c, left, vec);
+  }
+  Four f[W];
   load_filter<W>(p.w, c, left, f);
+  const Four bias = load_bias(p.bias, c, left);
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) out[i] = p.bias && i < left ? p.bias[c + i] : 0.f;
+  for (int i = 0; i < kSeqs; ++i) {
+    if (first + i >= p.N) break;
+    Four win[W];
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    float in[kVec];
-    r[j].get(in);
+    for (int j = 0; j < W; ++j) win[j] = four(r[i][j]);
+    filter<T, W>(f, bias, win, p.silu)
+        .store(static_cast<T*>(p.y) + (first + i) * p.D + c, left, vec);
+    T* s = static_cast<T*>(p.sT) + (first + i) * (W - 1) * p.D + c;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) out[i] = fmaf(f[i][j], in[i], out[i]);
+    for (int j = 0; j < W - 1; ++j) r[i][j + 1].store(s + (long long)j * p.D, left, vec);
   }
-  if (p.silu) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) out[i] = silu(out[i]);
-  }
-  Raw8<T> o;
-  o.set(out);
-  store8(static_cast<T*>(p.y) + n * p.D + c, o, left, vec);
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j) store8(s + (long long)j * p.D, r[j + 1], left, vec);
 }
 
 template <typename T, int W>
@@ -211,7 +252,9 @@ cudaError_t launch_w(const ConvParams& p, cudaStream_t stream) {
   const long long tokens = p.cu ? (long long)p.T : (long long)p.N * p.T;
   const int per_row = (p.D + kVec - 1) / kVec;
   const unsigned by = (per_row + kThreads - 1) / kThreads;
-  const int run = 32;
+  // long runs repeat fewer rows (W - 1 each), short ones fill the GPU: 8 blocks per SM
+  int run = 64;
+  while (run > kAhead && (tokens + run - 1) / run * by < 8 * kSms) run /= 2;
   const long long runs = (tokens + run - 1) / run;
   // sT == s0: the states wait for every block that reads them
   const bool apart = p.sT && (p.s0 == p.sT || tokens == 0);
@@ -233,14 +276,25 @@ cudaError_t launch_t(const ConvParams& p, cudaStream_t stream) {
   return launch_w<T, 2>(p, stream);
 }
 
+template <typename T, int W>
+cudaError_t launch_step_w(const ConvParams& p, cudaStream_t stream) {
+  const int per_row = (p.D + kVec - 1) / kVec;
+  const auto blocks = [&](int seqs) {
+    return (unsigned)(((long long)((p.N + seqs - 1) / seqs) * per_row + kThreads - 1) / kThreads);
+  };
+  // two sequences a thread once that still leaves 8 blocks per SM
+  if (blocks(2) >= 8 * kSms)
+    conv_step_kernel<T, W, 2><<<blocks(2), kThreads, 0, stream>>>(p, per_row);
+  else
+    conv_step_kernel<T, W, 1><<<blocks(1), kThreads, 0, stream>>>(p, per_row);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_step_t(const ConvParams& p, cudaStream_t stream) {
-  const int per_row = (p.D + kVec - 1) / kVec;
-  const unsigned blocks = (unsigned)(((long long)p.N * per_row + kThreads - 1) / kThreads);
-  if (p.W == 4) conv_step_kernel<T, 4><<<blocks, kThreads, 0, stream>>>(p, per_row);
-  else if (p.W == 3) conv_step_kernel<T, 3><<<blocks, kThreads, 0, stream>>>(p, per_row);
-  else conv_step_kernel<T, 2><<<blocks, kThreads, 0, stream>>>(p, per_row);
-  return cudaGetLastError();
+  if (p.W == 4) return launch_step_w<T, 4>(p, stream);
+  if (p.W == 3) return launch_step_w<T, 3>(p, stream);
+  return launch_step_w<T, 2>(p, stream);
 }
 
 }  // namespace
