@@ -66,13 +66,14 @@ __device__ __forceinline__ float scale_of(float amax) {
 }
 
 // One row per G threads (kBlock: per block), NV vectors of 8 columns a thread: vector
-// i * G + (thread of the row).  A block walks rows gridDim.x apart; the next row is loaded
-// while the present one is reduced, and w stays in registers (rows beyond 8192 columns: a
-// block of up to 1024 threads has registers for one row only, and loads w and the gate late).
+// i * G + (thread of the row).  Rows within a warp: a block walks rows, the next one is
+// loaded while the present one is reduced, and w stays in registers.  A row per block: one
+// row each, as many blocks side by side as fit (beyond 8192 columns a block of up to 1024
+// threads has registers for the row only, and loads w and the gate late).
 template <typename T, bool kFp8, bool kBlock, int NV>
 __global__ void __launch_bounds__(!kBlock ? 128 : NV == 4 ? 1024 : 1024 / NV)
     norm_kernel(const NormParams p, int G) {
-  constexpr bool kWide = kBlock && NV == 4;
+  constexpr bool kWide = kBlock && NV == 4, kLoop = !kBlock;
   __shared__ float s_red[2][2][32];  // by turns, so that one barrier a reduction is enough
   const int lane = kBlock ? threadIdx.x : threadIdx.x % G;
   const int per_block = kBlock ? 1 : blockDim.x / G;
@@ -107,7 +108,8 @@ __global__ void __launch_bounds__(!kBlock ? 128 : NV == 4 ? 1024 : 1024 / NV)
   if (!kWide && row0 < p.rows) load_row(row0);
   int turn = 0;
   // every thread of a warp stays for the shuffles: rows are per block, or guarded by `some`
-  for (long long base = (long long)blockIdx.x * per_block; base < p.rows; base += step, turn ^= 1) {
+  for (long long base = (long long)blockIdx.x * per_block; base < p.rows;
+       base = kLoop ? base + step : p.rows, turn ^= 1) {
     const long long row = base + (kBlock ? 0 : threadIdx.x / G);
     const bool some = row < p.rows;
     float r[NV][8];
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : NV == 4 ? 1024 : 1024 / NV)
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
     }
-    if (!kWide && row + step < p.rows) load_row(row + step);
+    if (kLoop && row + step < p.rows) load_row(row + step);
     if (p.residual && some) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -206,8 +208,8 @@ template <typename T, bool kFp8, bool kBlock, int NV>
 cudaError_t launch_k(const NormParams& p, int threads, int G, cudaStream_t stream) {
   const long long per_block = kBlock ? 1 : threads / G;
   const long long blocks = (p.rows + per_block - 1) / per_block;
-  // as many blocks as fit side by side; beyond that a block takes several rows in turn
-  const long long most = (long long)kSms * (kBlock ? (1536 / threads > 1 ? 1536 / threads : 1) : 12);
+  // rows within a warp: as many blocks as fit side by side, each takes its rows in turn
+  const long long most = kBlock ? blocks : 12ll * kSms;
   norm_kernel<T, kFp8, kBlock, NV>
       <<<(unsigned)(blocks < most ? blocks : most), threads, 0, stream>>>(p, G);
   return cudaGetLastError();

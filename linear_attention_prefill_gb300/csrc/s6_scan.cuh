@@ -85,8 +85,11 @@ struct Cfg {
   static constexpr int kPart = kWide + (kWiden ? 2 * kWideTile : 0);
   static constexpr int kPieces = kPart + (kSummary ? kTile / 4 * kCh / 4 : 2 * kPartTile);
   static constexpr int kBytes = kPieces * 16;
+  // The one-channel variant is for one CTA an SM: more than half of the shared memory, so that
+  // no SM takes two while others have none.
+  static constexpr int kAsked = kWidth == 1 && kBytes < 116 * 1024 ? 116 * 1024 : kBytes;
   // CTAs per SM: by shared memory, and by registers with at least 112 a thread
-  static constexpr int kBySmem = 227 * 1024 / (kBytes + 1024), kByRegs = 65536 / 112 / kThreads;
+  static constexpr int kBySmem = 227 * 1024 / (kAsked + 1024), kByRegs = 65536 / 112 / kThreads;
   static constexpr int kBlocks = kBySmem < kByRegs ? kBySmem : kByRegs < 1 ? 1 : kByRegs;
 };
 
@@ -670,7 +673,7 @@ template <class C>
 cudaError_t launch_k(const S6Params& p, cudaStream_t stream) {
   const auto kernel = s6_kernel<C>;
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes);
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAsked);
   if (e != cudaSuccess) return e;
   const int tiles = (p.dim + kCh - 1) / kCh;
   const long long whole = C::kSummary ? 0 : (long long)p.N * p.whole;
@@ -680,7 +683,7 @@ cudaError_t launch_k(const S6Params& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(whole + (long long)(tiles - p.whole) * p.slots));
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kBytes;
+  cfg.dynamicSmemBytes = C::kAsked;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
