@@ -11,6 +11,7 @@
 #include "abi_common.h"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "layer_internal.h"
 
 #ifdef GDN_PROFILE
 __device__ unsigned long long g_gdn_phase[64];
@@ -19,6 +20,10 @@ __device__ unsigned long long g_gdn_phase[64];
 namespace gdn {
 
 __device__ unsigned g_device_error = 0u;
+
+cudaError_t device_error_word(unsigned** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_device_error);
+}
 
 cudaError_t read_and_clear_device_error(unsigned* out, cudaStream_t stream) {
   unsigned zero = 0u;

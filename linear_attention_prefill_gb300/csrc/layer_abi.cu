@@ -274,12 +274,16 @@ gdn_status run_norm(const void* x, const float* w, const void* residual, const v
   p.x = x; p.residual = residual; p.gate = gate; p.w = w; p.y = y;
   p.residual_out = residual_out; p.scales = scales;
   p.rows = rows; p.x_stride = x_stride; p.gate_stride = gate_stride;
-  p.heads = heads; p.D = D; p.group = span < D ? span : D; p.eps = eps;
+  p.heads = heads; p.D = D; p.eps = eps;
+  p.group = span < D ? span : D;
+  p.groups = (D + p.group - 1) / p.group;
   const bool one = tokens <= 1;
   p.vec = D % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) &&
           aligned(gate, 16) && aligned(w, 16) && aligned(y, fp8 ? 8 : 16) &&
           (one || x_stride * elem % 16 == 0) && (one || !gate || gate_stride * elem % 16 == 0);
-  const cudaError_t e = gdn::launch_norm(p, f32, fp8, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = gdn::device_error_word(&p.err);
+  if (e != cudaSuccess) return cuda_fail(e, "locating the device error word");
+  e = gdn::launch_norm(p, f32, fp8, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the RMS norm");
 }
 

@@ -155,6 +155,29 @@ struct Raw4<float> {
     v = make_float4(a, b, c, d);
   }
 };
+// Eight elements as four packed pairs, and back.
+__device__ __forceinline__ void pairs_of(const Raw8<__nv_bfloat16>& r, unsigned long long (&o)[4]) {
+  const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("mov.b64 %0, {%1, %2};" : "=l"(o[i]) : "r"(w[i] << 16), "r"(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void pairs_of(const Raw8<float>& r, unsigned long long (&o)[4]) {
+  asm("mov.b64 %0, {%1, %2};" : "=l"(o[0]) : "f"(r.a.x), "f"(r.a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(o[1]) : "f"(r.a.z), "f"(r.a.w));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(o[2]) : "f"(r.b.x), "f"(r.b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(o[3]) : "f"(r.b.z), "f"(r.b.w));
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_of(const unsigned long long (&v)[4]) {
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o[2 * i]), "=f"(o[2 * i + 1]) : "l"(v[i]));
+  Raw8<T> r;
+  r.set(o);
+  return r;
+}
 // The first n of 8 elements at p, by one wide access where the caller's `vec` says that p
 // is 16-byte aligned and n >= 8.
 template <typename T>

@@ -10,6 +10,9 @@ namespace gdn {
 
 constexpr int kSms = 152;
 
+// Address of the device error word on the current device (gdn_abi.cu).
+cudaError_t device_error_word(unsigned** out);
+
 // Short causal convolution over tokens, one filter per channel.
 struct ConvParams {
   const void* x;      // rows of D channels, x_stride elements from token to token
@@ -72,9 +75,10 @@ struct NormParams {
   long long rows;                   // tokens * heads
   long long x_stride, gate_stride;  // elements from token to token
   int heads, D;
-  int group;                        // columns per scale; D for one scale a row
+  int group, groups;                // columns per scale (D: one scale a row), scales a row
   float eps;
   int vec;                          // every 8-column access is aligned and D is a multiple of 8
+  unsigned* err;                    // device error word: bounded waits record a timeout here
 };
 constexpr int kNormMaxD = 32768;
 cudaError_t launch_norm(const NormParams& p, bool f32, bool fp8, cudaStream_t stream);

@@ -8,51 +8,37 @@
 // r is added, normed and quantised in fp32; it is rounded once to be stored as the new
 // residual, and y once on the way out.  HBM bandwidth bounds it: every tensor crosses once,
 // with the row held in registers between the sum of squares and the output.  A thread
-// holds vectors of 8 columns, so a group of 32, 64 or 128 columns is 4, 8 or 16 lanes.
-#include <cuda_fp8.h>
-
+// holds vectors of 8 columns as packed pairs, so a group of 32, 64 or 128 columns is 4, 8 or 16
+// lanes.
+#include "gdn_common.cuh"
 #include "layer_common.cuh"
 #include "layer_internal.h"
 
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-// Four e4m3 of y * inv, saturating.
-__device__ __forceinline__ uint32_t e4m3x4(const float* y, float inv) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1] * inv), "f"(y[0] * inv));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3] * inv), "f"(y[2] * inv));
-  return lo | ((uint32_t)hi << 16);
+// max |a|, |b| as bit patterns: those of NaN are above those of infinity, so NaN wins
+__device__ __forceinline__ uint32_t abs_bits(float a) { return __float_as_uint(a) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t max_bits(f32x2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return max(abs_bits(a), abs_bits(b));
 }
 
-// Sum or maximum over the G threads of a row: G <= 32 lanes of a warp, or the whole block.
-template <bool kMax>
-__device__ __forceinline__ float combine(float a, float b) {
-  return kMax ? max_nan(a, b) : a + b;
+// Two e4m3, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(f32x2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  uint16_t q;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(b), "f"(a));
+  return q;
 }
-template <bool kMax, bool kBlock>
-__device__ __forceinline__ float reduce_row(float v, int G, float* s) {
-  const int lanes = kBlock ? 32 : G;
-  for (int off = lanes >> 1; off > 0; off >>= 1)
-    v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, off));
-  if (!kBlock) return v;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s[0];
-  for (int i = 1; i < warps; ++i) v = combine<kMax>(v, s[i]);
-  return v;
-}
-
-// The columns' e4m3 of one vector.
-__device__ __forceinline__ void store_e4m3(uint8_t* q, const float (&r)[8], float inv, int n,
+// One vector's e4m3 of y * inv.
+__device__ __forceinline__ void store_e4m3(uint8_t* q, const f32x2 (&y)[4], float inv, int n,
                                            bool vec) {
-  const uint2 v = make_uint2(e4m3x4(&r[0], inv), e4m3x4(&r[4], inv));
+  const f32x2 s = dup2(inv);
+  const uint2 v = make_uint2(e4m3x2(mul2(y[0], s)) | (e4m3x2(mul2(y[1], s)) << 16),
+                             e4m3x2(mul2(y[2], s)) | (e4m3x2(mul2(y[3], s)) << 16));
   if (vec) {
     *reinterpret_cast<uint2*>(q) = v;
   } else {
@@ -61,175 +47,371 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const float (&r)[8], floa
       if (j < n) q[j] = (uint8_t)((j < 4 ? v.x : v.y) >> (8 * (j & 3)));
   }
 }
-__device__ __forceinline__ float scale_of(float amax) {
-  return amax == 0.f ? 1.f : max_nan(__fdiv_rn(amax, 448.f), 1.17549435e-38f);
+// max|y| -> scale; the reciprocal and the product by 1 / 448 are within an ulp each
+__device__ __forceinline__ float scale_of(uint32_t amax) {
+  const float m = __uint_as_float(amax);
+  return m == 0.f ? 1.f : m < 5.2666e-36f ? 1.17549435e-38f : m * (1.f / 448.f);
 }
 
-// One row per G threads (kBlock: per block), NV vectors of 8 columns a thread: vector
-// i * G + (thread of the row).  Rows within a warp: a block walks rows, the next one is
-// loaded while the present one is reduced, and w stays in registers.  A row per block: one
-// row each, as many blocks side by side as fit (beyond 8192 columns a block of up to 1024
-// threads has registers for the row only, and loads w and the gate late).
+template <typename V>
+__device__ __forceinline__ V combine(V a, V b);
+template <>
+__device__ __forceinline__ float combine(float a, float b) { return a + b; }
+template <>
+__device__ __forceinline__ uint32_t combine(uint32_t a, uint32_t b) { return max(a, b); }
+// Sum (of floats) or maximum (of bit patterns) over the G threads of a row: G <= 32 lanes of a
+// warp, or the whole block.
+template <bool kBlock, typename V>
+__device__ __forceinline__ V reduce_row(V v, int G, V* s) {
+  const int lanes = kBlock ? 32 : G;
+  for (int off = lanes >> 1; off > 0; off >>= 1)
+    v = combine<V>(v, __shfl_xor_sync(0xffffffffu, v, off));
+  if (!kBlock) return v;
+  const int warps = blockDim.x >> 5;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = s[0];
+  for (int i = 1; i < warps; ++i) v = combine<V>(v, s[i]);
+  return v;
+}
+
+// What a row is after its sum of squares is known: y of every vector, stored.
 template <typename T, bool kFp8, bool kBlock, int NV>
-__global__ void __launch_bounds__(!kBlock ? 128 : NV == 4 ? 1024 : 1024 / NV)
-    norm_kernel(const NormParams p, int G) {
-  constexpr bool kWide = kBlock && NV == 4, kLoop = !kBlock;
-  __shared__ float s_red[2][2][32];  // by turns, so that one barrier a reduction is enough
-  const int lane = kBlock ? threadIdx.x : threadIdx.x % G;
-  const int per_block = kBlock ? 1 : blockDim.x / G;
-  const long long step = (long long)gridDim.x * per_block;
-  const bool vec = p.vec;
-  int n[NV];  // columns of this thread's vectors that exist
-  float w[kWide ? 1 : NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * G + lane) * 8;
-    n[i] = p.D - c;
-    if (!kWide && n[i] > 0) load8(p.w + c, n[i], vec).get(w[i]);
-  }
-  Raw8<T> x_next[NV], r_next[NV], g_next[kWide ? 1 : NV];
-  auto load_row = [&](long long row) {
-    const long long token = row / p.heads;
-    const long long col = (row - token * p.heads) * p.D;
-    const T* x = static_cast<const T*>(p.x) + token * p.x_stride + col;
-    const T* r = static_cast<const T*>(p.residual) + row * p.D;
-    const T* g = static_cast<const T*>(p.gate) + token * p.gate_stride + col;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * G + lane) * 8;
-      if (n[i] > 0) {
-        x_next[i] = load8(x + c, n[i], vec);
-        if (p.residual) r_next[i] = load8(r + c, n[i], vec);
-        if (!kWide && p.gate) g_next[i] = load8(g + c, n[i], vec);
-      }
-    }
-  };
-  const long long row0 = (long long)blockIdx.x * per_block + (kBlock ? 0 : threadIdx.x / G);
-  if (!kWide && row0 < p.rows) load_row(row0);
-  int turn = 0;
-  // every thread of a warp stays for the shuffles: rows are per block, or guarded by `some`
-  for (long long base = (long long)blockIdx.x * per_block; base < p.rows;
-       base = kLoop ? base + step : p.rows, turn ^= 1) {
-    const long long row = base + (kBlock ? 0 : threadIdx.x / G);
-    const bool some = row < p.rows;
-    float r[NV][8];
-    Raw8<T> g[kWide ? 1 : NV];
-    float ss = 0.f;
-    if (kWide) load_row(row);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (!kWide) g[i] = g_next[i];
-      if (!some || n[i] <= 0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = 0.f;
-        continue;
-      }
-      x_next[i].get(r[i]);
-      if (p.residual) {
-        float q[8];
-        r_next[i].get(q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] += q[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
-    }
-    if (kLoop && row + step < p.rows) load_row(row + step);
-    if (p.residual && some) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = (i * G + lane) * 8;
-        Raw8<T> o;
-        o.set(r[i]);
-        if (n[i] > 0) store8(static_cast<T*>(p.residual_out) + row * p.D + c, o, n[i], vec);
-      }
-    }
-    ss = reduce_row<false, kBlock>(ss, G, s_red[0][turn]);
-    const float rstd = rsqrtf(ss / (float)p.D + p.eps);
-    float amax = 0.f;
+struct Finish {
+  // r: the row's vectors; load_w(i), load_gate(i): vector i of w and of the gate; n[i]: columns
+  // that exist (whole vectors with p.vec); some: there is a row
+  template <typename W, typename G_>
+  static __device__ __forceinline__ void run(const NormParams& p, long long row, bool some, int G,
+                                             int lane, f32x2 (&r)[NV][4], const int (&n)[NV],
+                                             float ss, uint32_t* s_max, W load_w, G_ load_gate) {
+    const bool vec = p.vec;
+    const f32x2 rstd = dup2(rsqrtf(ss / (float)p.D + p.eps));
+    uint32_t amax = 0u;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * G + lane) * 8;
       const bool here = some && n[i] > 0;
       if (here) {
-        if (kWide) load8(p.w + c, n[i], vec).get(w[0]);
+        f32x2 q[4];
+        load_w(i, q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * rstd * w[kWide ? 0 : i][j];
+        for (int j = 0; j < 4; ++j) r[i][j] = mul2(mul2(r[i][j], rstd), q[j]);
         if (p.gate) {
-          float q[8];
-          if (kWide) {
-            const long long token = row / p.heads;
-            g[0] = load8(static_cast<const T*>(p.gate) + token * p.gate_stride +
-                             (row - token * p.heads) * p.D + c,
-                         n[i], vec);
-          }
-          g[kWide ? 0 : i].get(q);
+          load_gate(i, q);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) r[i][j] *= silu(q[j]);
+          for (int j = 0; j < 4; ++j) r[i][j] = mul2(r[i][j], silu2(q[j]));
         }
-        if (!kFp8) {
-          Raw8<T> o;
-          o.set(r[i]);
-          store8(static_cast<T*>(p.y) + row * p.D + c, o, n[i], vec);
-        }
+        if (!kFp8)
+          store8(static_cast<T*>(p.y) + row * p.D + c, raw_of<T>(r[i]), n[i], vec);
       }
       if (kFp8) {
-        float m = 0.f;
+        uint32_t m = 0u;
+        if (here) {
+          if (!vec) {  // columns that do not exist were read as zeros, but a row of NaN has none
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (here && j < n[i]) m = max_nan(m, fabsf(r[i][j]));
+            for (int j = 0; j < 4; ++j) {
+              float a, b;
+              unpack2(r[i][j], a, b);
+              r[i][j] = pack2(2 * j < n[i] ? a : 0.f, 2 * j + 1 < n[i] ? b : 0.f);
+            }
+          }
+          m = max(max(max_bits(r[i][0]), max_bits(r[i][1])),
+                  max(max_bits(r[i][2]), max_bits(r[i][3])));
+        }
         if (p.group < p.D) {  // the lanes of the group: group / 8 neighbours
           for (int off = p.group >> 4; off > 0; off >>= 1)
-            m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
           if (here) {
             const float scale = scale_of(m);
-            store_e4m3(static_cast<uint8_t*>(p.y) + row * p.D + c, r[i], __frcp_rn(scale), n[i], vec);
-            const int groups = (p.D + p.group - 1) / p.group;
-            if (c % p.group == 0) p.scales[row * groups + c / p.group] = scale;
+            store_e4m3(static_cast<uint8_t*>(p.y) + row * p.D + c, r[i], rcp(scale), n[i], vec);
+            if ((c & (p.group - 1)) == 0) p.scales[row * p.groups + c / p.group] = scale;
           }
         } else {
-          amax = max_nan(amax, m);
+          amax = max(amax, m);
         }
       }
     }
     if (kFp8 && p.group >= p.D) {  // one scale a row
-      amax = reduce_row<true, kBlock>(amax, G, s_red[1][turn]);
-      const float scale = scale_of(amax), inv = __frcp_rn(scale);
+      amax = reduce_row<kBlock>(amax, G, s_max);
+      const float scale = scale_of(amax), inv = rcp(scale);
       if (some && lane == 0) p.scales[row] = scale;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (some && n[i] > 0)
-          store_e4m3(static_cast<uint8_t*>(p.y) + row * p.D + (i * G + lane) * 8, r[i], inv, n[i], vec);
+          store_e4m3(static_cast<uint8_t*>(p.y) + row * p.D + (i * G + lane) * 8, r[i], inv, n[i],
+                     vec);
     }
+  }
+};
+
+// x + residual of one vector, the residual's update stored; adds the squares to ss.
+template <typename T>
+__device__ __forceinline__ void take(const NormParams& p, long long at, const Raw8<T>& x,
+                                     const Raw8<T>& res, int n, f32x2 (&r)[4], f32x2& ss) {
+  pairs_of(x, r);
+  if (p.residual) {
+    f32x2 q[4];
+    pairs_of(res, q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = add2(r[j], q[j]);
+    store8(static_cast<T*>(p.residual_out) + at, raw_of<T>(r), n, p.vec);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) ss = fma2(r[j], r[j], ss);
+}
+
+// Rows within a warp: G lanes a row, NV vectors of 8 columns a lane: vector i * G + lane.  A
+// block walks its rows, the next one is loaded while the present one is reduced, and w stays in
+// registers.
+template <typename T, bool kFp8, int NV>
+__global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p, int G) {
+  const int lane = threadIdx.x % G, per_block = 128 / G;
+  const long long step = (long long)gridDim.x * per_block;
+  const bool vec = p.vec;
+  int n[NV];
+  f32x2 w[NV][4];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + lane) * 8;
+    n[i] = p.D - c;
+    if (n[i] > 0) pairs_of(load8(p.w + c, n[i], vec), w[i]);
+  }
+  Raw8<T> x[NV], res[NV], gate[NV];
+  auto load_row = [&](long long row) {
+    const long long token = p.heads == 1 ? row : row / p.heads;
+    const long long col = (row - token * p.heads) * p.D + lane * 8;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (n[i] <= 0) continue;
+      x[i] = load8(static_cast<const T*>(p.x) + token * p.x_stride + col + i * G * 8, n[i], vec);
+      if (p.residual)
+        res[i] = load8(static_cast<const T*>(p.residual) + row * p.D + (i * G + lane) * 8, n[i], vec);
+      if (p.gate)
+        gate[i] = load8(static_cast<const T*>(p.gate) + token * p.gate_stride + col + i * G * 8, n[i],
+                        vec);
+    }
+  };
+  const long long row0 = (long long)blockIdx.x * per_block + threadIdx.x / G;
+  if (row0 < p.rows) load_row(row0);
+  // every lane of a warp stays for the shuffles
+  for (long long base = (long long)blockIdx.x * per_block; base < p.rows; base += step) {
+    const long long row = base + threadIdx.x / G;
+    const bool some = row < p.rows;
+    f32x2 r[NV][4], ss = 0ull;
+    Raw8<T> g[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (some && n[i] > 0) {
+        take(p, row * p.D + (i * G + lane) * 8, x[i], res[i], n[i], r[i], ss);
+        g[i] = gate[i];
+      }
+    }
+    if (row + step < p.rows) load_row(row + step);
+    float s0, s1;
+    unpack2(ss, s0, s1);
+    const float sum = reduce_row<false>(s0 + s1, G, (float*)nullptr);
+    Finish<T, kFp8, false, NV>::run(
+        p, row, some, G, lane, r, n, sum, nullptr,
+        [&](int i, f32x2 (&q)[4]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q[j] = w[i][j];
+        },
+        [&](int i, f32x2 (&q)[4]) { pairs_of(g[i], q); });
   }
 }
 
-template <typename T, bool kFp8, bool kBlock, int NV>
-cudaError_t launch_k(const NormParams& p, int threads, int G, cudaStream_t stream) {
-  const long long per_block = kBlock ? 1 : threads / G;
-  const long long blocks = (p.rows + per_block - 1) / per_block;
-  // rows within a warp: as many blocks as fit side by side, each takes its rows in turn
-  const long long most = kBlock ? blocks : 12ll * kSms;
-  norm_kernel<T, kFp8, kBlock, NV>
-      <<<(unsigned)(blocks < most ? blocks : most), threads, 0, stream>>>(p, G);
+// A row per block of G threads, NV vectors a thread.  Up to 8192 columns w and the gate are
+// loaded with the row; wider blocks (up to 1024 threads) have registers for the row only.
+template <typename T, bool kFp8, int NV>
+__global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
+    norm_block_kernel(const NormParams p, int G) {
+  constexpr bool kWide = NV == 4;
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int lane = threadIdx.x;
+  const bool vec = p.vec;
+  const long long row = blockIdx.x;
+  const long long token = p.heads == 1 ? row : row / p.heads;
+  const long long col = (row - token * p.heads) * p.D + lane * 8;
+  const T* xp = static_cast<const T*>(p.x) + token * p.x_stride + col;
+  const T* gp = static_cast<const T*>(p.gate) + token * p.gate_stride + col;
+  int n[NV];
+  Raw8<T> x[NV], res[NV], g[kWide ? 1 : NV];
+  Raw8<float> w[kWide ? 1 : NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + lane) * 8;
+    n[i] = p.D - c;
+    if (n[i] <= 0) continue;
+    x[i] = load8(xp + i * G * 8, n[i], vec);
+    if (p.residual) res[i] = load8(static_cast<const T*>(p.residual) + row * p.D + c, n[i], vec);
+  }
+  if (!kWide) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (n[i] <= 0) continue;
+      if (p.gate) g[i] = load8(gp + i * G * 8, n[i], vec);
+      w[i] = load8(p.w + (i * G + lane) * 8, n[i], vec);
+    }
+  }
+  f32x2 r[NV][4], ss = 0ull;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (n[i] > 0) take(p, row * p.D + (i * G + lane) * 8, x[i], res[i], n[i], r[i], ss);
+  float s0, s1;
+  unpack2(ss, s0, s1);
+  const float sum = reduce_row<true>(s0 + s1, G, s_sum);
+  Finish<T, kFp8, true, NV>::run(
+      p, row, true, G, lane, r, n, sum, s_max,
+      [&](int i, f32x2 (&q)[4]) {
+        if (kWide) w[0] = load8(p.w + (i * G + lane) * 8, n[i], vec);
+        pairs_of(w[kWide ? 0 : i], q);
+      },
+      [&](int i, f32x2 (&q)[4]) {
+        if (kWide) g[0] = load8(gp + i * G * 8, n[i], vec);
+        pairs_of(g[kWide ? 0 : i], q);
+      });
+}
+
+// Many wide rows: a persistent block whose rows arrive by bulk copies in a ring of shared
+// memory, several rows ahead, so that no row's arrival is waited for and none is held in
+// registers.  Every thread has vectors i * kRingThreads + thread.
+constexpr int kRingThreads = 256;
+template <typename T, bool kFp8, int NV>
+__global__ void __launch_bounds__(kRingThreads)
+    norm_ring_kernel(const NormParams p, int slots, int slot_bytes) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ uint64_t full[16];
+  __shared__ float s_sum[2][32];     // by turns, so that one barrier a reduction is enough
+  __shared__ uint32_t s_max[2][32];
+  const int tid = threadIdx.x;
+  const int row_bytes = p.D * (int)sizeof(T);
+  const int res_at = row_bytes, gate_at = row_bytes * (p.residual ? 2 : 1);
+  int n[NV];
+  Raw8<float> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * kRingThreads + tid) * 8;
+    n[i] = p.D - c;
+    if (n[i] > 0) w[i].load(p.w + c);
+  }
+  auto fetch = [&](long long row, int s) {  // one thread: the row's copies into slot s
+    const long long token = p.heads == 1 ? row : row / p.heads;
+    const long long col = (row - token * p.heads) * p.D;
+    unsigned char* dst = ring + (long long)s * slot_bytes;
+    mbar_expect_tx(&full[s], row_bytes * (1 + (p.residual ? 1 : 0) + (p.gate ? 1 : 0)));
+    bulk_g2s(dst, static_cast<const T*>(p.x) + token * p.x_stride + col, row_bytes, &full[s]);
+    if (p.residual)
+      bulk_g2s(dst + res_at, static_cast<const T*>(p.residual) + row * p.D, row_bytes, &full[s]);
+    if (p.gate)
+      bulk_g2s(dst + gate_at, static_cast<const T*>(p.gate) + token * p.gate_stride + col, row_bytes,
+               &full[s]);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < slots; ++s) mbar_init(&full[s], 1);
+    mbar_fence_init();
+    for (int s = 0; s < slots; ++s) {
+      const long long row = blockIdx.x + (long long)s * gridDim.x;
+      if (row < p.rows) fetch(row, s);
+    }
+  }
+  __syncthreads();
+  int s = 0, turn = 0;
+  unsigned phase = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    // a copy that does not arrive within about a second ends the block's work: it is recorded,
+    // and the other copies in flight are waited for before the block leaves
+    if (!mbar_wait(&full[s], phase, p.err)) {
+      for (int k = 1; k < slots; ++k) {
+        const int t = (s + k) % slots;
+        if (row + (long long)k * gridDim.x < p.rows) mbar_wait(&full[t], t > s ? phase : phase ^ 1, p.err);
+      }
+      break;
+    }
+    const unsigned char* at = ring + (long long)s * slot_bytes + tid * 8 * (int)sizeof(T);
+    f32x2 r[NV][4], ss = 0ull;
+    Raw8<T> g[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (n[i] <= 0) continue;
+      const unsigned char* q = at + i * kRingThreads * 8 * (int)sizeof(T);
+      Raw8<T> x, res;
+      x.load(reinterpret_cast<const T*>(q));
+      if (p.residual) res.load(reinterpret_cast<const T*>(q + res_at));
+      if (p.gate) g[i].load(reinterpret_cast<const T*>(q + gate_at));
+      take(p, row * p.D + (i * kRingThreads + tid) * 8, x, res, 8, r[i], ss);
+    }
+    float s0, s1;
+    unpack2(ss, s0, s1);
+    const float sum = reduce_row<true>(s0 + s1, kRingThreads, s_sum[turn]);
+    // the reduction's barrier: every thread has read the slot
+    const long long next = row + (long long)slots * gridDim.x;
+    if (tid == 0 && next < p.rows) {
+      fence_proxy_async();
+      fetch(next, s);
+    }
+    Finish<T, kFp8, true, NV>::run(
+        p, row, true, kRingThreads, tid, r, n, sum, s_max[turn],
+        [&](int i, f32x2 (&q)[4]) { pairs_of(w[i], q); },
+        [&](int i, f32x2 (&q)[4]) { pairs_of(g[i], q); });
+    if (++s == slots) s = 0, phase ^= 1;
+  }
+}
+
+template <typename T, bool kFp8>
+cudaError_t launch_warp(const NormParams& p, cudaStream_t stream) {
+  const int nvec = (p.D + 7) / 8;
+  int G = 4;
+  while (G < nvec && G < 32) G *= 2;
+  const long long rows = 128 / G, blocks = (p.rows + rows - 1) / rows, most = 12ll * kSms;
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  if (nvec <= 32) norm_warp_kernel<T, kFp8, 1><<<grid, 128, 0, stream>>>(p, G);
+  else norm_warp_kernel<T, kFp8, 2><<<grid, 128, 0, stream>>>(p, G);
+  return cudaGetLastError();
+}
+
+template <typename T, bool kFp8>
+cudaError_t launch_block(const NormParams& p, cudaStream_t stream) {
+  // one vector a thread for few rows (latency), two for many; four for the widest
+  const int nvec = (p.D + 7) / 8;
+  const int nv = nvec > 1024 ? 4 : p.rows <= kSms ? 1 : 2;
+  const int G = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+  const unsigned grid = (unsigned)p.rows;
+  if (nv == 1) norm_block_kernel<T, kFp8, 1><<<grid, G, 0, stream>>>(p, G);
+  else if (nv == 2) norm_block_kernel<T, kFp8, 2><<<grid, G, 0, stream>>>(p, G);
+  else norm_block_kernel<T, kFp8, 4><<<grid, G, 0, stream>>>(p, G);
+  return cudaGetLastError();
+}
+
+template <typename T, bool kFp8, int NV>
+cudaError_t launch_ring(const NormParams& p, cudaStream_t stream) {
+  const int slot_bytes = p.D * (int)sizeof(T) * (1 + (p.residual ? 1 : 0) + (p.gate ? 1 : 0));
+  // two blocks an SM with four slots or more each, else one block with up to twice the memory
+  int blocks = 2, slots = 110 * 1024 / slot_bytes;
+  if (slots < 4) blocks = 1, slots = 220 * 1024 / slot_bytes;
+  if (slots > 8) slots = 8;
+  const auto kernel = norm_ring_kernel<T, kFp8, NV>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             slots * slot_bytes);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)blocks * kSms;
+  const unsigned grid = (unsigned)(p.rows < most ? p.rows : most);
+  kernel<<<grid, kRingThreads, slots * slot_bytes, stream>>>(p, slots, slot_bytes);
   return cudaGetLastError();
 }
 
 template <typename T, bool kFp8>
 cudaError_t launch_t(const NormParams& p, cudaStream_t stream) {
-  const int nvec = (p.D + 7) / 8;
-  if (nvec <= 64) {  // rows within a warp, 128 threads a block
-    int G = 4;
-    while (G < nvec && G < 32) G *= 2;
-    if (nvec <= 32) return launch_k<T, kFp8, false, 1>(p, 128, G, stream);
-    return launch_k<T, kFp8, false, 2>(p, 128, G, stream);
+  if (p.D <= 512) return launch_warp<T, kFp8>(p, stream);
+  // the ring's copies are of whole 16-byte pieces; it pays once every block has a few rows
+  if (p.vec && p.D <= 8192 && p.rows >= 8 * kSms) {
+    const int nv = (p.D / 8 + kRingThreads - 1) / kRingThreads;
+    if (nv <= 1) return launch_ring<T, kFp8, 1>(p, stream);
+    if (nv == 2) return launch_ring<T, kFp8, 2>(p, stream);
+    if (nv == 3) return launch_ring<T, kFp8, 3>(p, stream);
+    return launch_ring<T, kFp8, 4>(p, stream);
   }
-  // one vector a thread for few rows (latency), two for many; four for the widest
-  const int nv = nvec > 1024 ? 4 : p.rows <= 152 ? 1 : 2;
-  const int G = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-  if (nv == 1) return launch_k<T, kFp8, true, 1>(p, G, G, stream);
-  if (nv == 2) return launch_k<T, kFp8, true, 2>(p, G, G, stream);
-  return launch_k<T, kFp8, true, 4>(p, G, G, stream);
+  return launch_block<T, kFp8>(p, stream);
 }
 
 }  // namespace

@@ -1,81 +1,133 @@
 // s6_step.cu - one token of the S6 recurrence per sequence (the decode step of s6_scan.cuh).
 //
-// A lane takes four states of one channel for kSeqs sequences at once: reads them, writes
-// them back; the LPC lanes of a channel add their parts of y by shuffles.  The states are read
-// and written once, 128 bytes a channel at Ns = 16, and HBM bandwidth bounds it: four
-// sequences a lane keep enough reads in flight and share A (one sequence measured 2.6 TB/s);
-// few sequences take one, and launch latency is all there is.
+// The states are read and written once, 128 bytes a channel at Ns = 16: HBM bandwidth bounds
+// many sequences, launch latency few.  A lane takes four states of one channel, LPC lanes a
+// channel, and kSeqs sequences at once: that keeps enough reads in flight, shares A, and lets
+// the lanes of a channel share what is computed once per sequence and channel (the step, the
+// gate): each lane does it for its own sequence, and the parts of y are summed so that they
+// end where they are needed.
 #include "layer_common.cuh"
 #include "layer_internal.h"
 
 namespace gdn {
 namespace {
 
+constexpr int kStepThreads = 256;
+
 template <typename T, int LPC, int kSeqs>
-__global__ void __launch_bounds__(256) s6_step_kernel(const S6Params p, int per_row) {
+__global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p, int per_row) {
+  // sequences a lane prepares and finishes: kOwn from number ln * kOwn on, of the kSeqs
+  constexpr int kOwn = (kSeqs + LPC - 1) / LPC;
   const int bx = blockIdx.x % per_row;
   const int first = blockIdx.x / per_row * kSeqs;
-  const int id = bx * 256 + threadIdx.x;
+  const int id = bx * kStepThreads + threadIdx.x;
   const bool some = id / LPC < p.dim;  // lanes behind the last channel only join the shuffles
-  const int ch = some ? id / LPC : p.dim - 1, n0 = id % LPC * 4;
+  const int ch = some ? id / LPC : p.dim - 1, ln = id % LPC, n0 = ln * 4;
   const int nst = some ? max(0, min(4, p.Ns - n0)) : 0;
   const long long hrow = (long long)ch * p.Ns + n0, hsize = (long long)p.dim * p.Ns;
-  float4 h[kSeqs], b[kSeqs], c[kSeqs];
-  float x[kSeqs], d[kSeqs], z[kSeqs];
-  const float4 a = load_h(p.A + hrow, nst, p.Ns);
+  const bool all = first + kSeqs <= p.N;
+
+  float4 h[kSeqs];
+  float* hp = p.hT + first * hsize + hrow;
+#pragma unroll
+  for (int i = 0; i < kSeqs; ++i)
+    h[i] = load_h(hp + (all || first + i < p.N ? i * hsize : 0), nst, p.Ns);
+  Raw4<T> rb[kSeqs], rc[kSeqs];
+  const T* bp = static_cast<const T*>(p.B) + first * p.b_stride + n0;
+  const T* cp = static_cast<const T*>(p.C) + first * p.c_stride + n0;
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
-    const long long n = first + i < p.N ? first + i : p.N - 1;
-    h[i] = load_h(p.hT + n * hsize + hrow, nst, p.Ns);
-    x[i] = to_f32(static_cast<const T*>(p.x)[n * p.x_stride + ch]);
-    d[i] = to_f32(static_cast<const T*>(p.dt)[n * p.dt_stride + ch]);
-    z[i] = p.z ? to_f32(static_cast<const T*>(p.z)[n * p.z_stride + ch]) : 0.f;
-    Raw4<T> rb, rc;
-    rb.zero();
-    rc.zero();
+    const long long k = all || first + i < p.N ? i : 0;
+    rb[i].zero();
+    rc[i].zero();
     if (nst > 0) {
-      rb.load(static_cast<const T*>(p.B) + n * p.b_stride + n0, nst, p.vec_bc);
-      rc.load(static_cast<const T*>(p.C) + n * p.c_stride + n0, nst, p.vec_bc);
+      rb[i].load(bp + k * p.b_stride, nst, p.vec_bc);
+      rc[i].load(cp + k * p.c_stride, nst, p.vec_bc);
     }
-    b[i] = rb.get();
-    c[i] = rc.get();
   }
+  float x[kOwn], d[kOwn], z[kOwn];
+  bool mine[kOwn];
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    const int i = ln * kOwn + o;
+    mine[o] = i < kSeqs && first + i < p.N;
+    const long long n = mine[o] ? first + i : first;
+    x[o] = to_f32(static_cast<const T*>(p.x)[n * p.x_stride + ch]);
+    d[o] = to_f32(static_cast<const T*>(p.dt)[n * p.dt_stride + ch]);
+    z[o] = p.z ? to_f32(static_cast<const T*>(p.z)[n * p.z_stride + ch]) : 0.f;
+  }
+  const float4 a = load_h(p.A + hrow, nst, p.Ns);
   const float bias = p.dt_bias ? p.dt_bias[ch] : 0.f, skip = p.D ? p.D[ch] : 0.f;
+  const float a0 = a.x * kLog2e, a1 = a.y * kLog2e, a2 = a.z * kLog2e, a3 = a.w * kLog2e;
+  float u[kOwn];
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    d[o] += bias;
+    if (p.softplus) d[o] = softplus(d[o]);
+    u[o] = d[o] * x[o];
+  }
+
+  float y[kSeqs];
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
-    const int n = first + i;
-    const float dl = p.softplus ? softplus(d[i] + bias) : d[i] + bias;
-    const float u = dl * x[i];
-    float4 o;
-    o.x = fmaf(ex2(dl * (a.x * kLog2e)), h[i].x, u * b[i].x);
-    o.y = fmaf(ex2(dl * (a.y * kLog2e)), h[i].y, u * b[i].y);
-    o.z = fmaf(ex2(dl * (a.z * kLog2e)), h[i].z, u * b[i].z);
-    o.w = fmaf(ex2(dl * (a.w * kLog2e)), h[i].w, u * b[i].w);
-    if (n < p.N) store_h(p.hT + n * hsize + hrow, o, nst, p.Ns);
-    float y = 0.f;  // only of states that exist
-    if (nst > 0) y = c[i].x * o.x;
-    if (nst > 1) y = fmaf(c[i].y, o.y, y);
-    if (nst > 2) y = fmaf(c[i].z, o.z, y);
-    if (nst > 3) y = fmaf(c[i].w, o.w, y);
-#pragma unroll
-    for (int off = LPC / 2; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-    if (some && n < p.N && id % LPC == 0) {
-      if (p.D) y = fmaf(skip, x[i], y);
-      if (p.z) y *= silu(z[i]);
-      from_f32(static_cast<T*>(p.y) + (long long)n * p.dim + ch, y);
+    // the step of sequence i, from the lane that has it
+    float di = d[i % kOwn], ui = u[i % kOwn];
+    if (LPC > 1) {
+      di = __shfl_sync(0xffffffffu, di, i / kOwn, LPC);
+      ui = __shfl_sync(0xffffffffu, ui, i / kOwn, LPC);
     }
+    const float4 b = rb[i].get(), c = rc[i].get();
+    float4 o;
+    o.x = fmaf(ex2(di * a0), h[i].x, ui * b.x);
+    o.y = fmaf(ex2(di * a1), h[i].y, ui * b.y);
+    o.z = fmaf(ex2(di * a2), h[i].z, ui * b.z);
+    o.w = fmaf(ex2(di * a3), h[i].w, ui * b.w);
+    if (all || first + i < p.N) store_h(hp + i * hsize, o, nst, p.Ns);
+    y[i] = 0.f;  // only of states that exist
+    if (nst > 0) y[i] = c.x * o.x;
+    if (nst > 1) y[i] = fmaf(c.y, o.y, y[i]);
+    if (nst > 2) y[i] = fmaf(c.z, o.z, y[i]);
+    if (nst > 3) y[i] = fmaf(c.w, o.w, y[i]);
+  }
+  // Sums over the LPC lanes.  While there are several sequences a lane gives half of them away
+  // for the other half's parts, so that a lane ends with the sequences it has; else plain sums.
+#pragma unroll
+  for (int off = LPC / 2, have = kSeqs; off > 0; off >>= 1) {
+    if (have > 1 && off < kSeqs) {
+      have /= 2;
+      const bool up = ln & off;
+#pragma unroll
+      for (int i = 0; i < kSeqs / 2; ++i) {
+        if (i >= have) break;
+        const float send = up ? y[i] : y[i + have], keep = up ? y[i + have] : y[i];
+        y[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kSeqs; ++i)
+        if (i < have) y[i] += __shfl_xor_sync(0xffffffffu, y[i], off);
+    }
+  }
+#pragma unroll
+  for (int o = 0; o < kOwn; ++o) {
+    if (!some || !mine[o]) continue;
+    float v = y[o];
+    if (p.D) v = fmaf(skip, x[o], v);
+    if (p.z) v *= silu(z[o]);
+    const long long n = first + ln * kOwn + o;
+    from_f32(static_cast<T*>(p.y) + n * p.dim + ch, v);
   }
 }
 
 template <typename T, int LPC>
 cudaError_t launch_step_l(const S6Params& p, cudaStream_t stream) {
-  const int per_row = (int)(((long long)p.dim * LPC + 255) / 256);
+  const int per_row = (int)(((long long)p.dim * LPC + kStepThreads - 1) / kStepThreads);
+  const auto blocks = [&](int seqs) { return (long long)per_row * ((p.N + seqs - 1) / seqs); };
   // four sequences a lane once that still leaves two blocks per SM
-  if ((long long)per_row * p.N >= 8 * kSms)
-    s6_step_kernel<T, LPC, 4>
-        <<<(unsigned)((long long)per_row * ((p.N + 3) / 4)), 256, 0, stream>>>(p, per_row);
+  if (blocks(4) >= 2 * kSms)
+    s6_step_kernel<T, LPC, 4><<<(unsigned)blocks(4), kStepThreads, 0, stream>>>(p, per_row);
   else
-    s6_step_kernel<T, LPC, 1><<<(unsigned)((long long)per_row * p.N), 256, 0, stream>>>(p, per_row);
+    s6_step_kernel<T, LPC, 1><<<(unsigned)blocks(1), kStepThreads, 0, stream>>>(p, per_row);
   return cudaGetLastError();
 }
 

@@ -10,16 +10,21 @@
 // HBM bandwidth bounds it: 2 bytes in and 2 out per element against ~8 instructions.  A
 // thread has 4 channels (8 bytes of bf16) and walks a run of tokens with the window in
 // registers as packed fp32 pairs, so that each input is loaded once except for the W - 1 rows
-// before a run; four tokens are loaded while the four before them are computed.
+// before a run.  Its own inputs come by cp.async through a private ring of shared memory, three
+// rounds of four tokens ahead: what is in flight then costs no registers (loads ahead in
+// registers, one round: 22.4 us at 4096 x 6144 where the ring takes CONV_RING).  Rows off
+// 4-channel pieces are loaded element by element, one round ahead.
+#include "gdn_common.cuh"
 #include "layer_common.cuh"
 #include "layer_internal.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kVec = 4;       // channels per thread
+constexpr int kVec4 = 4;      // channels per thread
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;     // tokens whose loads are in flight together
+constexpr int kAhead = 4;     // tokens of a round
+constexpr int kRounds = 4;    // rounds of the ring
 
 // Four channels of a row in fp32.
 struct Four {
@@ -35,8 +40,8 @@ __device__ __forceinline__ Four four(const Raw4<T>& r) {
 // floats are whole 16-byte pieces.
 template <int W>
 __device__ __forceinline__ void load_filter(const float* w, int c, int n, Four (&f)[W]) {
-  float v[kVec * W];
-  if (n >= kVec) {
+  float v[kVec4 * W];
+  if (n >= kVec4) {
     const float4* p = reinterpret_cast<const float4*>(w + (long long)c * W);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
@@ -45,15 +50,15 @@ __device__ __forceinline__ void load_filter(const float* w, int c, int n, Four (
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec * W; ++i) v[i] = i / W < n ? w[(long long)c * W + i] : 0.f;
+    for (int i = 0; i < kVec4 * W; ++i) v[i] = i / W < n ? w[(long long)c * W + i] : 0.f;
   }
 #pragma unroll
   for (int j = 0; j < W; ++j) f[j] = {pack2(v[j], v[W + j]), pack2(v[2 * W + j], v[3 * W + j])};
 }
 __device__ __forceinline__ Four load_bias(const float* bias, int c, int n) {
-  float b[kVec];
+  float b[kVec4];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) b[i] = bias && i < n ? bias[c + i] : 0.f;
+  for (int i = 0; i < kVec4; ++i) b[i] = bias && i < n ? bias[c + i] : 0.f;
   return {pack2(b[0], b[1]), pack2(b[2], b[3])};
 }
 // act(bias + sum of taps), rounded
@@ -118,15 +123,24 @@ __device__ __forceinline__ void write_state(const ConvParams& p, int n, int c, i
     r[j].store(static_cast<T*>(p.sT) + ((long long)n * (W - 1) + j) * p.D + c, left, vec);
 }
 
-// blockIdx.x: run of `run` tokens, then (with `states`) one sequence's state each;
-// blockIdx.y: 128 threads of 4 channels.
-template <typename T, int W>
+// cp.async of one thread's four channels
+__device__ __forceinline__ void copy_four(Raw4<__nv_bfloat16>* dst, const __nv_bfloat16* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_four(Raw4<float>* dst, const float* src) {
+  cp_async16(dst, src, true);
+}
+
+// blockIdx.x: run of `run` tokens, then (with sT) one sequence's state each; blockIdx.y: 128
+// threads of 4 channels.  kVec: whole aligned pieces.
+template <typename T, int W, bool kVec>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int run, int runs,
                                                         long long tokens) {
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec;
+  __shared__ __align__(16) unsigned char s_ring[kVec ? kRounds * kAhead * kThreads * sizeof(Raw4<T>) : 16];
+  const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec4;
   if (c >= p.D) return;
   const int left = p.D - c;
-  const bool vec = p.vec;
+  constexpr bool vec = kVec;
   if ((int)blockIdx.x >= runs) {
     write_state<T, W>(p, blockIdx.x - runs, c, left, vec);
     return;
@@ -134,10 +148,25 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   const long long t0 = (long long)blockIdx.x * run, t1 = min(t0 + run, tokens);
   const T* x = static_cast<const T*>(p.x) + t0 * p.x_stride + c;
   T* y = static_cast<T*>(p.y) + t0 * p.D + c;
-  Raw4<T> ahead[kAhead];  // the tokens of the next round
+  Raw4<T> ahead[kVec ? 1 : kAhead];  // the tokens of the next round
+  Raw4<T>* ring = reinterpret_cast<Raw4<T>*>(s_ring) + threadIdx.x;
+  const int len = (int)(t1 - t0);
+  auto request = [&](int round) {  // this thread's inputs of a round, x at its first token
+    if constexpr (kVec) {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (t0 + u < t1) ahead[u].load(x + u * p.x_stride, left, vec);
+      for (int u = 0; u < kAhead; ++u)
+        if (round * kAhead + u < len)
+          copy_four(ring + (round % kRounds * kAhead + u) * kThreads, x + u * p.x_stride);
+      cp_async_commit();
+    } else {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (round * kAhead + u < len) ahead[u].load(x + u * p.x_stride, left, false);
+    }
+    x += kAhead * p.x_stride;
+  };
+#pragma unroll
+  for (int round = 0; round < (kVec ? kRounds - 1 : 1); ++round) request(round);
 
   // the sequence of token t0: the first one that ends behind it
   int n = 0;
@@ -161,14 +190,19 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   for (int j = 0; j < W - 1; ++j)
     win[j] = four(tap<T, W>(p, s, n, max(t0, s.begin) - (W - 1) + j, c, left, vec));
 
-  for (long long t = t0; t < t1; t += kAhead) {
+  int round = 0;
+  for (long long t = t0; t < t1; t += kAhead, ++round) {
     Raw4<T> raw[kAhead];
+    if constexpr (kVec) {
+      request(round + kRounds - 1);
+      cp_async_wait<kRounds - 1>();
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
-    x += kAhead * p.x_stride;
+      for (int u = 0; u < kAhead; ++u) raw[u] = ring[(round % kRounds * kAhead + u) * kThreads];
+    } else {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (t + kAhead + u < t1) ahead[u].load(x + u * p.x_stride, left, vec);
+      for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
+      request(round + 1);
+    }
     if (t >= s.begin && t + kAhead <= min(t1, s.end)) {  // one sequence's tokens
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -206,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
 // of conv_kernel may still read it), or a batch without tokens.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_state_kernel(const ConvParams p) {
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec;
+  const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec4;
   if (c < p.D) write_state<T, W>(p, blockIdx.x, c, p.D - c, p.vec);
 }
 
@@ -218,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p,
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const long long first = id / per_row * kSeqs;
   if (first >= p.N) return;
-  const int c = (int)(id % per_row) * kVec;
+  const int c = (int)(id % per_row) * kVec4;
   const int left = p.D - c;
   const bool vec = p.vec;
   Raw4<T> r[kSeqs][W];
@@ -250,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p,
 template <typename T, int W>
 cudaError_t launch_w(const ConvParams& p, cudaStream_t stream) {
   const long long tokens = p.cu ? (long long)p.T : (long long)p.N * p.T;
-  const int per_row = (p.D + kVec - 1) / kVec;
+  const int per_row = (p.D + kVec4 - 1) / kVec4;
   const unsigned by = (per_row + kThreads - 1) / kThreads;
   // long runs repeat fewer rows (W - 1 each), short ones fill the GPU: 8 blocks per SM
   int run = 64;
@@ -260,7 +294,9 @@ cudaError_t launch_w(const ConvParams& p, cudaStream_t stream) {
   const bool apart = p.sT && (p.s0 == p.sT || tokens == 0);
   const long long bx = runs + (p.sT && !apart ? p.N : 0);
   if (tokens > 0) {
-    conv_kernel<T, W><<<dim3((unsigned)bx, by), kThreads, 0, stream>>>(p, run, (int)runs, tokens);
+    const dim3 grid((unsigned)bx, by);
+    if (p.vec) conv_kernel<T, W, true><<<grid, kThreads, 0, stream>>>(p, run, (int)runs, tokens);
+    else conv_kernel<T, W, false><<<grid, kThreads, 0, stream>>>(p, run, (int)runs, tokens);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -278,7 +314,7 @@ cudaError_t launch_t(const ConvParams& p, cudaStream_t stream) {
 
 template <typename T, int W>
 cudaError_t launch_step_w(const ConvParams& p, cudaStream_t stream) {
-  const int per_row = (p.D + kVec - 1) / kVec;
+  const int per_row = (p.D + kVec4 - 1) / kVec4;
   const auto blocks = [&](int seqs) {
     return (unsigned)(((long long)((p.N + seqs - 1) / seqs) * per_row + kThreads - 1) / kThreads);
   };
