@@ -275,6 +275,8 @@ gdn_status run_norm(const void* x, const float* w, const void* residual, const v
   p.residual_out = residual_out; p.scales = scales;
   p.rows = rows; p.x_stride = x_stride; p.gate_stride = gate_stride;
   p.heads = heads; p.D = D; p.eps = eps;
+  p.inv_d = 1.f / (float)D;
+  p.group_log = group == 32 ? 5 : group == 64 ? 6 : 7;
   p.group = span < D ? span : D;
   p.groups = (D + p.group - 1) / p.group;
   const bool one = tokens <= 1;

@@ -76,7 +76,8 @@ struct NormParams {
   long long x_stride, gate_stride;  // elements from token to token
   int heads, D;
   int group, groups;                // columns per scale (D: one scale a row), scales a row
-  float eps;
+  int group_log;                    // log2 of a group below D
+  float eps, inv_d;                 // inv_d: 1 / D
   int vec;                          // every 8-column access is aligned and D is a multiple of 8
   unsigned* err;                    // device error word: bounded waits record a timeout here
 };

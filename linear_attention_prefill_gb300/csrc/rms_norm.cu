@@ -17,12 +17,19 @@
 namespace gdn {
 namespace {
 
-// max |a|, |b| as bit patterns: those of NaN are above those of infinity, so NaN wins
-__device__ __forceinline__ uint32_t abs_bits(float a) { return __float_as_uint(a) & 0x7fffffffu; }
-__device__ __forceinline__ uint32_t max_bits(f32x2 v) {
-  float a, b;
-  unpack2(v, a, b);
-  return max(abs_bits(a), abs_bits(b));
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_abs(const f32x2 (&v)[4]) {
+  float a[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack2(v[j], a[2 * j], a[2 * j + 1]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) a[j] = fabsf(a[j]);
+  return max_nan(max_nan(max_nan(a[0], a[1]), max_nan(a[2], a[3])),
+                 max_nan(max_nan(a[4], a[5]), max_nan(a[6], a[7])));
 }
 
 // Two e4m3, saturating.
@@ -48,105 +55,103 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, const f32x2 (&y)[4], floa
   }
 }
 // max|y| -> scale; the reciprocal and the product by 1 / 448 are within an ulp each
-__device__ __forceinline__ float scale_of(uint32_t amax) {
-  const float m = __uint_as_float(amax);
+__device__ __forceinline__ float scale_of(float m) {
   return m == 0.f ? 1.f : m < 5.2666e-36f ? 1.17549435e-38f : m * (1.f / 448.f);
 }
 
-template <typename V>
-__device__ __forceinline__ V combine(V a, V b);
-template <>
-__device__ __forceinline__ float combine(float a, float b) { return a + b; }
-template <>
-__device__ __forceinline__ uint32_t combine(uint32_t a, uint32_t b) { return max(a, b); }
-// Sum (of floats) or maximum (of bit patterns) over the G threads of a row: G <= 32 lanes of a
-// warp, or the whole block.
-template <bool kBlock, typename V>
-__device__ __forceinline__ V reduce_row(V v, int G, V* s) {
-  const int lanes = kBlock ? 32 : G;
-  for (int off = lanes >> 1; off > 0; off >>= 1)
-    v = combine<V>(v, __shfl_xor_sync(0xffffffffu, v, off));
-  if (!kBlock) return v;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s[0];
-  for (int i = 1; i < warps; ++i) v = combine<V>(v, s[i]);
+// Sum or maximum over the G threads of a row: G <= 32 lanes of a warp, or the whole block.
+template <bool kMax>
+__device__ __forceinline__ float combine(float a, float b) {
+  return kMax ? max_nan(a, b) : a + b;
+}
+template <bool kMax, bool kBlock>
+__device__ __forceinline__ float reduce_row(float v, int G, float* s) {
+  if (kBlock) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, off));
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int warps = blockDim.x >> 5;  // every warp adds the warps' results
+    v = (threadIdx.x & 31) < warps ? s[threadIdx.x & 31] : 0.f;
+    for (int off = warps > 16 ? 16 : warps > 8 ? 8 : warps > 4 ? 4 : 2; off > 0; off >>= 1)
+      v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return __shfl_sync(0xffffffffu, v, 0);
+  }
+  for (int off = G >> 1; off > 0; off >>= 1)
+    v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
 }
 
-// What a row is after its sum of squares is known: y of every vector, stored.
-template <typename T, bool kFp8, bool kBlock, int NV>
-struct Finish {
-  // r: the row's vectors; load_w(i), load_gate(i): vector i of w and of the gate; n[i]: columns
-  // that exist (whole vectors with p.vec); some: there is a row
-  template <typename W, typename G_>
-  static __device__ __forceinline__ void run(const NormParams& p, long long row, bool some, int G,
-                                             int lane, f32x2 (&r)[NV][4], const int (&n)[NV],
-                                             float ss, uint32_t* s_max, W load_w, G_ load_gate) {
-    const bool vec = p.vec;
-    const f32x2 rstd = dup2(rsqrtf(ss / (float)p.D + p.eps));
-    uint32_t amax = 0u;
+// What a row is after its sum of squares is known: y of every vector, stored.  r: the row's
+// vectors; load_w(i), load_gate(i): vector i of w and of the gate; n[i]: columns that exist
+// (whole vectors with p.vec); some: there is a row.
+template <typename T, bool kFp8, bool kBlock, int NV, typename LoadW, typename LoadGate>
+__device__ __forceinline__ void finish(const NormParams& p, long long row, bool some, int G,
+                                       int lane, f32x2 (&r)[NV][4], const int (&n)[NV], float ss,
+                                       float* s_max, LoadW load_w, LoadGate load_gate) {
+  const bool vec = p.vec;
+  const f32x2 rstd = dup2(rsqrtf(ss * p.inv_d + p.eps));
+  const long long at = row * p.D + lane * 8;
+  T* y = static_cast<T*>(p.y) + at;
+  uint8_t* y8 = static_cast<uint8_t*>(p.y) + at;
+  float* scales = p.scales + row * p.groups;
+  float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * G + lane) * 8;
-      const bool here = some && n[i] > 0;
-      if (here) {
-        f32x2 q[4];
-        load_w(i, q);
+  for (int i = 0; i < NV; ++i) {
+    const bool here = some && n[i] > 0;
+    if (here) {
+      f32x2 q[4];
+      load_w(i, q);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[i][j] = mul2(mul2(r[i][j], rstd), q[j]);
-        if (p.gate) {
-          load_gate(i, q);
+      for (int j = 0; j < 4; ++j) r[i][j] = mul2(mul2(r[i][j], rstd), q[j]);
+      if (p.gate) {
+        load_gate(i, q);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) r[i][j] = mul2(r[i][j], silu2(q[j]));
-        }
-        if (!kFp8)
-          store8(static_cast<T*>(p.y) + row * p.D + c, raw_of<T>(r[i]), n[i], vec);
+        for (int j = 0; j < 4; ++j) r[i][j] = mul2(r[i][j], silu2(q[j]));
       }
-      if (kFp8) {
-        uint32_t m = 0u;
-        if (here) {
-          if (!vec) {  // columns that do not exist were read as zeros, but a row of NaN has none
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float a, b;
-              unpack2(r[i][j], a, b);
-              r[i][j] = pack2(2 * j < n[i] ? a : 0.f, 2 * j + 1 < n[i] ? b : 0.f);
-            }
-          }
-          m = max(max(max_bits(r[i][0]), max_bits(r[i][1])),
-                  max(max_bits(r[i][2]), max_bits(r[i][3])));
-        }
-        if (p.group < p.D) {  // the lanes of the group: group / 8 neighbours
-          for (int off = p.group >> 4; off > 0; off >>= 1)
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-          if (here) {
-            const float scale = scale_of(m);
-            store_e4m3(static_cast<uint8_t*>(p.y) + row * p.D + c, r[i], rcp(scale), n[i], vec);
-            if ((c & (p.group - 1)) == 0) p.scales[row * p.groups + c / p.group] = scale;
-          }
-        } else {
-          amax = max(amax, m);
-        }
-      }
+      if (!kFp8) store8(y + i * G * 8, raw_of<T>(r[i]), n[i], vec);
     }
-    if (kFp8 && p.group >= p.D) {  // one scale a row
-      amax = reduce_row<kBlock>(amax, G, s_max);
-      const float scale = scale_of(amax), inv = rcp(scale);
-      if (some && lane == 0) p.scales[row] = scale;
+    if (kFp8) {
+      float m = 0.f;
+      if (here) {
+        if (!vec) {  // columns that do not exist were read as zeros, but a row of NaN has none
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (some && n[i] > 0)
-          store_e4m3(static_cast<uint8_t*>(p.y) + row * p.D + (i * G + lane) * 8, r[i], inv, n[i],
-                     vec);
+          for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpack2(r[i][j], a, b);
+            r[i][j] = pack2(2 * j < n[i] ? a : 0.f, 2 * j + 1 < n[i] ? b : 0.f);
+          }
+        }
+        m = max_abs(r[i]);
+      }
+      if (p.group < p.D) {  // the lanes of the group: group / 8 neighbours
+        for (int off = p.group >> 4; off > 0; off >>= 1)
+          m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (here) {
+          const float scale = scale_of(m);
+          store_e4m3(y8 + i * G * 8, r[i], rcp(scale), n[i], vec);
+          const int c = (i * G + lane) * 8;
+          if ((c & (p.group - 1)) == 0) scales[c >> p.group_log] = scale;
+        }
+      } else {
+        amax = max_nan(amax, m);
+      }
     }
   }
-};
+  if (kFp8 && p.group >= p.D) {  // one scale a row
+    amax = reduce_row<true, kBlock>(amax, G, s_max);
+    const float scale = scale_of(amax), inv = rcp(scale);
+    if (some && lane == 0) *scales = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (some && n[i] > 0) store_e4m3(y8 + i * G * 8, r[i], inv, n[i], vec);
+  }
+}
 
 // x + residual of one vector, the residual's update stored; adds the squares to ss.
 template <typename T>
-__device__ __forceinline__ void take(const NormParams& p, long long at, const Raw8<T>& x,
+__device__ __forceinline__ void take(const NormParams& p, T* out, const Raw8<T>& x,
                                      const Raw8<T>& res, int n, f32x2 (&r)[4], f32x2& ss) {
   pairs_of(x, r);
   if (p.residual) {
@@ -154,7 +159,7 @@ __device__ __forceinline__ void take(const NormParams& p, long long at, const Ra
     pairs_of(res, q);
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = add2(r[j], q[j]);
-    store8(static_cast<T*>(p.residual_out) + at, raw_of<T>(r), n, p.vec);
+    store8(out, raw_of<T>(r), n, p.vec);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) ss = fma2(r[j], r[j], ss);
@@ -177,40 +182,51 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p, int 
     if (n[i] > 0) pairs_of(load8(p.w + c, n[i], vec), w[i]);
   }
   Raw8<T> x[NV], res[NV], gate[NV];
+  const long long row0 = (long long)blockIdx.x * per_block + threadIdx.x / G;
+  const T* xp = static_cast<const T*>(p.x) + lane * 8;
+  const T* gp = static_cast<const T*>(p.gate) + lane * 8;
+  const T* rp = static_cast<const T*>(p.residual) + row0 * p.D + lane * 8;
+  const bool heads = p.heads > 1;  // else a row's place moves on by a constant
+  if (!heads) xp += row0 * p.x_stride, gp += row0 * p.gate_stride;
   auto load_row = [&](long long row) {
-    const long long token = p.heads == 1 ? row : row / p.heads;
-    const long long col = (row - token * p.heads) * p.D + lane * 8;
+    const T *xr = xp, *gr = gp;
+    if (heads) {
+      const long long token = row / p.heads, col = (row - token * p.heads) * p.D;
+      xr += token * p.x_stride + col;
+      gr += token * p.gate_stride + col;
+    } else {
+      xp += step * p.x_stride;
+      gp += step * p.gate_stride;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (n[i] <= 0) continue;
-      x[i] = load8(static_cast<const T*>(p.x) + token * p.x_stride + col + i * G * 8, n[i], vec);
-      if (p.residual)
-        res[i] = load8(static_cast<const T*>(p.residual) + row * p.D + (i * G + lane) * 8, n[i], vec);
-      if (p.gate)
-        gate[i] = load8(static_cast<const T*>(p.gate) + token * p.gate_stride + col + i * G * 8, n[i],
-                        vec);
+      x[i] = load8(xr + i * G * 8, n[i], vec);
+      if (p.residual) res[i] = load8(rp + i * G * 8, n[i], vec);
+      if (p.gate) gate[i] = load8(gr + i * G * 8, n[i], vec);
     }
+    rp += step * p.D;
   };
-  const long long row0 = (long long)blockIdx.x * per_block + threadIdx.x / G;
   if (row0 < p.rows) load_row(row0);
   // every lane of a warp stays for the shuffles
   for (long long base = (long long)blockIdx.x * per_block; base < p.rows; base += step) {
     const long long row = base + threadIdx.x / G;
     const bool some = row < p.rows;
+    T* out = static_cast<T*>(p.residual_out) + row * p.D + lane * 8;
     f32x2 r[NV][4], ss = 0ull;
     Raw8<T> g[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (some && n[i] > 0) {
-        take(p, row * p.D + (i * G + lane) * 8, x[i], res[i], n[i], r[i], ss);
+        take(p, out + i * G * 8, x[i], res[i], n[i], r[i], ss);
         g[i] = gate[i];
       }
     }
     if (row + step < p.rows) load_row(row + step);
     float s0, s1;
     unpack2(ss, s0, s1);
-    const float sum = reduce_row<false>(s0 + s1, G, (float*)nullptr);
-    Finish<T, kFp8, false, NV>::run(
+    const float sum = reduce_row<false, false>(s0 + s1, G, nullptr);
+    finish<T, kFp8, false, NV>(
         p, row, some, G, lane, r, n, sum, nullptr,
         [&](int i, f32x2 (&q)[4]) {
 #pragma unroll
@@ -226,8 +242,7 @@ template <typename T, bool kFp8, int NV>
 __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
     norm_block_kernel(const NormParams p, int G) {
   constexpr bool kWide = NV == 4;
-  __shared__ float s_sum[32];
-  __shared__ uint32_t s_max[32];
+  __shared__ float s_sum[32], s_max[32];
   const int lane = threadIdx.x;
   const bool vec = p.vec;
   const long long row = blockIdx.x;
@@ -257,11 +272,13 @@ __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
   f32x2 r[NV][4], ss = 0ull;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (n[i] > 0) take(p, row * p.D + (i * G + lane) * 8, x[i], res[i], n[i], r[i], ss);
+    if (n[i] > 0)
+      take(p, static_cast<T*>(p.residual_out) + row * p.D + (i * G + lane) * 8, x[i], res[i], n[i],
+           r[i], ss);
   float s0, s1;
   unpack2(ss, s0, s1);
-  const float sum = reduce_row<true>(s0 + s1, G, s_sum);
-  Finish<T, kFp8, true, NV>::run(
+  const float sum = reduce_row<false, true>(s0 + s1, G, s_sum);
+  finish<T, kFp8, true, NV>(
       p, row, true, G, lane, r, n, sum, s_max,
       [&](int i, f32x2 (&q)[4]) {
         if (kWide) w[0] = load8(p.w + (i * G + lane) * 8, n[i], vec);
@@ -275,15 +292,14 @@ __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
 
 // Many wide rows: a persistent block whose rows arrive by bulk copies in a ring of shared
 // memory, several rows ahead, so that no row's arrival is waited for and none is held in
-// registers.  Every thread has vectors i * kRingThreads + thread.
-constexpr int kRingThreads = 256;
+// registers.  G threads have vectors i * G + thread.
+constexpr int kRingThreads = 384;
 template <typename T, bool kFp8, int NV>
 __global__ void __launch_bounds__(kRingThreads)
-    norm_ring_kernel(const NormParams p, int slots, int slot_bytes) {
+    norm_ring_kernel(const NormParams p, int G, int slots, int slot_bytes) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ uint64_t full[16];
-  __shared__ float s_sum[2][32];     // by turns, so that one barrier a reduction is enough
-  __shared__ uint32_t s_max[2][32];
+  __shared__ float s_sum[2][32], s_max[2][32];  // by turns: one barrier a reduction is enough
   const int tid = threadIdx.x;
   const int row_bytes = p.D * (int)sizeof(T);
   const int res_at = row_bytes, gate_at = row_bytes * (p.residual ? 2 : 1);
@@ -291,15 +307,15 @@ __global__ void __launch_bounds__(kRingThreads)
   Raw8<float> w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * kRingThreads + tid) * 8;
+    const int c = (i * G + tid) * 8;
     n[i] = p.D - c;
     if (n[i] > 0) w[i].load(p.w + c);
   }
   auto fetch = [&](long long row, int s) {  // one thread: the row's copies into slot s
     const long long token = p.heads == 1 ? row : row / p.heads;
     const long long col = (row - token * p.heads) * p.D;
-    unsigned char* dst = ring + (long long)s * slot_bytes;
-    mbar_expect_tx(&full[s], row_bytes * (1 + (p.residual ? 1 : 0) + (p.gate ? 1 : 0)));
+    unsigned char* dst = ring + s * slot_bytes;
+    mbar_expect_tx(&full[s], slot_bytes);
     bulk_g2s(dst, static_cast<const T*>(p.x) + token * p.x_stride + col, row_bytes, &full[s]);
     if (p.residual)
       bulk_g2s(dst + res_at, static_cast<const T*>(p.residual) + row * p.D, row_bytes, &full[s]);
@@ -328,30 +344,31 @@ __global__ void __launch_bounds__(kRingThreads)
       }
       break;
     }
-    const unsigned char* at = ring + (long long)s * slot_bytes + tid * 8 * (int)sizeof(T);
+    const T* at = reinterpret_cast<const T*>(ring + s * slot_bytes) + tid * 8;
+    T* out = static_cast<T*>(p.residual_out) + row * p.D + tid * 8;
     f32x2 r[NV][4], ss = 0ull;
     Raw8<T> g[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (n[i] <= 0) continue;
-      const unsigned char* q = at + i * kRingThreads * 8 * (int)sizeof(T);
+      const T* q = at + i * G * 8;
       Raw8<T> x, res;
-      x.load(reinterpret_cast<const T*>(q));
-      if (p.residual) res.load(reinterpret_cast<const T*>(q + res_at));
-      if (p.gate) g[i].load(reinterpret_cast<const T*>(q + gate_at));
-      take(p, row * p.D + (i * kRingThreads + tid) * 8, x, res, 8, r[i], ss);
+      x.load(q);
+      if (p.residual) res.load(q + p.D);
+      if (p.gate) g[i].load(q + (p.residual ? 2 : 1) * p.D);
+      take(p, out + i * G * 8, x, res, 8, r[i], ss);
     }
     float s0, s1;
     unpack2(ss, s0, s1);
-    const float sum = reduce_row<true>(s0 + s1, kRingThreads, s_sum[turn]);
+    const float sum = reduce_row<false, true>(s0 + s1, G, s_sum[turn]);
     // the reduction's barrier: every thread has read the slot
     const long long next = row + (long long)slots * gridDim.x;
     if (tid == 0 && next < p.rows) {
       fence_proxy_async();
       fetch(next, s);
     }
-    Finish<T, kFp8, true, NV>::run(
-        p, row, true, kRingThreads, tid, r, n, sum, s_max[turn],
+    finish<T, kFp8, true, NV>(
+        p, row, true, G, tid, r, n, sum, s_max[turn],
         [&](int i, f32x2 (&q)[4]) { pairs_of(w[i], q); },
         [&](int i, f32x2 (&q)[4]) { pairs_of(g[i], q); });
     if (++s == slots) s = 0, phase ^= 1;
@@ -396,7 +413,8 @@ cudaError_t launch_ring(const NormParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long long most = (long long)blocks * kSms;
   const unsigned grid = (unsigned)(p.rows < most ? p.rows : most);
-  kernel<<<grid, kRingThreads, slots * slot_bytes, stream>>>(p, slots, slot_bytes);
+  const int G = ((p.D / 8 + NV - 1) / NV + 31) / 32 * 32;
+  kernel<<<grid, G, slots * slot_bytes, stream>>>(p, G, slots, slot_bytes);
   return cudaGetLastError();
 }
 
@@ -408,8 +426,7 @@ cudaError_t launch_t(const NormParams& p, cudaStream_t stream) {
     const int nv = (p.D / 8 + kRingThreads - 1) / kRingThreads;
     if (nv <= 1) return launch_ring<T, kFp8, 1>(p, stream);
     if (nv == 2) return launch_ring<T, kFp8, 2>(p, stream);
-    if (nv == 3) return launch_ring<T, kFp8, 3>(p, stream);
-    return launch_ring<T, kFp8, 4>(p, stream);
+    return launch_ring<T, kFp8, 3>(p, stream);
   }
   return launch_block<T, kFp8>(p, stream);
 }
