@@ -10,19 +10,21 @@ S6Split s6_split(int N, int T, int dim, int Ns, bool packed) {
   const long long ctas = (long long)N * tiles;
   const long long per_seq = (packed ? (long long)T : (long long)N * T) / N;  // packed: their mean
   const long long waves = (ctas + kSms - 1) / kSms;
-  // Cycles, in 32-channel tokens an SM (measured at Ns = 16): 60 for one CTA alone on it, 52
-  // each for several, 80 for the two passes of a split channel, 170 a token for the two passes
-  // of one chunk, and about 10000 for the summaries' launch and the chunks' beginnings.
+  // Cycles an SM takes for a token of 32 channels (measured at Ns = 16, bf16): 70 with one CTA,
+  // 116 with two, 190 with four; 74 for the two passes of a split channel, with four CTAs an SM;
+  // 170 for the two passes along one chunk, and about 10000 for the summaries' launch and the
+  // chunks' beginnings.
+  const auto cost = [](long long ctas_an_sm) { return 48 * ctas_an_sm + 22; };
   const auto chunk_of = [&](long long parts) {
     parts = parts < 2 ? 2 : parts > 32 ? 32 : parts;
     const long long c = (per_seq + parts - 1) / parts;
     return (c < 128 ? 128 : (c + 15) / 16 * 16);
   };
   const auto cost_split = [&](long long tiles_split, long long chunk) {
-    const long long work = tiles_split * per_seq * 80 / kSms, chain = chunk * 170;
+    const long long work = tiles_split * per_seq * 74 / kSms, chain = chunk * 170;
     return (work > chain ? work : chain) + 10000;
   };
-  const long long none = per_seq * (waves == 1 ? 60 : 52 * waves);
+  const long long none = per_seq * cost(waves);
   // every channel split, into enough chunks for four rounds of two CTAs an SM; or whole waves of
   // CTAs and the tiles beyond them split, one more CTA an SM beside the whole ones
   const long long chunk_all = chunk_of(8 * kSms / ctas);
@@ -32,7 +34,7 @@ S6Split s6_split(int N, int T, int dim, int Ns, bool packed) {
   const long long rest = ctas - (long long)N * full;
   const bool can = full > 0 && rest > 0;
   const long long chunk_rest = can ? chunk_of(kSms / rest) : 0;
-  const long long some = can ? per_seq * (rounds == 1 ? 60 : 52 * rounds) + cost_split(rest, 0) : 0;
+  const long long some = can ? per_seq * cost(rounds) + cost_split(rest, 0) : 0;
   s.lone = waves == 1 ? 1 : 0;
   if (none <= all && (!can || none <= some)) return s;
   const bool part = can && some < all;

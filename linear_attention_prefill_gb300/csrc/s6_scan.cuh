@@ -236,8 +236,7 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
   const int off = p.whole * kCh, wdim = p.dim - off;
   const long long wsize = (long long)wdim * p.Ns;
 
-  float a[kWidth][4];
-  f32x2 h[kWidth][2];
+  f32x2 a[kWidth][2], h[kWidth][2];
   const bool kept = k.split && p.ws_h0;  // hT == h0: the scan reads the copy
   if (!kSummary && (k.c > 0 || kept)) griddep_wait();
 #pragma unroll
@@ -246,7 +245,8 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
     const long long hrow = (long long)(ch + j) * p.Ns + n0, wrow = hrow - (long long)off * p.Ns;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n > 0) v = load_h(p.A + hrow, n, p.Ns);
-    a[j][0] = v.x * kLog2e, a[j][1] = v.y * kLog2e, a[j][2] = v.z * kLog2e, a[j][3] = v.w * kLog2e;
+    a[j][0] = pack2(v.x * kLog2e, v.y * kLog2e);
+    a[j][1] = pack2(v.z * kLog2e, v.w * kLog2e);
     h[j][0] = h[j][1] = pack2(0.f, 0.f);
     if (n > 0 && k.c == 0) {
       if (p.h0) {
@@ -261,9 +261,12 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
 #pragma unroll 4
       for (int i = 0; i < k.c; ++i) {
         v = load_h(p.ws_h + (s0 + i) * wsize + wrow, n, p.Ns);
-        const float s = p.ws_sum[(s0 + i) * wdim + ch + j - off];
-        h[j][0] = fma2(pack2(ex2(a[j][0] * s), ex2(a[j][1] * s)), h[j][0], pack2(v.x, v.y));
-        h[j][1] = fma2(pack2(ex2(a[j][2] * s), ex2(a[j][3] * s)), h[j][1], pack2(v.z, v.w));
+        const f32x2 s = dup2(p.ws_sum[(s0 + i) * wdim + ch + j - off]);
+        float e0, e1, e2, e3;
+        unpack2(mul2(a[j][0], s), e0, e1);
+        unpack2(mul2(a[j][1], s), e2, e3);
+        h[j][0] = fma2(pack2(ex2(e0), ex2(e1)), h[j][0], pack2(v.x, v.y));
+        h[j][1] = fma2(pack2(ex2(e2), ex2(e3)), h[j][1], pack2(v.z, v.w));
       }
     }
   }
@@ -319,11 +322,14 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
         Ready r;
 #pragma unroll
         for (int j = 0; j < kWidth; ++j) {
-          const float d = in.d[j], u = in.u[j];
-          r.a[j][0] = pack2(ex2(a[j][0] * d), ex2(a[j][1] * d));
-          r.a[j][1] = pack2(ex2(a[j][2] * d), ex2(a[j][3] * d));
-          r.u[j][0] = pack2(in.b.x * u, in.b.y * u);
-          r.u[j][1] = pack2(in.b.z * u, in.b.w * u);
+          const f32x2 d = dup2(in.d[j]), u = dup2(in.u[j]);
+          float e0, e1, e2, e3;
+          unpack2(mul2(a[j][0], d), e0, e1);
+          unpack2(mul2(a[j][1], d), e2, e3);
+          r.a[j][0] = pack2(ex2(e0), ex2(e1));
+          r.a[j][1] = pack2(ex2(e2), ex2(e3));
+          r.u[j][0] = mul2(pack2(in.b.x, in.b.y), u);
+          r.u[j][1] = mul2(pack2(in.b.z, in.b.w), u);
         }
         if (!kSummary) r.c01 = pack2(in.c.x, in.c.y), r.c23 = pack2(in.c.z, in.c.w);
         return r;
