@@ -283,9 +283,8 @@ gdn_status run_norm(const void* x, const float* w, const void* residual, const v
   p.vec = D % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) &&
           aligned(gate, 16) && aligned(w, 16) && aligned(y, fp8 ? 8 : 16) &&
           (one || x_stride * elem % 16 == 0) && (one || !gate || gate_stride * elem % 16 == 0);
-  cudaError_t e = gdn::device_error_word(&p.err);
-  if (e != cudaSuccess) return cuda_fail(e, "locating the device error word");
-  e = gdn::launch_norm(p, f32, fp8, reinterpret_cast<cudaStream_t>(stream));
+  p.err = nullptr;
+  const cudaError_t e = gdn::launch_norm(p, f32, fp8, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the RMS norm");
 }
 

@@ -79,7 +79,8 @@ struct NormParams {
   int group_log;                    // log2 of a group below D
   float eps, inv_d;                 // inv_d: 1 / D
   int vec;                          // every 8-column access is aligned and D is a multiple of 8
-  unsigned* err;                    // device error word: bounded waits record a timeout here
+  unsigned* err;                    // device error word: bounded waits record a timeout here (set
+                                    // by the launch that has them)
 };
 constexpr int kNormMaxD = 32768;
 cudaError_t launch_norm(const NormParams& p, bool f32, bool fp8, cudaStream_t stream);

@@ -401,15 +401,16 @@ cudaError_t launch_block(const NormParams& p, cudaStream_t stream) {
 }
 
 template <typename T, bool kFp8, int NV>
-cudaError_t launch_ring(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_ring(NormParams p, cudaStream_t stream) {
   const int slot_bytes = p.D * (int)sizeof(T) * (1 + (p.residual ? 1 : 0) + (p.gate ? 1 : 0));
   // two blocks an SM with four slots or more each, else one block with up to twice the memory
   int blocks = 2, slots = 110 * 1024 / slot_bytes;
   if (slots < 4) blocks = 1, slots = 220 * 1024 / slot_bytes;
   if (slots > 8) slots = 8;
   const auto kernel = norm_ring_kernel<T, kFp8, NV>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             slots * slot_bytes);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       slots * slot_bytes);
+  if (e == cudaSuccess) e = device_error_word(&p.err);
   if (e != cudaSuccess) return e;
   const long long most = (long long)blocks * kSms;
   const unsigned grid = (unsigned)(p.rows < most ? p.rows : most);

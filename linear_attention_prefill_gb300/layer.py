@@ -28,20 +28,27 @@ def _function(name: str, dtype):
     return fn
 
 
-def _call(name: str, dtype, index: int, stream, args):
-    """One library call with device ``index`` current, on ``stream`` or its current one."""
+def _call(name: str, dtype, index: int, args):
+    """One library call on the current stream of device ``index``, with it as the current one."""
     fn = _FN.get((name, dtype)) or _function(name, dtype)
-    if stream is None:
-        handle = _current_stream(index)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if _current_device() == index:
-        status = fn(*args, handle)
+        status = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, handle)
+            status = fn(*args, _current_stream(index))
     if status:
         _check(status)
+
+
+def _on(stream, x):
+    """``stream`` (a torch stream, or a cudaStream_t as a number) as the current one: the call's
+    own allocations belong to the stream that it runs on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        if not isinstance(x, _Tensor) or x.get_device() < 0:
+            raise ValueError("a stream needs operands on a CUDA device")
+        stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else
+                  torch.cuda.default_stream(x.device))
+    return torch.cuda.stream(stream)
 
 
 def _kind(x, name: str, dims: int):
@@ -79,6 +86,14 @@ def _dense(t, name: str, dtype, index: int, shape) -> int:
             and t.shape == shape and t.is_contiguous()):
         _refuse(t, name, dtype, index, shape)
     return t.data_ptr()
+
+
+def _output(t, name: str, like, dtype, index: int, shape):
+    """(address, tensor) of an output: the caller's, or a fresh one on the device of ``like``."""
+    if t is None:
+        t = torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+        return t.data_ptr(), t
+    return _dense(t, name, dtype, index, shape), t
 
 
 def _maybe(t, name: str, dtype, index: int, shape):
@@ -161,6 +176,10 @@ def gdn_short_conv_fwd(x, weight, bias=None, s0=None, y=None, sT=None, *,
     packed row, B = 1; rows behind cu_seqlens[N] are left as they were.  sT [N, W-1, D] may
     be s0 (in place).
     """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_short_conv_fwd(x, weight, bias, s0, y, sT, activation=activation,
+                                      cu_seqlens=cu_seqlens, output_final_state=output_final_state)
     dtype, index = _kind(x, "x", 3)
     shape = x.shape
     D = shape[2]
@@ -168,14 +187,12 @@ def gdn_short_conv_fwd(x, weight, bias=None, s0=None, y=None, sT=None, *,
     N, T, cu = _sequences(shape, cu_seqlens, x.device)
     xp, stride = _rows(x, "x", dtype, index, shape)
     states = (N, W - 1, D)
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
+    yp, y = _output(y, "y", x, dtype, index, shape)
     if sT is None and output_final_state and W > 1:
         sT = torch.empty(states, dtype=dtype, device=x.device)
-    _call("gdn_short_conv_fwd", dtype, index, stream,
+    _call("gdn_short_conv_fwd", dtype, index,
           (xp, w, _maybe(bias, "bias", _F32, index, (D,)), _maybe(s0, "s0", dtype, index, states),
-           _dense(y, "y", dtype, index, shape), _maybe(sT, "sT", dtype, index, states), N, T, D, W,
-           stride, _act(activation), cu))
+           yp, _maybe(sT, "sT", dtype, index, states), N, T, D, W, stride, _act(activation), cu))
     return y, sT
 
 
@@ -186,17 +203,19 @@ def gdn_short_conv_step(x, weight, s, bias=None, y=None, *, activation: Optional
     x [N, D] (may be a slice of a wider projection); weight, bias and activation as in
     gdn_short_conv_fwd.
     """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_short_conv_step(x, weight, s, bias, y, activation=activation)
     dtype, index = _kind(x, "x", 2)
     shape = x.shape
     N, D = shape
     w, W = _taps(weight, index, D)
     xp, stride = _rows(x, "x", dtype, index, shape)
     sp = _dense(s, "s", dtype, index, (N, W - 1, D))
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    _call("gdn_short_conv_step", dtype, index, stream,
-          (xp, w, _maybe(bias, "bias", _F32, index, (D,)), sp, _dense(y, "y", dtype, index, shape),
-           N, D, W, stride, _act(activation)))
+    yp, y = _output(y, "y", x, dtype, index, shape)
+    _call("gdn_short_conv_step", dtype, index,
+          (xp, w, _maybe(bias, "bias", _F32, index, (D,)), sp, yp, N, D, W, stride,
+           _act(activation)))
     return y
 
 
@@ -239,11 +258,15 @@ def gdn_s6_chunk_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, y=No
     place).  ``workspace``: a uint8 device tensor of at least
     gdn_s6_chunk_fwd_workspace_size bytes, or None for a fresh one where the sizes need one.
     """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_s6_chunk_fwd(x, dt, A, B, C, D, z, dt_bias, h0, y, hT, dt_softplus=dt_softplus,
+                                    cu_seqlens=cu_seqlens, output_final_state=output_final_state,
+                                    workspace=workspace)
     dtype, index, dim, Ns, ptrs, strides = _s6_rows(x, dt, A, B, C, D, z, dt_bias, 3)
     N, T, cu = _sequences(x.shape, cu_seqlens, x.device)
     states = (N, dim, Ns)
-    if y is None:
-        y = torch.empty(x.shape, dtype=dtype, device=x.device)
+    yp, y = _output(y, "y", x, dtype, index, x.shape)
     if hT is None and output_final_state:
         hT = torch.empty(states, dtype=_F32, device=x.device)
     if workspace is None:
@@ -252,9 +275,8 @@ def gdn_s6_chunk_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, y=No
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     else:
         _need(workspace, "workspace", torch.uint8, x.device)
-    _call("gdn_s6_chunk_fwd", dtype, index, stream,
-          (*ptrs, _maybe(h0, "h0", _F32, index, states), _dense(y, "y", dtype, index, x.shape),
-           _maybe(hT, "hT", _F32, index, states), N, T, dim, Ns, *strides, int(bool(dt_softplus)), cu,
+    _call("gdn_s6_chunk_fwd", dtype, index,
+          (*ptrs, _maybe(h0, "h0", _F32, index, states), yp, _maybe(hT, "hT", _F32, index, states), N, T, dim, Ns, *strides, int(bool(dt_softplus)), cu,
            None if workspace is None else workspace.data_ptr(),
            0 if workspace is None else workspace.numel()))
     return y, hT
@@ -266,14 +288,16 @@ def gdn_s6_recurrent_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, y=Non
 
     x, dt, z [N, D]; B, C [N, Ns]; the rest as in gdn_s6_chunk_fwd.
     """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_s6_recurrent_step(x, dt, A, B, C, h, D, z, dt_bias, y, dt_softplus=dt_softplus)
     dtype, index, dim, Ns, ptrs, strides = _s6_rows(x, dt, A, B, C, D, z, dt_bias, 2)
     shape = x.shape
     N = shape[0]
     hp = _dense(h, "h", _F32, index, (N, dim, Ns))
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    _call("gdn_s6_recurrent_step", dtype, index, stream,
-          (*ptrs, hp, _dense(y, "y", dtype, index, shape), N, dim, Ns, *strides,
+    yp, y = _output(y, "y", x, dtype, index, shape)
+    _call("gdn_s6_recurrent_step", dtype, index,
+          (*ptrs, hp, yp, N, dim, Ns, *strides,
            int(bool(dt_softplus))))
     return y
 
@@ -289,6 +313,10 @@ def gdn_rms_norm_fwd(x, weight, residual=None, gate=None, y=None, residual_out=N
     scales [..., ceil(D / group)], one per ``group`` (32, 64, 128) columns or one a row (None):
     scale = max|y| / 448 (1 for zeros).  scales and residual_out are None where there are none.
     """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_rms_norm_fwd(x, weight, residual, gate, y, residual_out, scales, eps=eps,
+                                    out_dtype=out_dtype, group=group)
     dtype, index = _kind(x, "x", x.dim() if isinstance(x, _Tensor) and x.dim() else 1)
     shape = x.shape
     D = shape[-1]
@@ -321,25 +349,21 @@ def gdn_rms_norm_fwd(x, weight, residual=None, gate=None, y=None, residual_out=N
             _refuse(x, "x", dtype, index, shape, dense=False)
         if gs is None:
             _refuse(gate, "gate", dtype, index, shape, dense=False)
-    if y is None:
-        y = torch.empty(shape, dtype=_E4M3 if fp8 else dtype, device=x.device)
-    yp = _dense(y, "y", _E4M3 if fp8 else dtype, index, shape)
+    yp, y = _output(y, "y", x, _E4M3 if fp8 else dtype, index, shape)
     rp = op = None
     if residual is not None:
         rp = _dense(residual, "residual", dtype, index, shape)
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dtype, device=x.device)
-        op = _dense(residual_out, "residual_out", dtype, index, shape)
+        op, residual_out = _output(residual_out, "residual_out", residual, dtype, index, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if fp8:
         parts = shape[:-1] + (-(-D // group) if group else 1,)
         if scales is None:
             scales = torch.empty(parts, dtype=_F32, device=x.device)
-        _call("gdn_rms_norm_fwd_e4m3", dtype, index, stream,
+        _call("gdn_rms_norm_fwd_e4m3", dtype, index,
               (x.data_ptr(), wp, rp, gp, yp, _dense(scales, "scales", _F32, index, parts), op,
                rows // heads, heads, D, xs, gs, group or 0, eps))
     else:
-        _call("gdn_rms_norm_fwd", dtype, index, stream,
+        _call("gdn_rms_norm_fwd", dtype, index,
               (x.data_ptr(), wp, rp, gp, yp, op, rows // heads, heads, D, xs, gs, eps))
     return y, scales, residual_out

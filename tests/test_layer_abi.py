@@ -101,13 +101,16 @@ def test_s6_step_rejects(lib, case, status):
 
 def test_s6_workspace_size(lib):
     size = lib.gdn_s6_chunk_fwd_workspace_size
-    assert size(1, 4096, 5120, 16, 0) == 0 and size(64, 64, 64, 16, 0) == 0  # whole sequences
-    for N, T, dim, Ns, packed in ((1, 65536, 2048, 16, 0), (2, 3000, 33, 7, 0), (3, 9001, 100, 16, 1)):
+    assert size(1, 4096, 4864, 16, 0) == 0 and size(64, 64, 64, 16, 0) == 0  # whole sequences
+    for N, T, dim, Ns, packed in ((1, 65536, 2048, 16, 0), (2, 3000, 33, 7, 0), (3, 9001, 100, 16, 1),
+                                  (1, 4096, 5120, 16, 0)):
         got = size(N, T, dim, Ns, packed)
-        # slots x (steps' sum, states) and a copy of the states, each piece 256-byte aligned
+        # of the split channels (all, or those behind whole 32-channel tiles): slots x (steps' sum,
+        # states) and a copy of the states, each piece 256-byte aligned
         up = lambda v: -(-v // 64) * 64  # noqa: E731
-        assert got % 4 == 0 and any(
-            got == 4 * (up(s * dim) + up(s * dim * Ns) + N * dim * Ns) for s in range(N, 32 * N + N + 2))
+        assert got > 0 and got % 4 == 0 and any(
+            got == 4 * (up(s * d) + up(s * d * Ns) + N * d * Ns)
+            for s in range(N, 32 * N + N + 2) for d in {dim, dim - 32 * 152} if d > 0)
     assert size(-1, 64, 64, 16, 0) == 0 and size(1, 4096, 64, 65, 0) == 0
 
 

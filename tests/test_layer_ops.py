@@ -238,7 +238,8 @@ def s6_run(lib, x, softplus, cu=None, gate=True, skip=True, hT=None, **kw):
 @pytest.mark.parametrize("lens,packed,dim,Ns", [
     ((1,), False, 32, 16), ((70, 70), False, 100, 16), ((33,), False, 33, 5), ((64,), False, 16, 64),
     ((40, 0, 1, 95, 0), True, 72, 16), ((31, 65), True, 40, 8), ((17,), False, 34, 4),
-    ((3, 3, 3), False, 65, 1), ((32,), False, 64, 32), ((45,), False, 31, 23),
+    ((3, 3, 3), False, 65, 1), ((32,), False, 64, 32), ((45,), False, 31, 23), ((50,), False, 64, 6),
+    (tuple((7 * i) % 41 for i in range(170)), True, 40, 16),  # several CTAs on every SM
 ])
 def test_s6_prompt(cuda_lib, dtype, lens, packed, dim, Ns):
     dt, g = DT[dtype], gen_of(dim + Ns)
@@ -266,7 +267,7 @@ def test_s6_prompt(cuda_lib, dtype, lens, packed, dim, Ns):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens,packed,dim,Ns", [
     ((2085,), False, 64, 16), ((1300, 0, 2, 1700), True, 40, 16), ((1111, 1111), False, 33, 7),
-    ((1500,), False, 16, 64),
+    ((1500,), False, 16, 64), ((1100,), False, 4900, 16),  # the last: whole channels beside split ones
 ])
 def test_s6_split_over_time(cuda_lib, dtype, lens, packed, dim, Ns):
     """Few channels, many tokens: the split over time, with states and in place."""
@@ -384,7 +385,7 @@ def norm_ref(x, w, residual, gate, eps):
 
 
 NORM_ROWS = [(1, 64), (3, 8), (17, 129), (5, 128), (130, 72), (2, 1032), (9, 2560), (3, 5123), (2, 16392),
-             (1, 32768), (4, 1000), (6, 500)]
+             (1, 32768), (4, 1000), (6, 500), (1300, 520), (2500, 2560), (1217, 8192), (1216, 1001)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -450,10 +451,10 @@ def test_norm_zero_huge_and_nan_rows(cuda_lib):
             assert (q[1].float() == 448).all() and (s[1] > 0).all()
 
 
-def test_norm_of_heads_with_a_sliced_gate(cuda_lib):
+@pytest.mark.parametrize("B,T,H,D", [(2, 7, 3, 128), (1, 700, 2, 1024), (3, 5, 7, 40)])
+def test_norm_of_heads_with_a_sliced_gate(cuda_lib, B, T, H, D):
     """[B, T, H, D] with the gate a slice of the projection: tokens strided, heads dense."""
     g = gen_of(12)
-    B, T, H, D = 2, 7, 3, 128
     x = randn(g, B, T, H, D, dtype=torch.bfloat16)
     proj = randn(g, B, T, 2 * H * D + 16, dtype=torch.bfloat16)
     gate = proj[..., H * D:2 * H * D].unflatten(-1, (H, D))
@@ -546,6 +547,18 @@ def test_an_s6_layer_captured_and_replayed(cuda_lib):
         torch.cuda.synchronize()
         for a, b in zip(got, run()):
             assert torch.equal(a, b)
+
+
+def test_a_stream_by_its_handle(cuda_lib):
+    g = gen_of(23)
+    x, w = randn(g, 1, 40, 64, dtype=torch.bfloat16), randn(g, 64, 4)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    want, _ = cuda_lib.gdn_short_conv_fwd(x, w)
+    for handle in (side.cuda_stream, 0):
+        y, _ = cuda_lib.gdn_short_conv_fwd(x, w, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
 
 
 def test_calls_on_a_side_stream(cuda_lib):
