@@ -10,11 +10,11 @@ S6Split s6_split(int N, int T, int dim, int Ns, bool packed) {
   const long long ctas = (long long)N * tiles;
   const long long per_seq = (packed ? (long long)T : (long long)N * T) / N;  // packed: their mean
   const long long waves = (ctas + kSms - 1) / kSms;
-  // Cycles an SM takes for a token of 32 channels (measured at Ns = 16, bf16): 70 with one CTA,
-  // 116 with two, 190 with four; 74 for the two passes of a split channel, with four CTAs an SM;
+  // Cycles an SM takes for a token of 32 channels (measured at Ns = 16, bf16): 62 with one CTA,
+  // 117 with two, 192 with four; 74 for the two passes of a split channel, with four CTAs an SM;
   // 170 for the two passes along one chunk, and about 10000 for the summaries' launch and the
   // chunks' beginnings.
-  const auto cost = [](long long ctas_an_sm) { return 48 * ctas_an_sm + 22; };
+  const auto cost = [](long long ctas_an_sm) { return ctas_an_sm == 1 ? 62 : 48 * ctas_an_sm + 20; };
   const auto chunk_of = [&](long long parts) {
     parts = parts < 2 ? 2 : parts > 32 ? 32 : parts;
     const long long c = (per_seq + parts - 1) / parts;

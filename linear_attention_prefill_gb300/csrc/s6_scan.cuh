@@ -57,17 +57,22 @@ struct Cfg {
   static constexpr int kUnits = kCh / kWidth;  // channel pairs, or channels
   static constexpr int kCompute = kUnits * LPC < 32 ? 32 : kUnits * LPC;
   static constexpr int kHelpers = kPairs * kTile / 4;  // one has 2 channels x 4 tokens of a tile
-  static constexpr int kThreads = kCompute + kHelpers;
+  // Alone on its SM a CTA waits for the helpers' chains: one set of them prepares tiles, another
+  // finishes them (x for the skip then comes from a longer ring).
+  static constexpr bool kApart = kWidth == 1;
+  static constexpr int kThreads = kCompute + kHelpers * (kApart ? 2 : 1);
   // two computing warps and two helpers: one of each kind of warp a scheduler
-  static constexpr bool kPlace = kCompute == 64 && kHelpers == 64;
+  static constexpr bool kPlace = kCompute == 64 && kThreads == 128;
   // a raw row: 32 channels and 16 bytes more, so that rows 4 apart meet other banks
   static constexpr int kRowPieces = kCh * (int)sizeof(T) / 16, kPitch = kRowPieces + 1;
   static constexpr int kRawTile = kTile * kPitch;
   static constexpr int kCopies = kTile * kRowPieces / kHelpers;  // per helper, tensor and tile
   static constexpr int kDuTile = kPairs * (kTile + 1);  // (D0, D0 x0, D1, D1 x1) a pair and token
-  // four states' B and C of a token: one piece in bf16, two in fp32; bf16 ones are widened
-  // into two further tiles, fp32 ones are used where they arrive
-  static constexpr bool kWiden = sizeof(T) == 2;
+  // four states' B and C of a token: one piece in bf16, two in fp32.  They are read where they
+  // arrive, except that lanes with two channels have bf16 widened for them by the helpers, into
+  // two further tiles: there instructions count more than bytes (51 cycles against 55 where the
+  // lanes widen their own), with one channel a lane the bytes do (PACKED_LONE).
+  static constexpr bool kWiden = sizeof(T) == 2 && kWidth > 1, kPacked = sizeof(T) == 2 && !kWiden;
   static constexpr int kFours = kTile * LPC, kPerHelper = (kFours + kHelpers - 1) / kHelpers;
   static constexpr int kBcPieces = (int)sizeof(T) / 2, kBcTile = kFours * kBcPieces;
   static constexpr int kWideTile = kFours * 2;
@@ -78,8 +83,9 @@ struct Cfg {
   static constexpr int kParts = LPC < 4 ? LPC : 4, kLanes = LPC / kParts;
   static constexpr int kPartRow = kTile / 2 + 2, kPartPair = kParts * kPartRow + 1;
   static constexpr int kPartTile = kSummary ? 0 : kPairs * kPartPair;
-  static constexpr int kRaw = 0, kTensors = kSummary ? 2 : 3;
-  static constexpr int kDu = kRaw + kRing * kTensors * kRawTile;
+  static constexpr int kRingX = kApart ? 2 * kRing : kRing;
+  static constexpr int kX = 0, kDt = kX + kRingX * kRawTile, kZ = kDt + kRing * kRawTile;
+  static constexpr int kDu = kZ + (kSummary ? 0 : kRing * kRawTile);
   static constexpr int kBc = kDu + 2 * kDuTile;
   static constexpr int kWide = kBc + kRing * kBcTile;
   static constexpr int kPart = kWide + (kWiden ? 2 * kWideTile : 0);
@@ -146,7 +152,7 @@ __device__ __forceinline__ void cp_async8(void* dst, const void* src, bool ok) {
                "r"(ok ? 8 : 0)
                : "memory");
 }
-// cp.async of 4 bytes, zeros where !ok
+// cp.async of 4 bytes; zeros where !ok, and then nothing is read at src
 __device__ __forceinline__ void cp_async4(void* dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(dst)), "l"(src),
                "r"(ok ? 4 : 0)
@@ -282,8 +288,9 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
   for (int i = -1; i <= nt; ++i) {
     if (i >= 0 && i < nt) {
       const float4* du = smem + C::kDu + (i & 1) * C::kDuTile + pair * (kTile + 1);
+      constexpr int kFour = C::kPacked ? 1 : 2;  // pieces of a token's four states
       const float4* bc = (C::kWiden ? smem + C::kWide + (i & 1) * C::kWideTile
-                                    : smem + C::kBc + (i & (kRing - 1)) * C::kBcTile) + 2 * ln;
+                                    : smem + C::kBc + (i & (kRing - 1)) * C::kBcTile) + kFour * ln;
       float4* part = smem + C::kPart + (i & 1) * C::kPartTile + pair * C::kPartPair +
                      ln / C::kLanes * C::kPartRow;
       struct Two {
@@ -314,12 +321,14 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
           const float2 v = reinterpret_cast<const float2*>(du + t)[sub];
           r.d[0] = v.x, r.u[0] = v.y;
         }
-        r.b = bc[t * LPC * 2];
-        if (!kSummary) r.c = bc[t * LPC * 2 + 1];
+        r.b = bc[t * LPC * kFour];
+        if (!kSummary && !C::kPacked) r.c = bc[t * LPC * kFour + 1];
         return r;
       };
       auto ready = [&](const In& in) {
         Ready r;
+        const float4 b = C::kPacked ? wide4(in.b.x, in.b.y) : in.b;
+        const float4 c = C::kPacked ? wide4(in.b.z, in.b.w) : in.c;
 #pragma unroll
         for (int j = 0; j < kWidth; ++j) {
           const f32x2 d = dup2(in.d[j]), u = dup2(in.u[j]);
@@ -328,10 +337,10 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
           unpack2(mul2(a[j][1], d), e2, e3);
           r.a[j][0] = pack2(ex2(e0), ex2(e1));
           r.a[j][1] = pack2(ex2(e2), ex2(e3));
-          r.u[j][0] = mul2(pack2(in.b.x, in.b.y), u);
-          r.u[j][1] = mul2(pack2(in.b.z, in.b.w), u);
+          r.u[j][0] = mul2(pack2(b.x, b.y), u);
+          r.u[j][1] = mul2(pack2(b.z, b.w), u);
         }
-        if (!kSummary) r.c01 = pack2(in.c.x, in.c.y), r.c23 = pack2(in.c.z, in.c.w);
+        if (!kSummary) r.c01 = pack2(c.x, c.y), r.c23 = pack2(c.z, c.w);
         return r;
       };
       auto step = [&](const Ready& r, int j) -> float {
@@ -383,7 +392,7 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
         }
       }
     }
-    named_sync(2, C::kCompute + C::kHelpers);
+    named_sync(2, C::kThreads);
   }
 
 #pragma unroll
@@ -401,8 +410,8 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
 
 // The helper threads' part.  In iteration i the computing threads are at tile i; the helpers
 // start the copies of tiles to come (x and dt of tile i + 4, B and C of i + 3, z of i + 2: the
-// ring's places are free then), stage tile i + 1 and write y of tile i - 1.
-template <class C>
+// ring's places are free then), stage tile i + 1 (kStage) and write y of tile i - 1 (kFinish).
+template <class C, bool kStage, bool kFinish>
 __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4* smem, int nt,
                                         int tid) {
   using T = typename C::T;
@@ -412,8 +421,8 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
   const int c = k.ch0 + 2 * pair, left = p.dim - c;
   const f32x2 bias = pack2(p.dt_bias && left > 0 ? p.dt_bias[c] : 0.f,
                            p.dt_bias && left > 1 ? p.dt_bias[c + 1] : 0.f);
-  const f32x2 skip = pack2(!kSummary && p.D && left > 0 ? p.D[c] : 0.f,
-                           !kSummary && p.D && left > 1 ? p.D[c + 1] : 0.f);
+  const f32x2 skip = pack2(kFinish && p.D && left > 0 ? p.D[c] : 0.f,
+                           kFinish && p.D && left > 1 ? p.D[c + 1] : 0.f);
 
   // One tile of x (0), dt (1) or z (2) into the ring; rows and channels that do not exist: 0.
   // Rows on 4-byte boundaries only are copied by words, bf16 rows off those through registers,
@@ -428,10 +437,12 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
                      static_cast<const T*>(p.dt) + (some ? (k.t0 + row0) * p.dt_stride + ch : 0),
                      static_cast<const T*>(p.z) + (some ? (k.t0 + row0) * p.z_stride + ch : 0)};
   constexpr bool kHalves = sizeof(T) == 2;
-  Raw8<__nv_bfloat16> late[kHalves ? C::kTensors * C::kCopies : 1];
+  Raw8<__nv_bfloat16> late[kHalves ? 3 * C::kCopies : 1];
   auto place = [&](int tensor, int i, int j) {
-    return smem + C::kRaw + (tensor * kRing + (i & (kRing - 1))) * C::kRawTile +
-           (row0 + j * kRowStep) * C::kPitch + piece;
+    const int tile = tensor == 0   ? C::kX + (i & (C::kRingX - 1)) * C::kRawTile
+                     : tensor == 1 ? C::kDt + (i & (kRing - 1)) * C::kRawTile
+                                   : C::kZ + (i & (kRing - 1)) * C::kRawTile;
+    return smem + tile + (row0 + j * kRowStep) * C::kPitch + piece;
   };
   auto copy = [&](int tensor, long long stride, int i) {
     if (i >= nt) return;
@@ -445,10 +456,8 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
         cp_async16(dst, s, ok);
       } else if (p.copy == 4) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const bool in = ok && w * kWord < some;
-          cp_async4(reinterpret_cast<uint32_t*>(dst) + w, in ? s + w * kWord : s, in);
-        }
+        for (int w = 0; w < 4; ++w)
+          cp_async4(reinterpret_cast<uint32_t*>(dst) + w, s + w * kWord, w * kWord < (ok ? some : 0));
       } else if constexpr (kHalves) {
         late[tensor * C::kCopies + j].load_n(s, ok ? some : 0);
       }
@@ -490,10 +499,9 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
       } else if (p.copy_bc == 4) {
 #pragma unroll
         for (int w = 0; w < (int)sizeof(T); ++w) {
-          const bool in = ok && w * kWord < nst;
-          cp_async4(reinterpret_cast<uint32_t*>(dst) + w, in ? sb + w * kWord : sb, in);
-          if (!kSummary)
-            cp_async4(reinterpret_cast<uint32_t*>(dst_c) + w, in ? sc + w * kWord : sc, in);
+          const bool in = w * kWord < (ok ? nst : 0);
+          cp_async4(reinterpret_cast<uint32_t*>(dst) + w, sb + w * kWord, in);
+          if (!kSummary) cp_async4(reinterpret_cast<uint32_t*>(dst_c) + w, sc + w * kWord, in);
         }
       } else {
         Raw4<T> b, c;
@@ -512,30 +520,35 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
   T* yp = static_cast<T*>(p.y) + (k.t0 + 4 * quad) * p.dim + c;
   f32x2 sum = pack2(0.f, 0.f);  // of this thread's steps (kSummary)
   Raw2<T> x_next[4], x_now[4], x_last[4];  // x of tiles i + 1, i, i - 1 (the skip)
-  const bool gate = !kSummary && p.z;
+  const bool gate = kFinish && p.z;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    copy(0, p.x_stride, i);
-    copy(1, p.dt_stride, i);
-    if (i < 2) copy_bc(i);
+    if (kStage) {
+      copy(0, p.x_stride, i);
+      copy(1, p.dt_stride, i);
+      if (i < 2) copy_bc(i);
+    }
     if (i == 0 && gate) copy(2, p.z_stride, 0);
     cp_async_commit();
-    copy_late(0, i);
-    copy_late(1, i);
+    if (kStage) {
+      copy_late(0, i);
+      copy_late(1, i);
+    }
     if (i == 0 && gate) copy_late(2, 0);
   }
   cp_async_wait<2>();
-  named_sync(1, C::kHelpers);
+  if (kStage) named_sync(1, C::kHelpers);
   for (int i = -1; i <= nt; ++i) {
-    copy(0, p.x_stride, i + kRing);
-    copy(1, p.dt_stride, i + kRing);
-    copy_bc(i + 3);
+    if (kStage) {
+      copy(0, p.x_stride, i + kRing);
+      copy(1, p.dt_stride, i + kRing);
+      copy_bc(i + 3);
+    }
     if (gate) copy(2, p.z_stride, i + 2);
     cp_async_commit();
-    if (i + 1 < nt) {  // stage
-      const int s = (i + 1) & (kRing - 1);
-      const float4* rx = smem + C::kRaw + s * C::kRawTile;
-      const float4* rd = rx + kRing * C::kRawTile;
+    if (kStage && i + 1 < nt) {
+      const float4* rx = smem + C::kX + ((i + 1) & (C::kRingX - 1)) * C::kRawTile;
+      const float4* rd = smem + C::kDt + ((i + 1) & (kRing - 1)) * C::kRawTile;
       float4* du = smem + C::kDu + ((i + 1) & 1) * C::kDuTile + pair * (kTile + 1) + 4 * quad;
       const int rows = len - (i + 1) * kTile - 4 * quad;
       // (branches around the four tokens, not within: their chains run side by side)
@@ -560,7 +573,7 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
         du[u] = make_float4(d0, u0, d1, u1);
       }
       if (C::kWiden) {
-        const float4* raw = smem + C::kBc + s * C::kBcTile;
+        const float4* raw = smem + C::kBc + ((i + 1) & (kRing - 1)) * C::kBcTile;
         float4* wide = smem + C::kWide + ((i + 1) & 1) * C::kWideTile;
 #pragma unroll
         for (int j = 0; j < C::kPerHelper; ++j) {
@@ -573,7 +586,7 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
         }
       }
     }
-    if (!kSummary && i >= 1 && left > 0) {  // y of tile i - 1
+    if (kFinish && i >= 1 && left > 0) {
       const float4* part = smem + C::kPart + ((i - 1) & 1) * C::kPartTile + pair * C::kPartPair +
                            2 * quad;
       f32x2 v[4];
@@ -592,9 +605,14 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
         v[2 * q] = pack2(a0, b0);
         v[2 * q + 1] = pack2(a1, b1);
       }
-      const float4* rz = smem + C::kRaw + (2 * kRing + ((i - 1) & (kRing - 1))) * C::kRawTile;
+      const float4* rz = smem + C::kZ + ((i - 1) & (kRing - 1)) * C::kRawTile;
       const int rows = len - (i - 1) * kTile - 4 * quad;
       if (p.D) {
+        if (!kStage) {
+          const float4* rx = smem + C::kX + ((i - 1) & (C::kRingX - 1)) * C::kRawTile;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x_last[u].load(rx + (4 * quad + u) * C::kPitch, pair);
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) v[u] = fma2(skip, x_last[u].get(), v[u]);
       }
@@ -616,13 +634,17 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
       }
       yp += kTile * (long long)p.dim;
     }
+    if (kStage && kFinish) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) x_last[u] = x_now[u], x_now[u] = x_next[u];
-    copy_late(0, i + kRing);
-    copy_late(1, i + kRing);
+      for (int u = 0; u < 4; ++u) x_last[u] = x_now[u], x_now[u] = x_next[u];
+    }
+    if (kStage) {
+      copy_late(0, i + kRing);
+      copy_late(1, i + kRing);
+    }
     if (gate) copy_late(2, i + 2);
     cp_async_wait<2>();
-    named_sync(2, C::kCompute + C::kHelpers);
+    named_sync(2, C::kThreads);
   }
 
   if (kSummary) {  // the sum of the chunk's steps: kTile / 4 threads hold parts of each pair's
@@ -668,8 +690,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kBlocks) s6_kernel(const S6Par
     __syncthreads();
     if (s_seen == 15u) tid = w * 32 + tid % 32;
   }
-  if (tid >= C::kCompute) s6_help<C>(p, k, smem, nt, tid - C::kCompute);
-  else s6_compute<C>(p, k, smem, nt, tid);
+  if (tid < C::kCompute) {
+    s6_compute<C>(p, k, smem, nt, tid);
+  } else if constexpr (C::kApart) {
+    if (tid < C::kCompute + C::kHelpers) s6_help<C, true, false>(p, k, smem, nt, tid - C::kCompute);
+    else s6_help<C, false, true>(p, k, smem, nt, tid - C::kCompute - C::kHelpers);
+  } else {
+    s6_help<C, true, !C::kSummary>(p, k, smem, nt, tid - C::kCompute);
+  }
   // every block of the scan outlives the summaries, so what follows in the stream may reuse
   // the workspace
   if (!C::kSummary && p.chunk) griddep_wait();
