@@ -113,13 +113,13 @@ TRAFFIC_JSON = os.path.join(ROOT, "profiles", "traffic.json")
 
 
 def kernel_source_hash() -> str:
-    """Hash of every CUDA source of the library: a traffic figure is shown only for
-    the exact sources it was measured on."""
+    """Hash of every CUDA source of the forwards (gdn_*, kda_*): a traffic figure is shown
+    only for the exact sources it was measured on."""
     import hashlib
     csrc = os.path.join(ROOT, "linear_attention_prefill_gb300", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f.startswith(("gdn_", "kda_")) and f.endswith((".cu", ".cuh", ".h")):
             h.update(f.encode())
             with open(os.path.join(csrc, f), "rb") as fh:
                 h.update(fh.read())
