@@ -1,4 +1,5 @@
-"""Build libgdn.so in-tree with nvcc for sm_103a (no torch extension machinery).
+"""Build libgdn.so in-tree with nvcc for sm_103a (no torch extension machinery), and beside
+it the Python extension that binds the layer operators (layer_binding.cpp, host C++).
 
 Every .cu under csrc/ compiles to an object in parallel; the objects link into
 linear_attention_prefill_gb300/libgdn.so with the static CUDA runtime, so the
@@ -12,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
+BINDING = os.path.join(PKG, "_layer_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,10 +40,31 @@ def _deps():
         os.path.join(os.path.dirname(PKG), "include", "gdn.h")]
 
 
+def _build_binding() -> str:
+    """Compile the layer operators' binding against the installed torch; returns its compiler
+    messages."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SRC, "-o", tmp]
+    cmd += [f"-I{d}" for d in (os.path.join(root, "include"),
+                              os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                              sysconfig.get_paths()["include"], os.path.join(cuda, "include"))]
+    cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return r.stderr
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -63,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_build_binding)
         results = list(ex.map(compile_one, _sources()))
+        binding.result()
     logs = "".join(err for _, err in results)
     if verbose and logs:
         sys.stderr.write(logs)
