@@ -80,8 +80,8 @@ gdn_status check_conv(const void* x, const float* w, const float* bias, const vo
   if (overlap(ry, rx) || overlap(ry, r0) || overlap(ry, rT) || overlap(rT, rx) ||
       (s0 != sT && overlap(r0, rT)))
     return fail(GDN_ERR_INVALID_ARG, "y and sT must not overlap the inputs (sT may be s0)");
-  // blocks of 4 or more tokens, one per state; 512 channels a block
-  if (tokens / 4 + N + 1 > kMaxGrid || D > 65535 * 512)
+  // blocks of 4 or more tokens, one per state; 256 channels a block or more
+  if (tokens / 4 + N + 1 > kMaxGrid || D > 65535 * 256)
     return fail(GDN_ERR_INVALID_ARG, "problem too large: %lld tokens, D=%d", tokens, D);
   p->x = x; p->w = w; p->bias = bias; p->s0 = s0; p->y = y; p->sT = sT; p->cu = cu;
   p->x_stride = x_stride;

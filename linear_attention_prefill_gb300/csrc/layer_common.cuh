@@ -23,14 +23,6 @@ struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 v;
-  __device__ __forceinline__ void get(float (&o)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = __uint_as_float(w[i] << 16);
-      o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
   __device__ __forceinline__ void set(const float (&o)[8]) {
     uint32_t w[4];
 #pragma unroll

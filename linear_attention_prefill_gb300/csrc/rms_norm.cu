@@ -78,6 +78,7 @@ __device__ __forceinline__ float reduce_row(float v, int G, float* s) {
       v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, off));
     return __shfl_sync(0xffffffffu, v, 0);
   }
+#pragma unroll
   for (int off = G >> 1; off > 0; off >>= 1)
     v = combine<kMax>(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
@@ -168,9 +169,10 @@ __device__ __forceinline__ void take(const NormParams& p, T* out, const Raw8<T>&
 // Rows within a warp: G lanes a row, NV vectors of 8 columns a lane: vector i * G + lane.  A
 // block walks its rows, the next one is loaded while the present one is reduced, and w stays in
 // registers.
-template <typename T, bool kFp8, int NV>
-__global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p, int G) {
-  const int lane = threadIdx.x % G, per_block = 128 / G;
+template <typename T, bool kFp8, int G, int NV>
+__global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
+  constexpr int per_block = 128 / G;
+  const int lane = threadIdx.x % G;
   const long long step = (long long)gridDim.x * per_block;
   const bool vec = p.vec;
   int n[NV];
@@ -375,15 +377,17 @@ __global__ void __launch_bounds__(kRingThreads)
   }
 }
 
-template <typename T, bool kFp8>
+template <typename T, bool kFp8, int G, int NV>
 cudaError_t launch_warp(const NormParams& p, cudaStream_t stream) {
-  const int nvec = (p.D + 7) / 8;
-  int G = 4;
-  while (G < nvec && G < 32) G *= 2;
-  const long long rows = 128 / G, blocks = (p.rows + rows - 1) / rows, most = 12ll * kSms;
-  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
-  if (nvec <= 32) norm_warp_kernel<T, kFp8, 1><<<grid, 128, 0, stream>>>(p, G);
-  else norm_warp_kernel<T, kFp8, 2><<<grid, 128, 0, stream>>>(p, G);
+  const auto kernel = norm_warp_kernel<T, kFp8, G, NV>;
+  static_assert(32 % G == 0, "rows do not cross warps");
+  // as many blocks as are resident together; each takes its rows in turn
+  int resident = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, 128, 0);
+  if (e != cudaSuccess) return e;
+  const long long rows = 128 / G, blocks = (p.rows + rows - 1) / rows;
+  const long long most = (long long)(resident < 1 ? 1 : resident) * kSms;
+  kernel<<<(unsigned)(blocks < most ? blocks : most), 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -421,7 +425,11 @@ cudaError_t launch_ring(NormParams p, cudaStream_t stream) {
 
 template <typename T, bool kFp8>
 cudaError_t launch_t(const NormParams& p, cudaStream_t stream) {
-  if (p.D <= 512) return launch_warp<T, kFp8>(p, stream);
+  if (p.D <= 32) return launch_warp<T, kFp8, 4, 1>(p, stream);
+  if (p.D <= 64) return launch_warp<T, kFp8, 8, 1>(p, stream);
+  if (p.D <= 128) return launch_warp<T, kFp8, 16, 1>(p, stream);
+  if (p.D <= 256) return launch_warp<T, kFp8, 32, 1>(p, stream);
+  if (p.D <= 512) return launch_warp<T, kFp8, 32, 2>(p, stream);
   // the ring's copies are of whole 16-byte pieces; it pays once every block has a few rows
   if (p.vec && p.D <= 8192 && p.rows >= 8 * kSms) {
     const int nv = (p.D / 8 + kRingThreads - 1) / kRingThreads;

@@ -14,7 +14,8 @@ namespace {
 
 constexpr int kStepThreads = 256;
 
-template <typename T, int LPC, int kSeqs>
+// kFull: Ns is 4 LPC and rows of B and C are aligned, so every lane has four states.
+template <typename T, int LPC, int kSeqs, bool kFull>
 __global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p, int per_row) {
   // sequences a lane prepares and finishes: kOwn from number ln * kOwn on, of the kSeqs
   constexpr int kOwn = (kSeqs + LPC - 1) / LPC;
@@ -23,15 +24,16 @@ __global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p,
   const int id = bx * kStepThreads + threadIdx.x;
   const bool some = id / LPC < p.dim;  // lanes behind the last channel only join the shuffles
   const int ch = some ? id / LPC : p.dim - 1, ln = id % LPC, n0 = ln * 4;
-  const int nst = some ? max(0, min(4, p.Ns - n0)) : 0;
-  const long long hrow = (long long)ch * p.Ns + n0, hsize = (long long)p.dim * p.Ns;
+  const int Ns = kFull ? 4 * LPC : p.Ns, vec_bc = kFull ? 1 : p.vec_bc;
+  const int nst = kFull ? 4 : some ? max(0, min(4, Ns - n0)) : 0;
+  const long long hrow = (long long)ch * Ns + n0, hsize = (long long)p.dim * Ns;
   const bool all = first + kSeqs <= p.N;
 
   float4 h[kSeqs];
   float* hp = p.hT + first * hsize + hrow;
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i)
-    h[i] = load_h(hp + (all || first + i < p.N ? i * hsize : 0), nst, p.Ns);
+    h[i] = load_h(hp + (all || first + i < p.N ? i * hsize : 0), nst, Ns);
   Raw4<T> rb[kSeqs], rc[kSeqs];
   const T* bp = static_cast<const T*>(p.B) + first * p.b_stride + n0;
   const T* cp = static_cast<const T*>(p.C) + first * p.c_stride + n0;
@@ -41,8 +43,8 @@ __global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p,
     rb[i].zero();
     rc[i].zero();
     if (nst > 0) {
-      rb[i].load(bp + k * p.b_stride, nst, p.vec_bc);
-      rc[i].load(cp + k * p.c_stride, nst, p.vec_bc);
+      rb[i].load(bp + k * p.b_stride, nst, vec_bc);
+      rc[i].load(cp + k * p.c_stride, nst, vec_bc);
     }
   }
   float x[kOwn], d[kOwn], z[kOwn];
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p,
     d[o] = to_f32(static_cast<const T*>(p.dt)[n * p.dt_stride + ch]);
     z[o] = p.z ? to_f32(static_cast<const T*>(p.z)[n * p.z_stride + ch]) : 0.f;
   }
-  const float4 a = load_h(p.A + hrow, nst, p.Ns);
+  const float4 a = load_h(p.A + hrow, nst, Ns);
   const float bias = p.dt_bias ? p.dt_bias[ch] : 0.f, skip = p.D ? p.D[ch] : 0.f;
   const float a0 = a.x * kLog2e, a1 = a.y * kLog2e, a2 = a.z * kLog2e, a3 = a.w * kLog2e;
   float u[kOwn];
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p,
     o.y = fmaf(ex2(di * a1), h[i].y, ui * b.y);
     o.z = fmaf(ex2(di * a2), h[i].z, ui * b.z);
     o.w = fmaf(ex2(di * a3), h[i].w, ui * b.w);
-    if (all || first + i < p.N) store_h(hp + i * hsize, o, nst, p.Ns);
+    if ((!kFull || some) && (all || first + i < p.N)) store_h(hp + i * hsize, o, nst, Ns);
     y[i] = 0.f;  // only of states that exist
     if (nst > 0) y[i] = c.x * o.x;
     if (nst > 1) y[i] = fmaf(c.y, o.y, y[i]);
@@ -119,16 +121,22 @@ __global__ void __launch_bounds__(kStepThreads) s6_step_kernel(const S6Params p,
   }
 }
 
-template <typename T, int LPC>
-cudaError_t launch_step_l(const S6Params& p, cudaStream_t stream) {
+template <typename T, int LPC, bool kFull>
+cudaError_t launch_step_f(const S6Params& p, cudaStream_t stream) {
   const int per_row = (int)(((long long)p.dim * LPC + kStepThreads - 1) / kStepThreads);
   const auto blocks = [&](int seqs) { return (long long)per_row * ((p.N + seqs - 1) / seqs); };
   // four sequences a lane once that still leaves two blocks per SM
   if (blocks(4) >= 2 * kSms)
-    s6_step_kernel<T, LPC, 4><<<(unsigned)blocks(4), kStepThreads, 0, stream>>>(p, per_row);
+    s6_step_kernel<T, LPC, 4, kFull><<<(unsigned)blocks(4), kStepThreads, 0, stream>>>(p, per_row);
   else
-    s6_step_kernel<T, LPC, 1><<<(unsigned)blocks(1), kStepThreads, 0, stream>>>(p, per_row);
+    s6_step_kernel<T, LPC, 1, kFull><<<(unsigned)blocks(1), kStepThreads, 0, stream>>>(p, per_row);
   return cudaGetLastError();
+}
+
+template <typename T, int LPC>
+cudaError_t launch_step_l(const S6Params& p, cudaStream_t stream) {
+  return p.Ns == 4 * LPC && p.vec_bc ? launch_step_f<T, LPC, true>(p, stream)
+                                     : launch_step_f<T, LPC, false>(p, stream);
 }
 
 template <typename T>

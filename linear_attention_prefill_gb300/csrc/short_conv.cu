@@ -7,13 +7,15 @@
 // where the W - 1 inputs before the sequence come from its state s0 (zeros without one) and
 // the last W - 1 inputs become the state sT.  Sums in fp32, one rounding at the end.
 //
-// HBM bandwidth bounds it: 2 bytes in and 2 out per element against ~8 instructions.  A
+// HBM bandwidth bounds it: 2 bytes in and 2 out per element against ~13 instructions.  A
 // thread has 4 channels (8 bytes of bf16) and walks a run of tokens with the window in
 // registers as packed fp32 pairs, so that each input is loaded once except for the W - 1 rows
 // before a run.  Its own inputs come by cp.async through a private ring of shared memory, three
-// rounds of four tokens ahead: what is in flight then costs no registers (loads ahead in
-// registers, one round: 22.4 us at 4096 x 6144 where the ring takes CONV_RING).  Rows off
-// 4-channel pieces are loaded element by element, one round ahead.
+// rounds of four tokens ahead: what is in flight then costs no registers.  At 4096 x 6144 (bf16,
+// 101 MB): 39 us with 8 channels a thread and loads as they are needed, 26.6 us with 4 and one
+// round ahead in registers, 22.6 us with the ring (4.5 TB/s).  Eight channels a thread on the
+// ring take a quarter fewer instructions but 124 registers: no faster, and slower at 10007 x 5376
+// (43 us against 41).  Rows off 4-channel pieces are loaded element by element.
 #include "gdn_common.cuh"
 #include "layer_common.cuh"
 #include "layer_internal.h"
@@ -21,65 +23,77 @@
 namespace gdn {
 namespace {
 
-constexpr int kVec4 = 4;      // channels per thread
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
+constexpr int kStepThreads = 128;
 constexpr int kAhead = 4;     // tokens of a round
 constexpr int kRounds = 4;    // rounds of the ring
 
-// Four channels of a row in fp32.
-struct Four {
-  f32x2 lo, hi;
-};
-template <typename T>
-__device__ __forceinline__ Four four(const Raw4<T>& r) {
-  const float4 v = r.get();
-  return {pack2(v.x, v.y), pack2(v.z, v.w)};
-}
+constexpr int kChans = 4;          // channels per thread
 
-// The filters of channels c..c+3, tap by tap: w is [D, W] and c a multiple of 4, so the 4 W
+// kChans neighbouring channels of a row, as stored and as fp32 pairs.
+template <typename T>
+struct Piece {
+  Raw4<T> r;
+  __device__ __forceinline__ void zero() { r.zero(); }
+  __device__ __forceinline__ void load(const T* p, int n, bool vec) { r.load(p, n, vec); }
+  __device__ __forceinline__ void store(T* p, int n, bool vec) const { r.store(p, n, vec); }
+  __device__ __forceinline__ void get(f32x2 (&o)[kChans / 2]) const {
+    const float4 v = r.get();
+    o[0] = pack2(v.x, v.y);
+    o[1] = pack2(v.z, v.w);
+  }
+  __device__ __forceinline__ void set(const f32x2 (&v)[kChans / 2]) {
+    float a, b, c, d;
+    unpack2(v[0], a, b);
+    unpack2(v[1], c, d);
+    r.set(a, b, c, d);
+  }
+};
+
+// The filters of channels c..c+kChans-1, tap by tap: w is [D, W] and c a multiple of kChans, so the kChans W
 // floats are whole 16-byte pieces.
 template <int W>
-__device__ __forceinline__ void load_filter(const float* w, int c, int n, Four (&f)[W]) {
-  float v[kVec4 * W];
-  if (n >= kVec4) {
+__device__ __forceinline__ void load_filter(const float* w, int c, int n, f32x2 (&f)[W][kChans / 2]) {
+  float v[kChans * W];
+  if (n >= kChans) {
     const float4* p = reinterpret_cast<const float4*>(w + (long long)c * W);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < kChans * W / 4; ++i) {
       const float4 q = p[i];
       v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec4 * W; ++i) v[i] = i / W < n ? w[(long long)c * W + i] : 0.f;
+    for (int i = 0; i < kChans * W; ++i) v[i] = i / W < n ? w[(long long)c * W + i] : 0.f;
   }
 #pragma unroll
-  for (int j = 0; j < W; ++j) f[j] = {pack2(v[j], v[W + j]), pack2(v[2 * W + j], v[3 * W + j])};
-}
-__device__ __forceinline__ Four load_bias(const float* bias, int c, int n) {
-  float b[kVec4];
+  for (int j = 0; j < W; ++j)
 #pragma unroll
-  for (int i = 0; i < kVec4; ++i) b[i] = bias && i < n ? bias[c + i] : 0.f;
-  return {pack2(b[0], b[1]), pack2(b[2], b[3])};
+    for (int i = 0; i < kChans / 2; ++i) f[j][i] = pack2(v[2 * i * W + j], v[(2 * i + 1) * W + j]);
+}
+__device__ __forceinline__ void load_bias(const float* bias, int c, int n, f32x2 (&b)[kChans / 2]) {
+#pragma unroll
+  for (int i = 0; i < kChans / 2; ++i)
+    b[i] = pack2(bias && 2 * i < n ? bias[c + 2 * i] : 0.f,
+                 bias && 2 * i + 1 < n ? bias[c + 2 * i + 1] : 0.f);
 }
 // act(bias + sum of taps), rounded
 template <typename T, int W>
-__device__ __forceinline__ Raw4<T> filter(const Four (&f)[W], const Four& bias, const Four (&win)[W],
-                                          int act) {
-  Four a = bias;
+__device__ __forceinline__ Piece<T> filter(const f32x2 (&f)[W][kChans / 2], const f32x2 (&bias)[kChans / 2],
+                                              const f32x2 (&win)[W][kChans / 2], int act) {
+  f32x2 a[kChans / 2];
 #pragma unroll
-  for (int j = 0; j < W; ++j) {
-    a.lo = fma2(f[j].lo, win[j].lo, a.lo);
-    a.hi = fma2(f[j].hi, win[j].hi, a.hi);
+  for (int i = 0; i < kChans / 2; ++i) {
+    a[i] = bias[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) a[i] = fma2(f[j][i], win[j][i], a[i]);
   }
   if (act) {
-    a.lo = silu2(a.lo);
-    a.hi = silu2(a.hi);
+#pragma unroll
+    for (int i = 0; i < kChans / 2; ++i) a[i] = silu2(a[i]);
   }
-  float v0, v1, v2, v3;
-  unpack2(a.lo, v0, v1);
-  unpack2(a.hi, v2, v3);
-  Raw4<T> o;
-  o.set(v0, v1, v2, v3);
+  Piece<T> o;
+  o.set(a);
   return o;
 }
 
@@ -96,9 +110,9 @@ __device__ __forceinline__ Span span_of(const ConvParams& p, int n) {
 
 // Row of the window of a token of sequence n, t = an absolute row: an input, or the state.
 template <typename T, int W>
-__device__ __forceinline__ Raw4<T> tap(const ConvParams& p, const Span& s, int n, long long t,
-                                       int c, int left, bool vec) {
-  Raw4<T> r;
+__device__ __forceinline__ Piece<T> tap(const ConvParams& p, const Span& s, int n, long long t,
+                                           int c, int left, bool vec) {
+  Piece<T> r;
   if (t >= s.begin) {
     r.load(static_cast<const T*>(p.x) + t * p.x_stride + c, left, vec);
   } else if (p.s0) {
@@ -115,7 +129,7 @@ __device__ __forceinline__ Raw4<T> tap(const ConvParams& p, const Span& s, int n
 template <typename T, int W>
 __device__ __forceinline__ void write_state(const ConvParams& p, int n, int c, int left, bool vec) {
   const Span s = span_of(p, n);
-  Raw4<T> r[W - 1];
+  Piece<T> r[W - 1];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) r[j] = tap<T, W>(p, s, n, s.end - (W - 1) + j, c, left, vec);
 #pragma unroll
@@ -123,40 +137,41 @@ __device__ __forceinline__ void write_state(const ConvParams& p, int n, int c, i
     r[j].store(static_cast<T*>(p.sT) + ((long long)n * (W - 1) + j) * p.D + c, left, vec);
 }
 
-// cp.async of one thread's four channels
-__device__ __forceinline__ void copy_four(Raw4<__nv_bfloat16>* dst, const __nv_bfloat16* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_four(Raw4<float>* dst, const float* src) {
-  cp_async16(dst, src, true);
+// cp.async of one thread's piece
+template <int kBytes>
+__device__ __forceinline__ void copy_piece(void* dst, const void* src) {
+  if constexpr (kBytes == 16)
+    cp_async16(dst, src, true);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// blockIdx.x: run of `run` tokens, then (with sT) one sequence's state each; blockIdx.y: 128
-// threads of 4 channels.  kVec: whole aligned pieces.
+// blockIdx.x: run of `run` tokens, then (with sT) one sequence's state each; blockIdx.y: 64
+// threads of kChans channels.  kVec: whole aligned pieces.
 template <typename T, int W, bool kVec>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int run, int runs,
                                                         long long tokens) {
-  __shared__ __align__(16) unsigned char s_ring[kVec ? kRounds * kAhead * kThreads * sizeof(Raw4<T>) : 16];
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec4;
+  using P = Piece<T>;
+  __shared__ __align__(16) unsigned char s_ring[kVec ? kRounds * kAhead * kThreads * sizeof(P) : 16];
+  const int c = (blockIdx.y * kThreads + threadIdx.x) * kChans;
   if (c >= p.D) return;
   const int left = p.D - c;
-  constexpr bool vec = kVec;
   if ((int)blockIdx.x >= runs) {
-    write_state<T, W>(p, blockIdx.x - runs, c, left, vec);
+    write_state<T, W>(p, blockIdx.x - runs, c, left, kVec);
     return;
   }
   const long long t0 = (long long)blockIdx.x * run, t1 = min(t0 + run, tokens);
   const T* x = static_cast<const T*>(p.x) + t0 * p.x_stride + c;
   T* y = static_cast<T*>(p.y) + t0 * p.D + c;
-  Raw4<T> ahead[kVec ? 1 : kAhead];  // the tokens of the next round
-  Raw4<T>* ring = reinterpret_cast<Raw4<T>*>(s_ring) + threadIdx.x;
+  P ahead[kVec ? 1 : kAhead];  // the tokens of the next round
+  P* ring = reinterpret_cast<P*>(s_ring) + threadIdx.x;
   const int len = (int)(t1 - t0);
   auto request = [&](int round) {  // this thread's inputs of a round, x at its first token
     if constexpr (kVec) {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (round * kAhead + u < len)
-          copy_four(ring + (round % kRounds * kAhead + u) * kThreads, x + u * p.x_stride);
+          copy_piece<sizeof(P)>(ring + (round % kRounds * kAhead + u) * kThreads, x + u * p.x_stride);
       cp_async_commit();
     } else {
 #pragma unroll
@@ -183,16 +198,24 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   if (n >= p.N) return;  // behind the last sequence: left as it was
   Span s = span_of(p, n);
 
-  Four f[W], win[W];  // the filter, and the inputs under it
+  f32x2 f[W][kChans / 2], win[W][kChans / 2], bias[kChans / 2];  // the filter, and the inputs under it
   load_filter<W>(p.w, c, left, f);
-  const Four bias = load_bias(p.bias, c, left);
+  load_bias(p.bias, c, left, bias);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j)
-    win[j] = four(tap<T, W>(p, s, n, max(t0, s.begin) - (W - 1) + j, c, left, vec));
+    tap<T, W>(p, s, n, max(t0, s.begin) - (W - 1) + j, c, left, kVec).get(win[j]);
+  auto next = [&](const P& in, T* to) {  // one token
+    in.get(win[W - 1]);
+    filter<T, W>(f, bias, win, p.silu).store(to, left, kVec);
+#pragma unroll
+    for (int j = 0; j + 1 < W; ++j)
+#pragma unroll
+      for (int i = 0; i < kChans / 2; ++i) win[j][i] = win[j + 1][i];
+  };
 
   int round = 0;
   for (long long t = t0; t < t1; t += kAhead, ++round) {
-    Raw4<T> raw[kAhead];
+    P raw[kAhead];
     if constexpr (kVec) {
       request(round + kRounds - 1);
       cp_async_wait<kRounds - 1>();
@@ -205,12 +228,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
     }
     if (t >= s.begin && t + kAhead <= min(t1, s.end)) {  // one sequence's tokens
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        win[W - 1] = four(raw[u]);
-        filter<T, W>(f, bias, win, p.silu).store(y + (long long)u * p.D, left, vec);
-#pragma unroll
-        for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
-      }
+      for (int u = 0; u < kAhead; ++u) next(raw[u], y + (long long)u * p.D);
     } else {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -223,13 +241,10 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
           } while (tt >= s.end);
 #pragma unroll
           for (int j = 0; j < W - 1; ++j)
-            win[j] = four(tap<T, W>(p, s, n, max(tt, s.begin) - (W - 1) + j, c, left, vec));
+            tap<T, W>(p, s, n, max(tt, s.begin) - (W - 1) + j, c, left, kVec).get(win[j]);
         }
         if (tt < s.begin) continue;
-        win[W - 1] = four(raw[u]);
-        filter<T, W>(f, bias, win, p.silu).store(y + (long long)u * p.D, left, vec);
-#pragma unroll
-        for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
+        next(raw[u], y + (long long)u * p.D);
       }
     }
     y += kAhead * (long long)p.D;
@@ -240,7 +255,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
 // of conv_kernel may still read it), or a batch without tokens.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_state_kernel(const ConvParams p) {
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * kVec4;
+  const int c = (blockIdx.y * kThreads + threadIdx.x) * kChans;
   if (c < p.D) write_state<T, W>(p, blockIdx.x, c, p.D - c, p.vec);
 }
 
@@ -248,14 +263,14 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(const ConvParams p
 // shifts their states in place.  kSeqs > 1 shares the filter, which is as many bytes as the
 // window and the output of one sequence.
 template <typename T, int W, int kSeqs>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p, int per_row) {
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvParams p, int per_row) {
+  const long long id = (long long)blockIdx.x * kStepThreads + threadIdx.x;
   const long long first = id / per_row * kSeqs;
   if (first >= p.N) return;
-  const int c = (int)(id % per_row) * kVec4;
+  const int c = (int)(id % per_row) * kChans;
   const int left = p.D - c;
   const bool vec = p.vec;
-  Raw4<T> r[kSeqs][W];
+  Piece<T> r[kSeqs][W];
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
     if (first + i >= p.N) break;
@@ -264,15 +279,15 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p,
     for (int j = 0; j < W - 1; ++j) r[i][j].load(s + (long long)j * p.D, left, vec);
     r[i][W - 1].load(static_cast<const T*>(p.x) + (first + i) * p.x_stride + c, left, vec);
   }
-  Four f[W];
+  f32x2 f[W][kChans / 2], bias[kChans / 2];
   load_filter<W>(p.w, c, left, f);
-  const Four bias = load_bias(p.bias, c, left);
+  load_bias(p.bias, c, left, bias);
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
     if (first + i >= p.N) break;
-    Four win[W];
+    f32x2 win[W][kChans / 2];
 #pragma unroll
-    for (int j = 0; j < W; ++j) win[j] = four(r[i][j]);
+    for (int j = 0; j < W; ++j) r[i][j].get(win[j]);
     filter<T, W>(f, bias, win, p.silu)
         .store(static_cast<T*>(p.y) + (first + i) * p.D + c, left, vec);
     T* s = static_cast<T*>(p.sT) + (first + i) * (W - 1) * p.D + c;
@@ -281,27 +296,35 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p,
   }
 }
 
+template <typename T, int W, bool kVec>
+cudaError_t launch_v(const ConvParams& p, bool states, cudaStream_t stream) {
+  const long long tokens = p.cu ? (long long)p.T : (long long)p.N * p.T;
+  const unsigned by = ((p.D + kChans - 1) / kChans + kThreads - 1) / kThreads;
+  // long runs repeat fewer rows (W - 1 each), short ones fill the GPU: 16 blocks per SM (runs of
+  // 64: 23.4 us at 4096 x 6144 and 42.1 at 10007 x 5376; of 32: 22.6 and 41.1; of 16: 22.6, 45.5)
+  int run = 32;
+  while (run > kAhead && (tokens + run - 1) / run * by < 16 * kSms) run /= 2;
+  const long long runs = (tokens + run - 1) / run;
+  const dim3 grid((unsigned)(runs + (states ? p.N : 0)), by);
+  conv_kernel<T, W, kVec><<<grid, kThreads, 0, stream>>>(p, run, (int)runs, tokens);
+  return cudaGetLastError();
+}
+
 template <typename T, int W>
 cudaError_t launch_w(const ConvParams& p, cudaStream_t stream) {
-  const long long tokens = p.cu ? (long long)p.T : (long long)p.N * p.T;
-  const int per_row = (p.D + kVec4 - 1) / kVec4;
-  const unsigned by = (per_row + kThreads - 1) / kThreads;
-  // long runs repeat fewer rows (W - 1 each), short ones fill the GPU: 8 blocks per SM
-  int run = 64;
-  while (run > kAhead && (tokens + run - 1) / run * by < 8 * kSms) run /= 2;
-  const long long runs = (tokens + run - 1) / run;
+  const bool none = p.T == 0;
   // sT == s0: the states wait for every block that reads them
-  const bool apart = p.sT && (p.s0 == p.sT || tokens == 0);
-  const long long bx = runs + (p.sT && !apart ? p.N : 0);
-  if (tokens > 0) {
-    const dim3 grid((unsigned)bx, by);
-    if (p.vec) conv_kernel<T, W, true><<<grid, kThreads, 0, stream>>>(p, run, (int)runs, tokens);
-    else conv_kernel<T, W, false><<<grid, kThreads, 0, stream>>>(p, run, (int)runs, tokens);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  const bool apart = p.sT && (p.s0 == p.sT || none), states = p.sT && !apart;
+  cudaError_t e = cudaSuccess;
+  if (none) {
+  } else if (p.vec) {
+    e = launch_v<T, W, true>(p, states, stream);
+  } else {
+    e = launch_v<T, W, false>(p, states, stream);
   }
-  if (apart)
-    conv_state_kernel<T, W><<<dim3((unsigned)p.N, by), kThreads, 0, stream>>>(p);
+  if (e != cudaSuccess || !apart) return e;
+  const unsigned by = ((p.D + kChans - 1) / kChans + kThreads - 1) / kThreads;
+  conv_state_kernel<T, W><<<dim3((unsigned)p.N, by), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -314,15 +337,16 @@ cudaError_t launch_t(const ConvParams& p, cudaStream_t stream) {
 
 template <typename T, int W>
 cudaError_t launch_step_w(const ConvParams& p, cudaStream_t stream) {
-  const int per_row = (p.D + kVec4 - 1) / kVec4;
+  const int per_row = (p.D + kChans - 1) / kChans;
   const auto blocks = [&](int seqs) {
-    return (unsigned)(((long long)((p.N + seqs - 1) / seqs) * per_row + kThreads - 1) / kThreads);
+    return (unsigned)(((long long)((p.N + seqs - 1) / seqs) * per_row + kStepThreads - 1) /
+                      kStepThreads);
   };
   // two sequences a thread once that still leaves 8 blocks per SM
   if (blocks(2) >= 8 * kSms)
-    conv_step_kernel<T, W, 2><<<blocks(2), kThreads, 0, stream>>>(p, per_row);
+    conv_step_kernel<T, W, 2><<<blocks(2), kStepThreads, 0, stream>>>(p, per_row);
   else
-    conv_step_kernel<T, W, 1><<<blocks(1), kThreads, 0, stream>>>(p, per_row);
+    conv_step_kernel<T, W, 1><<<blocks(1), kStepThreads, 0, stream>>>(p, per_row);
   return cudaGetLastError();
 }
 
