@@ -409,8 +409,8 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
 }
 
 // The helper threads' part.  In iteration i the computing threads are at tile i; the helpers
-// start the copies of tiles to come (x and dt of tile i + 4, B and C of i + 3, z of i + 2: the
-// ring's places are free then), stage tile i + 1 (kStage) and write y of tile i - 1 (kFinish).
+// start the copies of tiles to come (x and dt of tile i + 4, B and C of i + 4 or i + 3, z of
+// i + 2: the ring's places are free then), stage tile i + 1 (kStage) and write y of tile i - 1 (kFinish).
 template <class C, bool kStage, bool kFinish>
 __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4* smem, int nt,
                                         int tid) {
@@ -479,6 +479,9 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
   const int nst = max(0, p.Ns - n0);
   const T* bs = static_cast<const T*>(p.B) + (nst ? (k.t0 + brow) * p.b_stride + n0 : 0);
   const T* cs = static_cast<const T*>(p.C) + (nst ? (k.t0 + brow) * p.c_stride + n0 : 0);
+  // Copies are complete three iterations after the one that starts them.  Widened, B and C are
+  // read while their tile is staged, with x and dt; as they are, one iteration later.
+  constexpr int kBcAhead = C::kWiden ? 4 : 3;
   auto copy_bc = [&](int i) {
     if (i >= nt) return;
     const int rows = len - i * kTile - brow;
@@ -526,7 +529,7 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
     if (kStage) {
       copy(0, p.x_stride, i);
       copy(1, p.dt_stride, i);
-      if (i < 2) copy_bc(i);
+      if (i < kBcAhead - 1) copy_bc(i);
     }
     if (i == 0 && gate) copy(2, p.z_stride, 0);
     cp_async_commit();
@@ -542,7 +545,7 @@ __device__ __forceinline__ void s6_help(const S6Params& p, const Task& k, float4
     if (kStage) {
       copy(0, p.x_stride, i + kRing);
       copy(1, p.dt_stride, i + kRing);
-      copy_bc(i + 3);
+      copy_bc(i + kBcAhead);
     }
     if (gate) copy(2, p.z_stride, i + 2);
     cp_async_commit();

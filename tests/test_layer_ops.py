@@ -292,6 +292,22 @@ def test_s6_split_over_time(cuda_lib, dtype, lens, packed, dim, Ns):
     assert torch.equal(y3, y) and torch.equal(h3, hT)
 
 
+@pytest.mark.parametrize("Ns", [8, 16])
+def test_s6_repeats_its_bits_beside_other_work(cuda_lib, Ns):
+    """Chunks beside whole sequences, and a copy that keeps the memory busy: every wait is needed."""
+    x = s6_inputs(gen_of(Ns), (1, 4064), 1, 5088, Ns, torch.bfloat16)
+    other, a = torch.cuda.Stream(), torch.empty(1 << 28, device="cuda", dtype=torch.uint8)
+    y, hT = s6_run(cuda_lib, x, True)
+    ends = []
+    for i in range(6):
+        with torch.cuda.stream(other):
+            b = a.clone()
+        y2, h2 = s6_run(cuda_lib, x, True)
+        ends.append((torch.equal(y2, y), torch.equal(h2, hT)))
+        del b
+    assert ends == [(True, True)] * 6
+
+
 def test_s6_leaves_rows_behind_the_last_sequence(cuda_lib):
     for T, borders, dim in ((100, [0, 33, 60], 64), (4000, [0, 1500, 3100], 32)):
         x = s6_inputs(gen_of(T), (1, T), 2, dim, 16, torch.bfloat16)
