@@ -295,9 +295,9 @@ __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
 // Many wide rows: a persistent block whose rows arrive by bulk copies in a ring of shared
 // memory, several rows ahead, so that no row's arrival is waited for and none is held in
 // registers.  G threads have vectors i * G + thread.
-constexpr int kRingThreads = 384;
+constexpr int kRingThreads = 512, kRingBytes = 220 * 1024;
 template <typename T, bool kFp8, int NV>
-__global__ void __launch_bounds__(kRingThreads)
+__global__ void __maxnreg__(NV == 1 ? 64 : NV > 2 ? 128 : sizeof(T) == 4 ? 96 : 80)
     norm_ring_kernel(const NormParams p, int G, int slots, int slot_bytes) {
   extern __shared__ __align__(16) unsigned char ring[];
   __shared__ uint64_t full[16];
@@ -404,12 +404,19 @@ cudaError_t launch_block(const NormParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <typename T>
+int slot_of(const NormParams& p) {  // bytes of a row's tensors
+  return p.D * (int)sizeof(T) * (1 + (p.residual ? 1 : 0) + (p.gate ? 1 : 0));
+}
 template <typename T, bool kFp8, int NV>
 cudaError_t launch_ring(NormParams p, cudaStream_t stream) {
-  const int slot_bytes = p.D * (int)sizeof(T) * (1 + (p.residual ? 1 : 0) + (p.gate ? 1 : 0));
-  // two blocks an SM with four slots or more each, else one block with up to twice the memory
-  int blocks = 2, slots = 110 * 1024 / slot_bytes;
-  if (slots < 4) blocks = 1, slots = 220 * 1024 / slot_bytes;
+  const int slot_bytes = slot_of<T>(p);
+  const int G = ((p.D / 8 + NV - 1) / NV + 31) / 32 * 32;
+  // blocks of about 1024 threads an SM together, each with four slots or more; fewer where the
+  // rows are too wide for that, down to one with two slots
+  int blocks = 1024 / G < 2 ? 2 : 1024 / G > 8 ? 8 : 1024 / G;
+  while (blocks > 1 && kRingBytes / blocks / slot_bytes < 4) --blocks;
+  int slots = kRingBytes / blocks / slot_bytes;
   if (slots > 8) slots = 8;
   const auto kernel = norm_ring_kernel<T, kFp8, NV>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -418,7 +425,6 @@ cudaError_t launch_ring(NormParams p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const long long most = (long long)blocks * kSms;
   const unsigned grid = (unsigned)(p.rows < most ? p.rows : most);
-  const int G = ((p.D / 8 + NV - 1) / NV + 31) / 32 * 32;
   kernel<<<grid, G, slots * slot_bytes, stream>>>(p, G, slots, slot_bytes);
   return cudaGetLastError();
 }
@@ -430,8 +436,9 @@ cudaError_t launch_t(const NormParams& p, cudaStream_t stream) {
   if (p.D <= 128) return launch_warp<T, kFp8, 16, 1>(p, stream);
   if (p.D <= 256) return launch_warp<T, kFp8, 32, 1>(p, stream);
   if (p.D <= 512) return launch_warp<T, kFp8, 32, 2>(p, stream);
-  // the ring's copies are of whole 16-byte pieces; it pays once every block has a few rows
-  if (p.vec && p.D <= 8192 && p.rows >= 8 * kSms) {
+  // the ring's copies are of whole 16-byte pieces; it pays once every block has a few rows (8192
+  // rows of 5120, e4m3: 64 us a row per block, 52; 3531 of 11648 with a gate, e4m3: 72, 54)
+  if (p.vec && p.D <= 24 * kRingThreads && p.rows >= 8 * kSms && 2 * slot_of<T>(p) <= kRingBytes) {
     const int nv = (p.D / 8 + kRingThreads - 1) / kRingThreads;
     if (nv <= 1) return launch_ring<T, kFp8, 1>(p, stream);
     if (nv == 2) return launch_ring<T, kFp8, 2>(p, stream);

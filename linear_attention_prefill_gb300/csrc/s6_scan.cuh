@@ -194,10 +194,13 @@ __device__ __forceinline__ bool find_task(const S6Params& p, bool summary, int t
       k->n = slot / per;
       k->c = slot % per;
     } else {
+      // the last sequence that begins at the slot or before it: 32 of them tried at once
       int lo = 0, hi = p.N - 1;
       while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (border(p, mid) / p.chunk + mid <= slot) lo = mid; else hi = mid - 1;
+        const int step = (hi - lo + 31) / 32, i = lo + ((int)(threadIdx.x & 31) + 1) * step;
+        const bool before = i <= hi && border(p, i) / p.chunk + i <= slot;
+        lo += __popc(__ballot_sync(0xffffffffu, before)) * step;
+        hi = min(hi, lo + step - 1);
       }
       k->n = lo;
       k->c = slot - (border(p, lo) / p.chunk + lo);
@@ -734,8 +737,11 @@ cudaError_t launch_l(const S6Params& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   // whole sequences and first chunks need no summary, so the scan may start beside them
-  if constexpr (LPC == 4 && !kPad) {
-    if (p.lone) return launch_k<Cfg<T, 4, 1, 32, false, false>>(p, stream);
+  // One channel a lane where every CTA has an SM for itself (1024 tokens of 4864 channels, us,
+  // against two channels a lane; bf16 with Ns 4, 8, 32, 64: 37 : 56, 35 : 47, 57 : 82, 98 : 138;
+  // fp32: 29 : 47, 31 : 47, but 95 : 74, 182 : 127, where B and C are twice the bytes).
+  if constexpr (!kPad && (sizeof(T) == 2 || LPC <= 4)) {
+    if (p.lone) return launch_k<Cfg<T, LPC, 1, 32, false, false>>(p, stream);
   }
   return launch_k<Cfg<T, LPC, 2, 16, kPad, false>>(p, stream);
 }
@@ -743,7 +749,9 @@ cudaError_t launch_l(const S6Params& p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_scan(const S6Params& p, cudaStream_t stream) {
   if (p.Ns % 4)  // lanes with fewer than four states
-    return p.Ns < 16 ? launch_l<T, 4, true>(p, stream) : launch_l<T, 16, true>(p, stream);
+    return p.Ns < 16   ? launch_l<T, 4, true>(p, stream)
+           : p.Ns < 32 ? launch_l<T, 8, true>(p, stream)
+                       : launch_l<T, 16, true>(p, stream);
   if (p.Ns <= 4) return launch_l<T, 1, false>(p, stream);
   if (p.Ns <= 8) return launch_l<T, 2, false>(p, stream);
   if (p.Ns <= 16) return launch_l<T, 4, false>(p, stream);

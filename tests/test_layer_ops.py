@@ -292,6 +292,29 @@ def test_s6_split_over_time(cuda_lib, dtype, lens, packed, dim, Ns):
     assert torch.equal(y3, y) and torch.equal(h3, hT)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,dim,Ns", [
+    ((700,) + (5,) * 15, 40, 16),             # one CTA an SM
+    ((3,) * 60 + (1400, 0, 33), 96, 16),      # several
+    ((1, 900) + (20,) * 30, 64, 24), ((900, 40) + (9,) * 40, 33, 19),
+])
+def test_s6_one_long_sequence_among_short_ones(cuda_lib, dtype, lens, dim, Ns):
+    dt, g = DT[dtype], gen_of(dim + Ns)
+    T = sum(lens)
+    assert cuda_lib.gdn_s6_chunk_fwd_workspace_size(len(lens), T, dim, Ns, True) > 0
+    cu = torch.from_numpy(cu_seqlens_of(lens)).cuda()
+    x = s6_inputs(g, (1, T), len(lens), dim, Ns, dt)
+    y, hT = s6_run(cuda_lib, x, True, cu)
+    ry, ey, rh, eh = s6_ref(x, True, spans_of(lens, True, 1))
+    assert_within(hT, rh, eh, torch.float32, "hT")
+    # y reads states with the chunk sums' error too, as above
+    cm = x["C"].double().abs().amax() * Ns * rh.abs().amax() * 4
+    assert_within(y, ry, ey + max(lens) * U * 0.37 * cm * (dsilu(x["z"].double())).abs(), dt, "y")
+    h = x["h0"].clone()
+    y2, _ = s6_run(cuda_lib, dict(x, h0=h), True, cu, hT=h)
+    assert torch.equal(h, hT) and torch.equal(y2, y)
+
+
 @pytest.mark.parametrize("Ns", [8, 16])
 def test_s6_repeats_its_bits_beside_other_work(cuda_lib, Ns):
     """Chunks beside whole sequences, and a copy that keeps the memory busy: every wait is needed."""
@@ -401,7 +424,8 @@ def norm_ref(x, w, residual, gate, eps):
 
 
 NORM_ROWS = [(1, 64), (3, 8), (17, 129), (5, 128), (130, 72), (2, 1032), (9, 2560), (3, 5123), (2, 16392),
-             (1, 32768), (4, 1000), (6, 500), (1300, 520), (2500, 2560), (1217, 8192), (1216, 1001)]
+             (1, 32768), (4, 1000), (6, 500), (1300, 520), (2500, 2560), (1217, 8192), (1216, 1001),
+             (5000, 952), (1217, 4096), (1216, 12288)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
