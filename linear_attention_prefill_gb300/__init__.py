@@ -4,8 +4,9 @@ The compute lives in libgdn.so (``csrc/``, C ABI in ``include/gdn.h``); this
 package holds the Python binding with the ABI's names, the seeded synthetic
 workloads and the algorithmic byte/FLOP model.  The same kernels also run the
 Mamba-2 SSD scan (the recurrence without the delta rule's erase term), and Kimi
-Delta Attention (the delta rule with a per-key-channel gate) shares the chain.  Around them a layer's
-other operators: the short causal convolution, the S6 scan and the RMS norm (layer.py).
+Delta Attention (the delta rule with a per-key-channel gate) shares the chain.
+Around them a layer's other operators: the short causal convolution, the S6 scan
+and the RMS norm (layer.py).
 """
 from .binding import (GdnError, HostPipeline, chain_kind, gdn_chunk_fwd, gdn_chunk_fwd_host, gdn_chunk_fwd_prologue,
                       gdn_chunk_fwd_workspace_size, gdn_recurrent_step_prologue,

@@ -240,7 +240,7 @@ gdn_status run_norm(const void* x, const float* w, const void* residual, const v
   if (D > gdn::kNormMaxD)
     return fail(GDN_ERR_UNSUPPORTED, "D=%d: rows of at most %d columns", D, gdn::kNormMaxD);
   if (!(eps >= 0.f)) return fail(GDN_ERR_INVALID_ARG, "eps must be >= 0");
-  if (tokens > kMaxGrid / heads || (long long)heads * D > (1ll << 31))
+  if (tokens > kMaxGrid / heads || (long long)heads * D > 0x7fffffffll)
     return fail(GDN_ERR_INVALID_ARG, "problem too large: tokens=%lld heads=%d D=%d", tokens, heads, D);
   if (group != 0 && group != 32 && group != 64 && group != 128)
     return fail(GDN_ERR_UNSUPPORTED, "group=%d: scales cover 32, 64, 128 columns or a row (0)", group);

@@ -10,8 +10,8 @@ S6Split s6_split(int N, int T, int dim, int Ns, bool packed) {
   const long long ctas = (long long)N * tiles;
   const long long per_seq = (packed ? (long long)T : (long long)N * T) / N;  // packed: their mean
   const long long waves = (ctas + kSms - 1) / kSms;
-  // Cycles an SM takes for a token of 32 channels (measured at Ns = 16, bf16): 62 with one CTA,
-  // 117 with two, 192 with four; 74 for the two passes of a split channel, with four CTAs an SM;
+  // Cycles an SM takes for a token of 32 channels (measured at Ns = 16, bf16, 4096 tokens with
+  // the launch and the ends): 62 with one CTA, 117 with two, 192 with four; 74 for the two passes of a split channel, with four CTAs an SM;
   // 170 for the two passes along one chunk, and about 10000 for the summaries' launch and the
   // chunks' beginnings.
   const auto cost = [](long long ctas_an_sm) { return ctas_an_sm == 1 ? 62 : 48 * ctas_an_sm + 20; };

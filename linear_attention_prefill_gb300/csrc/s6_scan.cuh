@@ -25,8 +25,12 @@
 // What bounds it is the path between the schedulers and the special-function units and shared
 // memory: a lane takes 4 bytes a clock and SM from shared memory, whatever lanes share, so the
 // bytes per (channel, state) count.  A lane with four states of two channels reads 6 (D and Dx
-// 16 bytes, B and C 32, for 8 products), one with a single channel 10.  Cycles an SM takes for a
-// token of 32 channels (Ns = 16, bf16, at 1.92 GHz): SIX_CYCLES
+// 16 bytes, B and C 32, for 8 products); one with a single channel 10, or 6 where it takes bf16 B
+// and C as they are.  Cycles an SM takes for a token of 32 channels (Ns = 16, 1.92 GHz, 16384
+// tokens of 4864 channels a sequence): bf16 58 with one CTA an SM (one channel a lane), 54 with
+// two, 46 with four; fp32 62, 55 and 51.  The exponentials alone are 16, the multiply-adds 16,
+// the reads 24 or more.  4096 tokens of 5120 channels take 144 us; their bytes alone would take
+// 25.
 //
 // Splitting over time.  A CTA per 32 channels leaves SMs idle when there are few of them.
 // Channels beyond the whole-sequence ones are split over time: a first launch computes the
@@ -71,7 +75,8 @@ struct Cfg {
   // four states' B and C of a token: one piece in bf16, two in fp32.  They are read where they
   // arrive, except that lanes with two channels have bf16 widened for them by the helpers, into
   // two further tiles: there instructions count more than bytes (51 cycles against 55 where the
-  // lanes widen their own), with one channel a lane the bytes do (PACKED_LONE).
+  // lanes widen their own), with one channel a lane the bytes do (the recurrence alone: 52 cycles
+  // packed, 58 widened).
   static constexpr bool kWiden = sizeof(T) == 2 && kWidth > 1, kPacked = sizeof(T) == 2 && !kWiden;
   static constexpr int kFours = kTile * LPC, kPerHelper = (kFours + kHelpers - 1) / kHelpers;
   static constexpr int kBcPieces = (int)sizeof(T) / 2, kBcTile = kFours * kBcPieces;

@@ -48,6 +48,8 @@ def _on(stream, x):
             raise ValueError("a stream needs operands on a CUDA device")
         stream = (torch.cuda.ExternalStream(int(stream), device=x.device) if int(stream) else
                   torch.cuda.default_stream(x.device))
+    elif isinstance(x, torch.Tensor) and x.device != stream.device:
+        raise ValueError(f"x is on {x.device}, the stream on {stream.device}")
     return torch.cuda.stream(stream)
 
 
@@ -138,8 +140,9 @@ def gdn_rms_norm_fwd(x, weight, residual=None, gate=None, y=None, residual_out=N
 
     r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight * silu(gate).  x, residual, gate
     are bf16 or fp32, all the same; weight [D] fp32.  x and gate may be slices: rows a
-    constant stride apart, or [..., H, D] with dense H D and a constant stride before it.  residual is contiguous and residual_out (a fresh tensor, or residual itself:
-    in place) takes r in x's type.  out_dtype torch.float8_e4m3fn gives y in 8 bits with fp32
+    constant stride apart, or [..., H, D] with dense H D and a constant stride before it.
+    residual is contiguous and residual_out (a fresh tensor, or residual itself: in place) takes
+    r in x's type.  out_dtype torch.float8_e4m3fn gives y in 8 bits with fp32
     scales [..., ceil(D / group)], one per ``group`` (32, 64, 128) columns or one a row (None):
     scale = max|y| / 448 (1 for zeros).  scales and residual_out are None where there are none.
     """

@@ -138,6 +138,7 @@ def norm(lib, fp8=False, f32=False, **kw):
     (dict(x=at(0, 1)), 1), (dict(w=at(1, 2)), 1), (dict(res=at(4, 1), out=at(5)), 1),
     (dict(y=at(0)), 1), (dict(res=at(4), out=at(4, 32)), 1), (dict(res=at(4), out=at(0)), 1),
     (dict(res=at(2), out=at(2)), 1), (dict(tokens=1 << 40), 1), (dict(heads=1 << 20, D=32768), 1),
+    (dict(tokens=1, heads=1 << 16, D=32768, xs=1 << 31), 1),
 ])
 def test_norm_rejects(lib, case, status, fp8, f32):
     assert norm(lib, fp8, f32, **case) == status
@@ -148,3 +149,28 @@ def test_norm_e4m3_rejects(lib):
     assert norm(lib, True, scales=None) == 1 and norm(lib, True, group=48) == 2
     assert norm(lib, True, scales=at(2)) == 1 and norm(lib, True, scales=at(3, 2)) == 1
     assert norm(lib, True, tokens=0) == 0 and norm(lib, tokens=0, x=None, w=None, y=None) == 0
+
+
+def test_binding_refuses_what_is_not_on_a_gpu(lib):
+    import torch
+
+    import linear_attention_prefill_gb300 as lap
+    x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
+    A, B, h = torch.zeros(8, 16), torch.zeros(1, 4, 16), torch.zeros(1, 8, 16)
+    for call in (lambda **k: lap.gdn_short_conv_fwd(x, w, **k),
+                 lambda **k: lap.gdn_short_conv_step(x[:, 0], w, x[:, :3], **k),
+                 lambda **k: lap.gdn_s6_chunk_fwd(x, x, A, B, B, **k),
+                 lambda **k: lap.gdn_s6_recurrent_step(x[:, 0], x[:, 0], A, B[:, 0], B[:, 0], h, **k),
+                 lambda **k: lap.gdn_rms_norm_fwd(x, w[:, 0], **k)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+        with pytest.raises(ValueError, match="CUDA"):
+            call(stream=1)
+    with pytest.raises(TypeError):
+        lap.gdn_rms_norm_fwd([0.0], w[:, 0])
+    with pytest.raises(ValueError):
+        lap.gdn_short_conv_fwd(x, w, activation="relu")
+    with pytest.raises(ValueError):
+        lap.gdn_rms_norm_fwd(x, w[:, 0], group=32)
+    with pytest.raises(TypeError):
+        lap.gdn_rms_norm_fwd(x, w[:, 0], out_dtype=torch.float16)
