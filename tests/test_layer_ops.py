@@ -618,6 +618,124 @@ def test_calls_on_a_side_stream(cuda_lib):
             assert s is None and t is None or torch.equal(s, t)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [1, 2, 3, 5, 31, 33])
+def test_narrow_rows(cuda_lib, dtype, D):
+    dt, g = DT[dtype], gen_of(D)
+    x, w = randn(g, 2, 9, D, dtype=dt), randn(g, D, 3)
+    s0 = randn(g, 2, 2, D, dtype=dt)
+    y, sT = cuda_lib.gdn_short_conv_fwd(x, w, s0=s0)
+    ref, err, st = conv_ref(x, w, None, s0, "silu", spans_of((9, 9), False, 2))
+    assert_within(y, ref, err, dt, "convolution")
+    assert torch.equal(sT.double(), st)
+    for Ns in (1, 2, 16):
+        z = s6_inputs(g, (2, 9), 2, D, Ns, dt)
+        y, hT = s6_run(cuda_lib, z, True)
+        ry, ey, rh, eh = s6_ref(z, True, spans_of((9, 9), False, 2))
+        assert_within(y, ry, ey, dt, "scan")
+        assert_within(hT, rh, eh, torch.float32, "state")
+    wn, gate = randn(g, D), randn(g, 2, 9, D, dtype=dt)
+    ref, rel, _ = norm_ref(x, wn, None, gate, 1e-6)
+    assert_within(cuda_lib.gdn_rms_norm_fwd(x, wn, gate=gate)[0], ref, rel * ref.abs(), dt, "norm")
+    for group in (None, 32, 128):
+        q, scales, _ = cuda_lib.gdn_rms_norm_fwd(x, wn, gate=gate, out_dtype=E4M3, group=group)
+        width = group or D
+        rs = torch.nn.functional.pad(ref, (0, -D % width)).unflatten(-1, (-1, width)).abs().amax(-1) / 448
+        assert ((scales.double() - rs).abs() <= (rel.amax() + 2 * U) * rs).all()
+        v = ref / rs.repeat_interleave(width, -1)[..., :D]
+        off = (2 * rel.amax() + 4 * U) * v.abs()
+        assert ((q.double() - v).abs() <= off + 2.0 ** -4 * (v.abs() + off) + 2.0 ** -10).all()
+
+
+def test_offsets_beyond_32_bits(cuda_lib):
+    """Tensors of more than 2^31 elements: the last rows against the definition."""
+    g, bf = gen_of(31), torch.bfloat16
+    D, T = 32768, 66016
+    x = torch.zeros(1, T, D, dtype=bf, device="cuda")
+    x[:, -40:] = randn(g, 1, 40, D, dtype=bf)
+    assert x.numel() > 2 ** 31
+    w, wn = randn(g, D, 4), randn(g, D)
+    y, sT = cuda_lib.gdn_short_conv_fwd(x, w)
+    ref, err, st = conv_ref(x[:, -40:], w, None, None, "silu", [(0, 0, 40)])
+    assert_within(y[:, -40:], ref, err, bf, "convolution")
+    assert torch.equal(sT.double(), st)
+    del y
+    y = cuda_lib.gdn_rms_norm_fwd(x, wn, x)[0]
+    ref, rel, _ = norm_ref(x[:, -40:], wn, x[:, -40:], None, 1e-6)
+    assert_within(y[:, -40:], ref, rel * ref.abs(), bf, "norm")
+    del y
+    n, d = T // 32, 16  # the same memory as sequences of 32 tokens; B, C and dt far apart too
+    z = s6_inputs(g, (1, 32), 1, D, 8, bf)
+    rows = x.view(-1)[:n * 32 * D].view(n, 32, D)
+    rows[-1] = z["x"][0]
+    bc = torch.zeros(n, 32, D, dtype=bf, device="cuda")[..., D - d:]
+    bc[-1, :, :8], bc[-1, :, 8:] = z["B"][0], z["C"][0]
+    h0 = torch.zeros(n, D, 8, device="cuda")
+    h0[-1] = z["h0"][0]
+    step = dict(z, x=rows, dt=rows, z=None, B=bc[..., :8], C=bc[..., 8:], h0=h0)
+    y, hT = s6_run(cuda_lib, step, True, gate=False)
+    ry, ey, rh, eh = s6_ref(dict(z, dt=z["x"], z=None), True, [(0, 0, 32)], gate=False)
+    assert_within(y[-1:], ry, ey, bf, "scan")
+    assert_within(hT[-1:], rh, eh, torch.float32, "state")
+    del y, hT, rows, step, bc, x, h0
+    N, dim, Ns = 2200, 16384, 64
+    h = torch.zeros(N, dim, Ns, device="cuda")
+    assert h.numel() > 2 ** 31
+    z = s6_inputs(g, (1, 1), 1, dim, Ns, bf)
+    h[-1] = z["h0"][0]
+    many = {k: z[k][0].expand(N, -1).contiguous() for k in ("x", "dt", "z", "B", "C")}
+    y = cuda_lib.gdn_s6_recurrent_step(many["x"], many["dt"], z["A"], many["B"], many["C"], h, z["D"], many["z"],
+                                       z["dt_bias"], dt_softplus=True)
+    ry, ey, rh, eh = s6_ref(z, True, [(0, 0, 1)])
+    assert_within(y[-1:, None], ry, ey, bf, "step")
+    assert_within(h[-1:], rh, eh, torch.float32, "state")
+    del h, many
+    s = torch.zeros(22000, 3, D, dtype=bf, device="cuda")
+    assert s.numel() > 2 ** 31
+    s[-1] = randn(g, 3, D, dtype=bf)
+    last, x1 = s[-1:].clone(), randn(g, 1, D, dtype=bf)
+    y = cuda_lib.gdn_short_conv_step(x1.expand(22000, -1).contiguous(), w, s)
+    ref, err, st = conv_ref(x1[:, None], w, None, last, "silu", [(0, 0, 1)])
+    assert_within(y[-1:, None], ref, err, bf, "step")
+    assert torch.equal(s[-1:].double(), st)
+
+
+def test_two_graphs_replayed_in_turn_and_two_threads(cuda_lib):
+    """Each graph has its own workspace, each thread its own stream."""
+    import threading
+    xs = [s6_inputs(gen_of(40 + i), (1, 1500), 1, 64, 16, torch.bfloat16) for i in range(2)]
+    want = [s6_run(cuda_lib, x, True) for x in xs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(s6_run(cuda_lib, x, True))
+        graphs.append(graph)
+    sides = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        for graph, side in zip(graphs, sides):
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for o, w in zip(outs, want) for a, b in zip(o, w))
+    bad = []
+
+    def work(i):
+        for _ in range(50):
+            y, hT = s6_run(cuda_lib, xs[i], True, stream=sides[i])
+            sides[i].synchronize()
+            if not (torch.equal(y, want[i][0]) and torch.equal(hT, want[i][1])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_empty_batches(cuda_lib):
     dev, bf = "cuda", torch.bfloat16
     w, A = torch.ones(16, 4, device=dev), -torch.ones(16, 8, device=dev)
