@@ -280,9 +280,15 @@ gdn_status run_norm(const void* x, const float* w, const void* residual, const v
   p.group = span < D ? span : D;
   p.groups = (D + p.group - 1) / p.group;
   const bool one = tokens <= 1;
-  p.vec = D % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) &&
-          aligned(gate, 16) && aligned(w, 16) && aligned(y, fp8 ? 8 : 16) &&
-          (one || x_stride * elem % 16 == 0) && (one || !gate || gate_stride * elem % 16 == 0);
+  // the widest accesses that every tensor allows: of 8, 4 or 2 columns, 16 bytes at most
+  const auto fits = [&](int by) {
+    const size_t wide = by * elem < 16 ? by * elem : 16, of_w = by * 4 < 16 ? by * 4 : 16;
+    return D % by == 0 && aligned(x, wide) && aligned(residual, wide) && aligned(residual_out, wide) &&
+           aligned(gate, wide) && aligned(w, of_w) && aligned(y, fp8 ? by : wide) &&
+           (one || x_stride * elem % (long long)wide == 0) &&
+           (one || !gate || gate_stride * elem % (long long)wide == 0);
+  };
+  p.by = fits(8) ? 8 : fits(4) ? 4 : fits(2) ? 2 : 1;
   p.err = nullptr;
   const cudaError_t e = gdn::launch_norm(p, f32, fp8, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the RMS norm");

@@ -34,6 +34,35 @@ struct Raw8<__nv_bfloat16> {
     v = *reinterpret_cast<const uint4*>(p);
   }
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  // the first n of 8, n a multiple of the `by` (4, 2 or 1) elements of an access; the others read
+  // as zero
+  __device__ __forceinline__ void load_by(const __nv_bfloat16* p, int n, int by) {
+    if (by == 1) {
+      load_n(p, n);
+    } else if (by == 2) {
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+      v = make_uint4(n > 0 ? q[0] : 0u, n > 2 ? q[1] : 0u, n > 4 ? q[2] : 0u, n > 6 ? q[3] : 0u);
+    } else {
+      const uint2 zero = make_uint2(0u, 0u);
+      const uint2 a = n > 0 ? *reinterpret_cast<const uint2*>(p) : zero;
+      const uint2 b = n > 4 ? *reinterpret_cast<const uint2*>(p + 4) : zero;
+      v = make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+  __device__ __forceinline__ void store_by(__nv_bfloat16* p, int n, int by) const {
+    if (by == 1) {
+      store_n(p, n);
+    } else if (by == 2) {
+      uint32_t* q = reinterpret_cast<uint32_t*>(p);
+      if (n > 0) q[0] = v.x;
+      if (n > 2) q[1] = v.y;
+      if (n > 4) q[2] = v.z;
+      if (n > 6) q[3] = v.w;
+    } else {
+      if (n > 0) *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+      if (n > 4) *reinterpret_cast<uint2*>(p + 4) = make_uint2(v.z, v.w);
+    }
+  }
   // element by element, the first n of 8 (n <= 0: none); the others read as zero
   __device__ __forceinline__ void load_n(const __nv_bfloat16* p, int n) {
     const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
@@ -72,6 +101,36 @@ struct Raw8<float> {
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void load_by(const float* p, int n, int by) {
+    if (by == 1) {
+      load_n(p, n);
+    } else if (by == 2) {
+      const float2* q = reinterpret_cast<const float2*>(p);
+      const float2 zero = make_float2(0.f, 0.f);
+      const float2 c = n > 0 ? q[0] : zero, d = n > 2 ? q[1] : zero;
+      const float2 e = n > 4 ? q[2] : zero, f = n > 6 ? q[3] : zero;
+      a = make_float4(c.x, c.y, d.x, d.y);
+      b = make_float4(e.x, e.y, f.x, f.y);
+    } else {
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      a = n > 0 ? reinterpret_cast<const float4*>(p)[0] : zero;
+      b = n > 4 ? reinterpret_cast<const float4*>(p)[1] : zero;
+    }
+  }
+  __device__ __forceinline__ void store_by(float* p, int n, int by) const {
+    if (by == 1) {
+      store_n(p, n);
+    } else if (by == 2) {
+      float2* q = reinterpret_cast<float2*>(p);
+      if (n > 0) q[0] = make_float2(a.x, a.y);
+      if (n > 2) q[1] = make_float2(a.z, a.w);
+      if (n > 4) q[2] = make_float2(b.x, b.y);
+      if (n > 6) q[3] = make_float2(b.z, b.w);
+    } else {
+      if (n > 0) reinterpret_cast<float4*>(p)[0] = a;
+      if (n > 4) reinterpret_cast<float4*>(p)[1] = b;
+    }
   }
   __device__ __forceinline__ void load_n(const float* p, int n) {
     float o[8];
@@ -170,17 +229,17 @@ __device__ __forceinline__ Raw8<T> raw_of(const unsigned long long (&v)[4]) {
   r.set(o);
   return r;
 }
-// The first n of 8 elements at p, by one wide access where the caller's `vec` says that p
-// is 16-byte aligned and n >= 8.
+// The first n of 8 elements at p in accesses of `by` elements (8, 4, 2 or 1): p is aligned to
+// them (at most 16 bytes) and n a multiple of `by`, or larger.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* p, int n, bool vec) {
+__device__ __forceinline__ Raw8<T> load8(const T* p, int n, int by) {
   Raw8<T> r;
-  if (vec) r.load(p); else r.load_n(p, n);
+  if (by == 8) r.load(p); else r.load_by(p, n, by);
   return r;
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int n, bool vec) {
-  if (vec) r.store(p); else r.store_n(p, n);
+__device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int n, int by) {
+  if (by == 8) r.store(p); else r.store_by(p, n, by);
 }
 
 // Four states of the recurrence (n of them exist): rows of Ns floats, 16-byte aligned bases.

@@ -78,7 +78,7 @@ struct NormParams {
   int group, groups;                // columns per scale (D: one scale a row), scales a row
   int group_log;                    // log2 of a group below D
   float eps, inv_d;                 // inv_d: 1 / D
-  int vec;                          // every 8-column access is aligned and D is a multiple of 8
+  int by;                           // columns of an access (8, 4, 2, 1): D is a multiple, all are aligned
   unsigned* err;                    // device error word: bounded waits record a timeout here (set
                                     // by the launch that has them)
 };

@@ -42,12 +42,19 @@ __device__ __forceinline__ uint32_t e4m3x2(f32x2 v) {
 }
 // One vector's e4m3 of y * inv.
 __device__ __forceinline__ void store_e4m3(uint8_t* q, const f32x2 (&y)[4], float inv, int n,
-                                           bool vec) {
+                                           int by) {
   const f32x2 s = dup2(inv);
   const uint2 v = make_uint2(e4m3x2(mul2(y[0], s)) | (e4m3x2(mul2(y[1], s)) << 16),
                              e4m3x2(mul2(y[2], s)) | (e4m3x2(mul2(y[3], s)) << 16));
-  if (vec) {
+  if (by == 8) {
     *reinterpret_cast<uint2*>(q) = v;
+  } else if (by == 4) {
+    if (n > 0) reinterpret_cast<uint32_t*>(q)[0] = v.x;
+    if (n > 4) reinterpret_cast<uint32_t*>(q)[1] = v.y;
+  } else if (by == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (2 * j < n) reinterpret_cast<uint16_t*>(q)[j] = (uint16_t)((j < 2 ? v.x : v.y) >> (16 * (j & 1)));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -86,12 +93,12 @@ __device__ __forceinline__ float reduce_row(float v, int G, float* s) {
 
 // What a row is after its sum of squares is known: y of every vector, stored.  r: the row's
 // vectors; load_w(i), load_gate(i): vector i of w and of the gate; n[i]: columns that exist
-// (whole vectors with p.vec); some: there is a row.
-template <typename T, bool kFp8, bool kBlock, int NV, typename LoadW, typename LoadGate>
+// (whole vectors with kWhole, where p.by is 8); some: there is a row.
+template <typename T, bool kFp8, bool kBlock, bool kWhole, int NV, typename LoadW, typename LoadGate>
 __device__ __forceinline__ void finish(const NormParams& p, long long row, bool some, int G,
                                        int lane, f32x2 (&r)[NV][4], const int (&n)[NV], float ss,
                                        float* s_max, LoadW load_w, LoadGate load_gate) {
-  const bool vec = p.vec;
+  const int by = kWhole ? 8 : p.by;
   const f32x2 rstd = dup2(rsqrtf(ss * p.inv_d + p.eps));
   const long long at = row * p.D + lane * 8;
   T* y = static_cast<T*>(p.y) + at;
@@ -111,12 +118,12 @@ __device__ __forceinline__ void finish(const NormParams& p, long long row, bool 
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[i][j] = mul2(r[i][j], silu2(q[j]));
       }
-      if (!kFp8) store8(y + i * G * 8, raw_of<T>(r[i]), n[i], vec);
+      if (!kFp8) store8(y + i * G * 8, raw_of<T>(r[i]), n[i], by);
     }
     if (kFp8) {
       float m = 0.f;
       if (here) {
-        if (!vec) {  // columns that do not exist were read as zeros, but a row of NaN has none
+        if (by != 8) {  // columns that do not exist were read as zeros, but a row of NaN has none
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float a, b;
@@ -131,7 +138,7 @@ __device__ __forceinline__ void finish(const NormParams& p, long long row, bool 
           m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
         if (here) {
           const float scale = scale_of(m);
-          store_e4m3(y8 + i * G * 8, r[i], rcp(scale), n[i], vec);
+          store_e4m3(y8 + i * G * 8, r[i], rcp(scale), n[i], by);
           const int c = (i * G + lane) * 8;
           if ((c & (p.group - 1)) == 0) scales[c >> p.group_log] = scale;
         }
@@ -146,12 +153,12 @@ __device__ __forceinline__ void finish(const NormParams& p, long long row, bool 
     if (some && lane == 0) *scales = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (some && n[i] > 0) store_e4m3(y8 + i * G * 8, r[i], inv, n[i], vec);
+      if (some && n[i] > 0) store_e4m3(y8 + i * G * 8, r[i], inv, n[i], by);
   }
 }
 
 // x + residual of one vector, the residual's update stored; adds the squares to ss.
-template <typename T>
+template <typename T, bool kWhole>
 __device__ __forceinline__ void take(const NormParams& p, T* out, const Raw8<T>& x,
                                      const Raw8<T>& res, int n, f32x2 (&r)[4], f32x2& ss) {
   pairs_of(x, r);
@@ -160,7 +167,7 @@ __device__ __forceinline__ void take(const NormParams& p, T* out, const Raw8<T>&
     pairs_of(res, q);
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] = add2(r[j], q[j]);
-    store8(out, raw_of<T>(r), n, p.vec);
+    store8(out, raw_of<T>(r), n, kWhole ? 8 : p.by);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) ss = fma2(r[j], r[j], ss);
@@ -169,19 +176,19 @@ __device__ __forceinline__ void take(const NormParams& p, T* out, const Raw8<T>&
 // Rows within a warp: G lanes a row, NV vectors of 8 columns a lane: vector i * G + lane.  A
 // block walks its rows, the next one is loaded while the present one is reduced, and w stays in
 // registers.
-template <typename T, bool kFp8, int G, int NV>
+template <typename T, bool kFp8, bool kWhole, int G, int NV>
 __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
   constexpr int per_block = 128 / G;
   const int lane = threadIdx.x % G;
   const long long step = (long long)gridDim.x * per_block;
-  const bool vec = p.vec;
+  const int by = kWhole ? 8 : p.by;
   int n[NV];
   f32x2 w[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * G + lane) * 8;
     n[i] = p.D - c;
-    if (n[i] > 0) pairs_of(load8(p.w + c, n[i], vec), w[i]);
+    if (n[i] > 0) pairs_of(load8(p.w + c, n[i], by), w[i]);
   }
   Raw8<T> x[NV], res[NV], gate[NV];
   const long long row0 = (long long)blockIdx.x * per_block + threadIdx.x / G;
@@ -203,9 +210,9 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (n[i] <= 0) continue;
-      x[i] = load8(xr + i * G * 8, n[i], vec);
-      if (p.residual) res[i] = load8(rp + i * G * 8, n[i], vec);
-      if (p.gate) gate[i] = load8(gr + i * G * 8, n[i], vec);
+      x[i] = load8(xr + i * G * 8, n[i], by);
+      if (p.residual) res[i] = load8(rp + i * G * 8, n[i], by);
+      if (p.gate) gate[i] = load8(gr + i * G * 8, n[i], by);
     }
     rp += step * p.D;
   };
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (some && n[i] > 0) {
-        take(p, out + i * G * 8, x[i], res[i], n[i], r[i], ss);
+        take<T, kWhole>(p, out + i * G * 8, x[i], res[i], n[i], r[i], ss);
         g[i] = gate[i];
       }
     }
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
     float s0, s1;
     unpack2(ss, s0, s1);
     const float sum = reduce_row<false, false>(s0 + s1, G, nullptr);
-    finish<T, kFp8, false, NV>(
+    finish<T, kFp8, false, kWhole, NV>(
         p, row, some, G, lane, r, n, sum, nullptr,
         [&](int i, f32x2 (&q)[4]) {
 #pragma unroll
@@ -240,13 +247,13 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
 
 // A row per block of G threads, NV vectors a thread.  Up to 8192 columns w and the gate are
 // loaded with the row; wider blocks (up to 1024 threads) have registers for the row only.
-template <typename T, bool kFp8, int NV>
+template <typename T, bool kFp8, bool kWhole, int NV>
 __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
     norm_block_kernel(const NormParams p, int G) {
   constexpr bool kWide = NV == 4;
   __shared__ float s_sum[32], s_max[32];
   const int lane = threadIdx.x;
-  const bool vec = p.vec;
+  const int by = kWhole ? 8 : p.by;
   const long long row = blockIdx.x;
   const long long token = p.heads == 1 ? row : row / p.heads;
   const long long col = (row - token * p.heads) * p.D + lane * 8;
@@ -260,34 +267,34 @@ __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
     const int c = (i * G + lane) * 8;
     n[i] = p.D - c;
     if (n[i] <= 0) continue;
-    x[i] = load8(xp + i * G * 8, n[i], vec);
-    if (p.residual) res[i] = load8(static_cast<const T*>(p.residual) + row * p.D + c, n[i], vec);
+    x[i] = load8(xp + i * G * 8, n[i], by);
+    if (p.residual) res[i] = load8(static_cast<const T*>(p.residual) + row * p.D + c, n[i], by);
   }
   if (!kWide) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (n[i] <= 0) continue;
-      if (p.gate) g[i] = load8(gp + i * G * 8, n[i], vec);
-      w[i] = load8(p.w + (i * G + lane) * 8, n[i], vec);
+      if (p.gate) g[i] = load8(gp + i * G * 8, n[i], by);
+      w[i] = load8(p.w + (i * G + lane) * 8, n[i], by);
     }
   }
   f32x2 r[NV][4], ss = 0ull;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (n[i] > 0)
-      take(p, static_cast<T*>(p.residual_out) + row * p.D + (i * G + lane) * 8, x[i], res[i], n[i],
+      take<T, kWhole>(p, static_cast<T*>(p.residual_out) + row * p.D + (i * G + lane) * 8, x[i], res[i], n[i],
            r[i], ss);
   float s0, s1;
   unpack2(ss, s0, s1);
   const float sum = reduce_row<false, true>(s0 + s1, G, s_sum);
-  finish<T, kFp8, true, NV>(
+  finish<T, kFp8, true, kWhole, NV>(
       p, row, true, G, lane, r, n, sum, s_max,
       [&](int i, f32x2 (&q)[4]) {
-        if (kWide) w[0] = load8(p.w + (i * G + lane) * 8, n[i], vec);
+        if (kWide) w[0] = load8(p.w + (i * G + lane) * 8, n[i], by);
         pairs_of(w[kWide ? 0 : i], q);
       },
       [&](int i, f32x2 (&q)[4]) {
-        if (kWide) g[0] = load8(gp + i * G * 8, n[i], vec);
+        if (kWide) g[0] = load8(gp + i * G * 8, n[i], by);
         pairs_of(g[kWide ? 0 : i], q);
       });
 }
@@ -358,7 +365,7 @@ __global__ void __maxnreg__(NV == 1 ? 64 : NV > 2 ? 128 : sizeof(T) == 4 ? 96 : 
       x.load(q);
       if (p.residual) res.load(q + p.D);
       if (p.gate) g[i].load(q + (p.residual ? 2 : 1) * p.D);
-      take(p, out + i * G * 8, x, res, 8, r[i], ss);
+      take<T, true>(p, out + i * G * 8, x, res, 8, r[i], ss);
     }
     float s0, s1;
     unpack2(ss, s0, s1);
@@ -369,7 +376,7 @@ __global__ void __maxnreg__(NV == 1 ? 64 : NV > 2 ? 128 : sizeof(T) == 4 ? 96 : 
       fence_proxy_async();
       fetch(next, s);
     }
-    finish<T, kFp8, true, NV>(
+    finish<T, kFp8, true, true, NV>(
         p, row, true, G, tid, r, n, sum, s_max[turn],
         [&](int i, f32x2 (&q)[4]) { pairs_of(w[i], q); },
         [&](int i, f32x2 (&q)[4]) { pairs_of(g[i], q); });
@@ -379,7 +386,7 @@ __global__ void __maxnreg__(NV == 1 ? 64 : NV > 2 ? 128 : sizeof(T) == 4 ? 96 : 
 
 template <typename T, bool kFp8, int G, int NV>
 cudaError_t launch_warp(const NormParams& p, cudaStream_t stream) {
-  const auto kernel = norm_warp_kernel<T, kFp8, G, NV>;
+  const auto kernel = p.by == 8 ? norm_warp_kernel<T, kFp8, true, G, NV> : norm_warp_kernel<T, kFp8, false, G, NV>;
   static_assert(32 % G == 0, "rows do not cross warps");
   // as many blocks as are resident together; each takes its rows in turn
   int resident = 0;
@@ -391,16 +398,17 @@ cudaError_t launch_warp(const NormParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename T, bool kFp8>
+template <typename T, bool kFp8, bool kWhole>
 cudaError_t launch_block(const NormParams& p, cudaStream_t stream) {
   // one vector a thread for few rows (latency), two for many; four for the widest
   const int nvec = (p.D + 7) / 8;
   const int nv = nvec > 1024 ? 4 : p.rows <= kSms ? 1 : 2;
   const int G = ((nvec + nv - 1) / nv + 31) / 32 * 32;
   const unsigned grid = (unsigned)p.rows;
-  if (nv == 1) norm_block_kernel<T, kFp8, 1><<<grid, G, 0, stream>>>(p, G);
-  else if (nv == 2) norm_block_kernel<T, kFp8, 2><<<grid, G, 0, stream>>>(p, G);
-  else norm_block_kernel<T, kFp8, 4><<<grid, G, 0, stream>>>(p, G);
+  const auto kernel = nv == 1   ? norm_block_kernel<T, kFp8, kWhole, 1>
+                      : nv == 2 ? norm_block_kernel<T, kFp8, kWhole, 2>
+                                : norm_block_kernel<T, kFp8, kWhole, 4>;
+  kernel<<<grid, G, 0, stream>>>(p, G);
   return cudaGetLastError();
 }
 
@@ -438,13 +446,13 @@ cudaError_t launch_t(const NormParams& p, cudaStream_t stream) {
   if (p.D <= 512) return launch_warp<T, kFp8, 32, 2>(p, stream);
   // the ring's copies are of whole 16-byte pieces; it pays once every block has a few rows (8192
   // rows of 5120, e4m3: 64 us a row per block, 52; 3531 of 11648 with a gate, e4m3: 72, 54)
-  if (p.vec && p.D <= 24 * kRingThreads && p.rows >= 8 * kSms && 2 * slot_of<T>(p) <= kRingBytes) {
+  if (p.by == 8 && p.D <= 24 * kRingThreads && p.rows >= 8 * kSms && 2 * slot_of<T>(p) <= kRingBytes) {
     const int nv = (p.D / 8 + kRingThreads - 1) / kRingThreads;
     if (nv <= 1) return launch_ring<T, kFp8, 1>(p, stream);
     if (nv == 2) return launch_ring<T, kFp8, 2>(p, stream);
     return launch_ring<T, kFp8, 3>(p, stream);
   }
-  return launch_block<T, kFp8>(p, stream);
+  return p.by == 8 ? launch_block<T, kFp8, true>(p, stream) : launch_block<T, kFp8, false>(p, stream);
 }
 
 }  // namespace

@@ -425,7 +425,7 @@ def norm_ref(x, w, residual, gate, eps):
 
 NORM_ROWS = [(1, 64), (3, 8), (17, 129), (5, 128), (130, 72), (2, 1032), (9, 2560), (3, 5123), (2, 16392),
              (1, 32768), (4, 1000), (6, 500), (1300, 520), (2500, 2560), (1217, 8192), (1216, 1001),
-             (5000, 952), (1217, 4096), (1216, 12288)]
+             (5000, 952), (1217, 4096), (1216, 12288), (70, 12900), (40, 250), (33, 1330), (9, 36), (5, 22)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
