@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
   auto load_row = [&](long long row) {
     const T *xr = xp, *gr = gp;
     if (heads) {
-      const long long token = row / p.heads, col = (row - token * p.heads) * p.D;
+      // (rows fit 31 bits; with a 64-bit quotient 131072 heads of 64: 12.7 us against 10.9)
+      const long long token = (unsigned)row / (unsigned)p.heads, col = (row - token * p.heads) * p.D;
       xr += token * p.x_stride + col;
       gr += token * p.gate_stride + col;
     } else {
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
   const int lane = threadIdx.x;
   const int by = kWhole ? 8 : p.by;
   const long long row = blockIdx.x;
-  const long long token = p.heads == 1 ? row : row / p.heads;
+  const long long token = p.heads == 1 ? row : (unsigned)row / (unsigned)p.heads;
   const long long col = (row - token * p.heads) * p.D + lane * 8;
   const T* xp = static_cast<const T*>(p.x) + token * p.x_stride + col;
   const T* gp = static_cast<const T*>(p.gate) + token * p.gate_stride + col;
@@ -321,7 +322,7 @@ __global__ void __maxnreg__(NV == 1 ? 64 : NV > 2 ? 128 : sizeof(T) == 4 ? 96 : 
     if (n[i] > 0) w[i].load(p.w + c);
   }
   auto fetch = [&](long long row, int s) {  // one thread: the row's copies into slot s
-    const long long token = p.heads == 1 ? row : row / p.heads;
+    const long long token = p.heads == 1 ? row : (unsigned)row / (unsigned)p.heads;
     const long long col = (row - token * p.heads) * p.D;
     unsigned char* dst = ring + s * slot_bytes;
     mbar_expect_tx(&full[s], slot_bytes);

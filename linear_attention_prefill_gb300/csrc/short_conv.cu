@@ -262,22 +262,21 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(const ConvParams p
 // One token per sequence: a thread holds the windows of 4 channels of kSeqs sequences and
 // shifts their states in place.  kSeqs > 1 shares the filter, which is as many bytes as the
 // window and the output of one sequence.
-template <typename T, int W, int kSeqs>
+template <typename T, int W, int kSeqs, bool kVec>
 __global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvParams p, int per_row) {
   const long long id = (long long)blockIdx.x * kStepThreads + threadIdx.x;
   const long long first = id / per_row * kSeqs;
   if (first >= p.N) return;
   const int c = (int)(id % per_row) * kChans;
-  const int left = p.D - c;
-  const bool vec = p.vec;
+  const int left = kVec ? kChans : p.D - c;
   Piece<T> r[kSeqs][W];
 #pragma unroll
   for (int i = 0; i < kSeqs; ++i) {
     if (first + i >= p.N) break;
     const T* s = static_cast<const T*>(p.sT) + (first + i) * (W - 1) * p.D + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) r[i][j].load(s + (long long)j * p.D, left, vec);
-    r[i][W - 1].load(static_cast<const T*>(p.x) + (first + i) * p.x_stride + c, left, vec);
+    for (int j = 0; j < W - 1; ++j) r[i][j].load(s + (long long)j * p.D, left, kVec);
+    r[i][W - 1].load(static_cast<const T*>(p.x) + (first + i) * p.x_stride + c, left, kVec);
   }
   f32x2 f[W][kChans / 2], bias[kChans / 2];
   load_filter<W>(p.w, c, left, f);
@@ -289,10 +288,10 @@ __global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvParam
 #pragma unroll
     for (int j = 0; j < W; ++j) r[i][j].get(win[j]);
     filter<T, W>(f, bias, win, p.silu)
-        .store(static_cast<T*>(p.y) + (first + i) * p.D + c, left, vec);
+        .store(static_cast<T*>(p.y) + (first + i) * p.D + c, left, kVec);
     T* s = static_cast<T*>(p.sT) + (first + i) * (W - 1) * p.D + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) r[i][j + 1].store(s + (long long)j * p.D, left, vec);
+    for (int j = 0; j < W - 1; ++j) r[i][j + 1].store(s + (long long)j * p.D, left, kVec);
   }
 }
 
@@ -335,8 +334,8 @@ cudaError_t launch_t(const ConvParams& p, cudaStream_t stream) {
   return launch_w<T, 2>(p, stream);
 }
 
-template <typename T, int W>
-cudaError_t launch_step_w(const ConvParams& p, cudaStream_t stream) {
+template <typename T, int W, bool kVec>
+cudaError_t launch_step_v(const ConvParams& p, cudaStream_t stream) {
   const int per_row = (p.D + kChans - 1) / kChans;
   const auto blocks = [&](int seqs) {
     return (unsigned)(((long long)((p.N + seqs - 1) / seqs) * per_row + kStepThreads - 1) /
@@ -344,10 +343,14 @@ cudaError_t launch_step_w(const ConvParams& p, cudaStream_t stream) {
   };
   // two sequences a thread once that still leaves 8 blocks per SM
   if (blocks(2) >= 8 * kSms)
-    conv_step_kernel<T, W, 2><<<blocks(2), kStepThreads, 0, stream>>>(p, per_row);
+    conv_step_kernel<T, W, 2, kVec><<<blocks(2), kStepThreads, 0, stream>>>(p, per_row);
   else
-    conv_step_kernel<T, W, 1><<<blocks(1), kStepThreads, 0, stream>>>(p, per_row);
+    conv_step_kernel<T, W, 1, kVec><<<blocks(1), kStepThreads, 0, stream>>>(p, per_row);
   return cudaGetLastError();
+}
+template <typename T, int W>
+cudaError_t launch_step_w(const ConvParams& p, cudaStream_t stream) {
+  return p.vec ? launch_step_v<T, W, true>(p, stream) : launch_step_v<T, W, false>(p, stream);
 }
 
 template <typename T>
