@@ -261,9 +261,11 @@ __global__ void __launch_bounds__(kThreads) conv_state_kernel(const ConvParams p
 
 // One token per sequence: a thread holds the windows of 4 channels of kSeqs sequences and
 // shifts their states in place.  kSeqs > 1 shares the filter, which is as many bytes as the
-// window and the output of one sequence.
+// window and the output of one sequence.  256 x 8192 (bf16, 34 MB): 7.0 us in a graph (4.8 TB/s), 1
+// x 8192 1.6.  The 1 in the bounds lets the compiler take the registers to have every load in
+// flight at once (70; 56 by itself, 8.9 us).
 template <typename T, int W, int kSeqs, bool kVec>
-__global__ void __launch_bounds__(kStepThreads) conv_step_kernel(const ConvParams p, int per_row) {
+__global__ void __launch_bounds__(kStepThreads, 1) conv_step_kernel(const ConvParams p, int per_row) {
   const long long id = (long long)blockIdx.x * kStepThreads + threadIdx.x;
   const long long first = id / per_row * kSeqs;
   if (first >= p.N) return;
