@@ -53,7 +53,7 @@ def _build_binding() -> str:
                               sysconfig.get_paths()["include"], os.path.join(cuda, "include"))]
     cmd += [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-            "-lc10_cuda"]
+            "-lc10_cuda", "-ltorch_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")

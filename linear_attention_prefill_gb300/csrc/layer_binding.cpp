@@ -2,7 +2,7 @@
 // (_layer_native), behind the functions of layer.py.
 //
 // A decode step takes a few microseconds on the GPU.  Checking its tensors and allocating its
-// outputs from Python took the S6 step 17 us a call on the host, here it takes 3.9.  Argument
+// outputs from Python took the S6 step 17 us a call on the host, here it takes 3.5.  Argument
 // marshalling only: types, devices, shapes and strides are checked, outputs allocated, the
 // library's entry points called on the current stream.  The entry points' addresses and the
 // raiser of their errors come from Python (init).
@@ -12,7 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -142,6 +142,12 @@ Rows rows(PyObject* o, const char* name, ScalarType type, int device, IntArrayRe
   return {t.data_ptr(), stride};
 }
 
+// A tensor from torch's allocator, on the device's current stream.
+Tensor fresh(IntArrayRef shape, ScalarType type, int device) {
+  return Tensor(at::detail::empty_cuda(
+      shape, type, c10::Device(c10::DeviceType::CUDA, (c10::DeviceIndex)device), std::nullopt));
+}
+
 // An output: the caller's, or a fresh one.  `object` is a new reference.
 struct Output {
   void* p;
@@ -158,7 +164,7 @@ Output output(PyObject* o, const char* name, ScalarType type, int device, IntArr
     Py_INCREF(o);
     return {p, o};
   }
-  Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, device));
+  Tensor t = fresh(shape, type, device);
   void* p = t.data_ptr();
   return {p, wrap(std::move(t))};
 }
@@ -330,7 +336,7 @@ PyObject* s6_fwd(PyObject* const* a) {
     ws = dense(t, "workspace", ScalarType::Byte, dev, t.sizes());
     bytes = (size_t)t.numel();
   } else if ((bytes = lib.s6_workspace(b.n, b.t, dim, Ns, b.cu != nullptr)) != 0) {
-    scratch = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, dev));
+    scratch = fresh({(int64_t)bytes}, ScalarType::Byte, dev);
     ws = scratch.data_ptr();
   }
   run(dev, [&](gdn_stream_t st) {
