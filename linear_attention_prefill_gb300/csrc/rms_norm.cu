@@ -9,7 +9,11 @@
 // residual, and y once on the way out.  HBM bandwidth bounds it: every tensor crosses once,
 // with the row held in registers between the sum of squares and the output.  A thread
 // holds vectors of 8 columns as packed pairs, so a group of 32, 64 or 128 columns is 4, 8 or 16
-// lanes.
+// lanes.  Rows of up to 512 columns stay within a warp (65536 gated heads of 128, bf16, 50 MB:
+// 11.6 us in a graph, 4.3 TB/s); wider ones take a block each (16 rows of 2560 with residual into
+// e4m3: 2.1 us) or, many of them, a ring of bulk copies (8192 x 5120 with residual into e4m3, 295
+// MB: 52 us, 5.7 TB/s).  Kernels of whole vectors are apart from those for other rows: with both
+// in one the compiler left fewer loads in flight (13.4 us against 12.4 for the heads, a call).
 #include "gdn_common.cuh"
 #include "layer_common.cuh"
 #include "layer_internal.h"
