@@ -10,12 +10,13 @@
 // HBM bandwidth bounds it: 2 bytes in and 2 out per element against ~13 instructions.  A
 // thread has 4 channels (8 bytes of bf16) and walks a run of tokens with the window in
 // registers as packed fp32 pairs, so that each input is loaded once except for the W - 1 rows
-// before a run.  Its own inputs come by cp.async through a private ring of shared memory, three
+// before a run.  Its own inputs come by cp.async through a private ring of shared memory, two
 // rounds of four tokens ahead: what is in flight then costs no registers.  At 4096 x 6144 (bf16,
 // 101 MB): 39 us with 8 channels a thread and loads as they are needed, 26.6 us with 4 and one
-// round ahead in registers, 22.6 us with the ring (4.5 TB/s).  Eight channels a thread on the
-// ring take a quarter fewer instructions but 124 registers: no faster, and slower at 10007 x 5376
-// (43 us against 41).  Rows off 4-channel pieces are loaded element by element.
+// round ahead in registers, 19.7 us with the ring (5.1 TB/s; 10007 x 5376 36.8 us, 5.9 TB/s), both
+// in a graph; one round more or less ahead 20.0 and 21.2.  Eight channels a thread on the ring
+// take a quarter fewer instructions but 124 registers: no faster.  Rows off 4-channel pieces are
+// loaded element by element.
 #include "gdn_common.cuh"
 #include "layer_common.cuh"
 #include "layer_internal.h"
@@ -26,7 +27,7 @@ namespace {
 constexpr int kThreads = 64;
 constexpr int kStepThreads = 128;
 constexpr int kAhead = 4;     // tokens of a round
-constexpr int kRounds = 4;    // rounds of the ring
+constexpr int kRounds = 3;    // rounds of the ring
 
 constexpr int kChans = 4;          // channels per thread
 
@@ -166,22 +167,22 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   P ahead[kVec ? 1 : kAhead];  // the tokens of the next round
   P* ring = reinterpret_cast<P*>(s_ring) + threadIdx.x;
   const int len = (int)(t1 - t0);
-  auto request = [&](int round) {  // this thread's inputs of a round, x at its first token
-    if constexpr (kVec) {
+  int wanted = len, to = 0;  // tokens not yet requested; the ring's place for the next round
+  auto request = [&]() {     // this thread's inputs of the next round, x at its first token
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (round * kAhead + u < len)
-          copy_piece<sizeof(P)>(ring + (round % kRounds * kAhead + u) * kThreads, x + u * p.x_stride);
-      cp_async_commit();
-    } else {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (round * kAhead + u < len) ahead[u].load(x + u * p.x_stride, left, false);
+    for (int u = 0; u < kAhead; ++u) {
+      if (u < wanted) {
+        if constexpr (kVec) copy_piece<sizeof(P)>(ring + (to * kAhead + u) * kThreads, x);
+        else ahead[u].load(x, left, false);
+      }
+      x += p.x_stride;
     }
-    x += kAhead * p.x_stride;
+    if constexpr (kVec) cp_async_commit();
+    wanted -= kAhead;
+    if (++to == kRounds) to = 0;
   };
 #pragma unroll
-  for (int round = 0; round < (kVec ? kRounds - 1 : 1); ++round) request(round);
+  for (int round = 0; round < (kVec ? kRounds - 1 : 1); ++round) request();
 
   // the sequence of token t0: the first one that ends behind it
   int n = 0;
@@ -213,41 +214,47 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
       for (int i = 0; i < kChans / 2; ++i) win[j][i] = win[j + 1][i];
   };
 
-  int round = 0;
-  for (long long t = t0; t < t1; t += kAhead, ++round) {
+  // the sequence's tokens, counted from t0
+  int begin = (int)max(s.begin - t0, 0ll), end = (int)min(s.end - t0, (long long)len);
+  for (int t = 0, from = 0; t < len; t += kAhead) {
     P raw[kAhead];
     if constexpr (kVec) {
-      request(round + kRounds - 1);
+      request();
       cp_async_wait<kRounds - 1>();
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) raw[u] = ring[(round % kRounds * kAhead + u) * kThreads];
+      for (int u = 0; u < kAhead; ++u) raw[u] = ring[(from * kAhead + u) * kThreads];
+      if (++from == kRounds) from = 0;
     } else {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
-      request(round + 1);
+      request();
     }
-    if (t >= s.begin && t + kAhead <= min(t1, s.end)) {  // one sequence's tokens
+    if (t >= begin && t + kAhead <= end) {  // one sequence's tokens
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) next(raw[u], y + (long long)u * p.D);
+      for (int u = 0; u < kAhead; ++u) {
+        next(raw[u], y);
+        y += p.D;
+      }
     } else {
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const long long tt = t + u;
-        if (tt >= t1) return;
-        if (tt >= s.end) {  // the next sequence that has tokens begins
+        const int tt = t + u;
+        if (tt >= len) return;
+        if (tt >= end) {  // the next sequence that has tokens begins
           do {
             if (++n >= p.N) return;
             s = span_of(p, n);
-          } while (tt >= s.end);
+          } while (t0 + tt >= s.end);
+          begin = (int)max(s.begin - t0, 0ll);
+          end = (int)min(s.end - t0, (long long)len);
 #pragma unroll
           for (int j = 0; j < W - 1; ++j)
-            tap<T, W>(p, s, n, max(tt, s.begin) - (W - 1) + j, c, left, kVec).get(win[j]);
+            tap<T, W>(p, s, n, max(t0 + tt, s.begin) - (W - 1) + j, c, left, kVec).get(win[j]);
         }
-        if (tt < s.begin) continue;
-        next(raw[u], y + (long long)u * p.D);
+        if (tt >= begin) next(raw[u], y);
+        y += p.D;
       }
     }
-    y += kAhead * (long long)p.D;
   }
 }
 
@@ -302,7 +309,7 @@ cudaError_t launch_v(const ConvParams& p, bool states, cudaStream_t stream) {
   const long long tokens = p.cu ? (long long)p.T : (long long)p.N * p.T;
   const unsigned by = ((p.D + kChans - 1) / kChans + kThreads - 1) / kThreads;
   // long runs repeat fewer rows (W - 1 each), short ones fill the GPU: 16 blocks per SM (runs of
-  // 64: 23.4 us at 4096 x 6144 and 42.1 at 10007 x 5376; of 32: 22.6 and 41.1; of 16: 22.6, 45.5)
+  // 64: 22.0 us at 4096 x 6144 and 26.3 at 16384 x 2048; of 32: 21.1 and 26.4; of 16: 23.2, 28.3)
   int run = 32;
   while (run > kAhead && (tokens + run - 1) / run * by < 16 * kSms) run /= 2;
   const long long runs = (tokens + run - 1) / run;
