@@ -97,17 +97,16 @@ __device__ __forceinline__ float reduce_row(float v, int G, float* s) {
 
 // What a row is after its sum of squares is known: y of every vector, stored.  r: the row's
 // vectors; load_w(i), load_gate(i): vector i of w and of the gate; n[i]: columns that exist
-// (whole vectors with kWhole, where p.by is 8); some: there is a row.
+// (whole vectors with kWhole, where p.by is 8); some: there is a row; at: its
+// first element of the lane in the outputs, scales: its scales.
 template <typename T, bool kFp8, bool kBlock, bool kWhole, int NV, typename LoadW, typename LoadGate>
-__device__ __forceinline__ void finish(const NormParams& p, long long row, bool some, int G,
-                                       int lane, f32x2 (&r)[NV][4], const int (&n)[NV], float ss,
+__device__ __forceinline__ void finish(const NormParams& p, long long at, float* scales, bool some,
+                                       int G, int lane, f32x2 (&r)[NV][4], const int (&n)[NV], float ss,
                                        float* s_max, LoadW load_w, LoadGate load_gate) {
   const int by = kWhole ? 8 : p.by;
   const f32x2 rstd = dup2(rsqrtf(ss * p.inv_d + p.eps));
-  const long long at = row * p.D + lane * 8;
   T* y = static_cast<T*>(p.y) + at;
   uint8_t* y8 = static_cast<uint8_t*>(p.y) + at;
-  float* scales = p.scales + row * p.groups;
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -184,7 +183,7 @@ template <typename T, bool kFp8, bool kWhole, int G, int NV>
 __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
   constexpr int per_block = 128 / G;
   const int lane = threadIdx.x % G;
-  const long long step = (long long)gridDim.x * per_block;
+  const unsigned step = gridDim.x * per_block, rows = (unsigned)p.rows;  // (rows fit 31 bits)
   const int by = kWhole ? 8 : p.by;
   int n[NV];
   f32x2 w[NV][4];
@@ -195,17 +194,21 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
     if (n[i] > 0) pairs_of(load8(p.w + c, n[i], by), w[i]);
   }
   Raw8<T> x[NV], res[NV], gate[NV];
-  const long long row0 = (long long)blockIdx.x * per_block + threadIdx.x / G;
+  const unsigned row0 = blockIdx.x * per_block + threadIdx.x / G;
+  long long at = (long long)row0 * p.D + lane * 8;  // of the present row in the dense tensors
+  const long long step_at = (long long)step * p.D;
+  float* scales = p.scales + (long long)row0 * p.groups;
   const T* xp = static_cast<const T*>(p.x) + lane * 8;
   const T* gp = static_cast<const T*>(p.gate) + lane * 8;
-  const T* rp = static_cast<const T*>(p.residual) + row0 * p.D + lane * 8;
+  const T* rp = static_cast<const T*>(p.residual) + at;
   const bool heads = p.heads > 1;  // else a row's place moves on by a constant
   if (!heads) xp += row0 * p.x_stride, gp += row0 * p.gate_stride;
-  auto load_row = [&](long long row) {
+  auto load_row = [&](unsigned row) {
     const T *xr = xp, *gr = gp;
     if (heads) {
-      // (rows fit 31 bits; with a 64-bit quotient 131072 heads of 64: 12.7 us against 10.9)
-      const long long token = (unsigned)row / (unsigned)p.heads, col = (row - token * p.heads) * p.D;
+      // (with a 64-bit quotient 131072 heads of 64: 12.7 us against 10.9)
+      const unsigned token = row / (unsigned)p.heads;
+      const int col = (int)(row - token * p.heads) * p.D;
       xr += token * p.x_stride + col;
       gr += token * p.gate_stride + col;
     } else {
@@ -219,14 +222,13 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
       if (p.residual) res[i] = load8(rp + i * G * 8, n[i], by);
       if (p.gate) gate[i] = load8(gr + i * G * 8, n[i], by);
     }
-    rp += step * p.D;
+    rp += step_at;
   };
-  if (row0 < p.rows) load_row(row0);
+  if (row0 < rows) load_row(row0);
   // every lane of a warp stays for the shuffles
-  for (long long base = (long long)blockIdx.x * per_block; base < p.rows; base += step) {
-    const long long row = base + threadIdx.x / G;
-    const bool some = row < p.rows;
-    T* out = static_cast<T*>(p.residual_out) + row * p.D + lane * 8;
+  for (unsigned row = row0; row - threadIdx.x / G < rows; row += step) {
+    const bool some = row < rows;
+    T* out = static_cast<T*>(p.residual_out) + at;
     f32x2 r[NV][4], ss = 0ull;
     Raw8<T> g[NV];
 #pragma unroll
@@ -236,17 +238,19 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
         g[i] = gate[i];
       }
     }
-    if (row + step < p.rows) load_row(row + step);
+    if (row + step < rows) load_row(row + step);
     float s0, s1;
     unpack2(ss, s0, s1);
     const float sum = reduce_row<false, false>(s0 + s1, G, nullptr);
     finish<T, kFp8, false, kWhole, NV>(
-        p, row, some, G, lane, r, n, sum, nullptr,
+        p, at, scales, some, G, lane, r, n, sum, nullptr,
         [&](int i, f32x2 (&q)[4]) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) q[j] = w[i][j];
         },
         [&](int i, f32x2 (&q)[4]) { pairs_of(g[i], q); });
+    at += step_at;
+    if (kFp8) scales += (long long)step * p.groups;
   }
 }
 
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(NV == 4 ? 1024 : 1024 / NV, 1)
   unpack2(ss, s0, s1);
   const float sum = reduce_row<false, true>(s0 + s1, G, s_sum);
   finish<T, kFp8, true, kWhole, NV>(
-      p, row, true, G, lane, r, n, sum, s_max,
+      p, row * p.D + lane * 8, p.scales + row * p.groups, true, G, lane, r, n, sum, s_max,
       [&](int i, f32x2 (&q)[4]) {
         if (kWide) w[0] = load8(p.w + (i * G + lane) * 8, n[i], by);
         pairs_of(w[kWide ? 0 : i], q);
@@ -382,7 +386,7 @@ __global__ void __maxnreg__(NV == 1 ? 64 : NV > 2 ? 128 : sizeof(T) == 4 ? 96 : 
       fetch(next, s);
     }
     finish<T, kFp8, true, true, NV>(
-        p, row, true, G, tid, r, n, sum, s_max[turn],
+        p, row * p.D + tid * 8, p.scales + row * p.groups, true, G, tid, r, n, sum, s_max[turn],
         [&](int i, f32x2 (&q)[4]) { pairs_of(w[i], q); },
         [&](int i, f32x2 (&q)[4]) { pairs_of(g[i], q); });
     if (++s == slots) s = 0, phase ^= 1;
