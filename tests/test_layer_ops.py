@@ -268,6 +268,7 @@ def test_s6_prompt(cuda_lib, dtype, lens, packed, dim, Ns):
 @pytest.mark.parametrize("lens,packed,dim,Ns", [
     ((2085,), False, 64, 16), ((1300, 0, 2, 1700), True, 40, 16), ((1111, 1111), False, 33, 7),
     ((1500,), False, 16, 64), ((1100,), False, 4900, 16),  # the last: whole channels beside split ones
+    ((1100,), False, 4900, 8), ((8950,), False, 32, 16), ((4500, 7, 4400), True, 31, 32),
 ])
 def test_s6_split_over_time(cuda_lib, dtype, lens, packed, dim, Ns):
     """Few channels, many tokens: the split over time, with states and in place."""
