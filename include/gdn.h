@@ -353,8 +353,8 @@ gdn_status kda_recurrent_step(const void* q, const void* k, const void* v, const
  *    in elements from token to token (>= the row's length; rows of a batch
  *    follow each other, so token t of row b is at (b T + t) * stride) and need
  *    only their element's alignment; outputs are dense.  Rows of 16-byte
- *    aligned, 8-element multiples run on wide accesses, others element by
- *    element with the same results.
+ *    aligned, 8-element multiples run on wide accesses, others on narrower ones
+ *    with the same results.
  *  - cu_seqlens [N + 1]: sequences of a packed row of T tokens.  cu[N] may be
  *    below T: rows behind the last sequence are left as they were.  The borders
  *    are clamped to [0, T] on the device; a table that is not ordered gives

@@ -5,8 +5,8 @@ As in binding.py the functions carry the C ABI's names; the signatures are here,
 allocations and calls in the extension module that csrc/layer_binding.cpp builds.  Row operands
 may be slices of a wider projection (the last dimension dense, tokens a constant stride apart);
 parameters, states and outputs are contiguous.  As everywhere in the library the outputs carry
-no gradient.  ``stream`` (a torch stream, or a cudaStream_t
-as a number) runs a call, and makes its allocations, on another stream than the current one.
+no gradient.  ``stream`` (a torch stream, or a cudaStream_t as a number) runs a call, and makes
+its allocations, on another stream than the current one.
 """
 from __future__ import annotations
 
