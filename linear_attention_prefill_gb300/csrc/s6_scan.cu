@@ -42,8 +42,8 @@ S6Split s6_split(int N, int T, int dim, int Ns, bool packed) {
     // mean length; whatever is shorter is one chunk and computed once, as it would be anyway.
     // 512 channels, one of 8000 tokens and 15 of 12: 348 -> 115 us; 40 of 200: 33 -> 37; 16 of
     // 1024: 64 -> 84.  With more channels (2049) even batches lose more (72 -> 95) and uneven
-    // ones gain less.
-    const long long chunk = (2 * per_seq + 127) / 128 * 128;
+    // ones gain less.  (The mean rounds down, to 0 where there are more sequences than tokens.)
+    const long long chunk = per_seq ? (2 * per_seq + 127) / 128 * 128 : 128;
     if (!packed || tiles > kSms / 4 || chunk >= T) return s;
     s.whole = 0;
     s.chunk = (int)chunk;

@@ -114,6 +114,21 @@ def test_s6_workspace_size(lib):
     assert size(-1, 64, 64, 16, 0) == 0 and size(1, 4096, 64, 65, 0) == 0
 
 
+def test_s6_workspace_size_of_more_sequences_than_tokens(lib):
+    """Packed batches may hold empty sequences, any number of them: every size has an answer."""
+    size = lib.gdn_s6_chunk_fwd_workspace_size
+    for packed in (0, 1):
+        for dim in (1, 64, 1216, 1217):
+            for N in list(range(1, 20)) + [31, 64, 127, 152, 200, 299, 1000]:
+                for T in list(range(0, 20)) + [31, 64, 127, 128, 129, 150, 255, 257, 300]:
+                    got = size(N, T, dim, 16, packed)
+                    assert got >= 0
+                    if N > T and T <= 128:  # no sequence is longer than a chunk
+                        assert got == 0
+    # 150 tokens among 200 sequences, in chunks of 128: 1 + 200 + 1 slots
+    assert size(200, 150, 64, 16, 1) == 4 * (202 * 64 + 202 * 64 * 16 + 200 * 64 * 16)
+
+
 NORM = dict(x=at(0), w=at(1), res=None, gate=None, y=at(2), out=None, scales=at(3), tokens=4, heads=1, D=64,
             xs=64, gs=64, group=32, eps=1e-6)
 
