@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   } else {
     n = (int)(t0 / p.T);
   }
-  if (n >= p.N) return;  // behind the last sequence: left as it was
+  if (n >= p.N) {  // behind the last sequence: left as it was
+    if constexpr (kVec) cp_async_wait<0>();  // (no thread leaves while its copies are in flight)
+    return;
+  }
   Span s = span_of(p, n);
 
   f32x2 f[W][kChans / 2], win[W][kChans / 2], bias[kChans / 2];  // the filter, and the inputs under it
@@ -242,7 +245,10 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
         if (tt >= len) return;
         if (tt >= end) {  // the next sequence that has tokens begins
           do {
-            if (++n >= p.N) return;
+            if (++n >= p.N) {
+              if constexpr (kVec) cp_async_wait<0>();
+              return;
+            }
             s = span_of(p, n);
           } while (t0 + tt >= s.end);
           begin = (int)max(s.begin - t0, 0ll);

@@ -795,3 +795,29 @@ def test_binding_refusals(cuda_lib):
     with pytest.raises(err, match="workspace"):
         scan(big, big, -torch.ones(32, 16, device=dev), bb, bb,
              workspace=torch.empty(256, dtype=torch.uint8, device=dev))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("end", [1, 7, 2049, 2050, 4095])
+def test_conv_blocks_behind_the_last_sequence_leave_nothing_in_flight(cuda_lib, dtype, end):
+    """Most blocks find their rows behind the last sequence (or meet its end within a round) and leave
+    early; other kernels take their shared memory at once, on the same and on another stream."""
+    dt, g, T, D = DT[dtype], gen_of(end), 4096, 2048
+    x, w = randn(g, 1, T, D, dtype=dt), randn(g, D, 4)
+    cu = torch.tensor([0, end], dtype=torch.int32, device="cuda")
+    ref, err, st = conv_ref(x[:, :end], w, None, None, "silu", [(0, 0, end)])
+    s = s6_inputs(gen_of(1), (1, 256), 1, 512, 16, torch.bfloat16)
+    torch.cuda.synchronize()
+    other, want, ends = torch.cuda.Stream(), s6_run(cuda_lib, s, True), []
+    torch.cuda.synchronize()
+    for _ in range(8):
+        y = torch.full_like(x, 7.0)
+        with torch.cuda.stream(other):
+            beside = s6_run(cuda_lib, s, True)
+        _, sT = cuda_lib.gdn_short_conv_fwd(x, w, y=y, cu_seqlens=cu)
+        ends.append((y, sT, s6_run(cuda_lib, s, True), beside))
+    torch.cuda.synchronize()
+    for y, sT, *scans in ends:
+        assert_within(y[:, :end], ref, err, dt, "y")
+        assert (y[:, end:] == 7).all() and torch.equal(sT.double(), st)
+        assert all(torch.equal(a, b) for scan in scans for a, b in zip(scan, want))
