@@ -50,13 +50,17 @@ constexpr int kCh = 32;   // channels per CTA
 constexpr int kRing = 4;  // tiles of raw inputs in shared memory
 constexpr int kPairs = kCh / 2;
 
+// How a channel's states fill its LPC lanes, four each: all of them (Ns = 4 LPC), some of them (Ns a
+// multiple of 4), or with fewer than four in a lane.
+enum class Fill { kAll, kSome, kPart };
+
 // A variant: T inputs, LPC lanes per channel or channel pair, kWidth channels a lane, tiles of
 // kTokens.  Sizes of shared memory are in pieces of 16 bytes.
-template <typename T_, int LPC_, int kWidth_, int kTokens, bool kPad_, bool kSummary_>
+template <typename T_, int LPC_, int kWidth_, int kTokens, Fill kFill, bool kSummary_>
 struct Cfg {
   using T = T_;
   static constexpr int LPC = LPC_, kWidth = kWidth_, kTile = kTokens;
-  static constexpr bool kPad = kPad_;  // Ns is not a multiple of 4: lanes with fewer states
+  static constexpr bool kPad = kFill == Fill::kPart, kEmpty = kFill == Fill::kSome;
   static constexpr bool kSummary = kSummary_;
   static constexpr int kUnits = kCh / kWidth;  // channel pairs, or channels
   static constexpr int kCompute = kUnits * LPC < 32 ? 32 : kUnits * LPC;
@@ -307,6 +311,14 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
         float y[kWidth][2];
       };
       auto put = [&](int t, Two v) {  // the sums of tokens t and t + 1
+        // A lane without states has A, B and C of zero, but an infinite step or input makes its
+        // sums NaN (0 times infinity): they do not count.  (Kernels apart: 4096 tokens of 5120
+        // channels, 24 states, bf16 238 us without the selects, 246 with; 12 states 148, 150.)
+        if (C::kEmpty) {
+#pragma unroll
+          for (int j = 0; j < kWidth; ++j)
+            v.y[j][0] = nst ? v.y[j][0] : 0.f, v.y[j][1] = nst ? v.y[j][1] : 0.f;
+        }
 #pragma unroll
         for (int o = 1; o < C::kLanes; o *= 2)
 #pragma unroll
@@ -737,33 +749,40 @@ cudaError_t launch_k(const S6Params& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p, tiles);
 }
 
-template <typename T, int LPC, bool kPad>
+template <typename T, int LPC, Fill kFill>
 cudaError_t launch_l(const S6Params& p, cudaStream_t stream) {
-  if (p.chunk) {
-    const cudaError_t e = launch_k<Cfg<T, LPC, 2, 16, kPad, true>>(p, stream);
+  if (p.chunk) {  // (summaries have no sums over the lanes)
+    constexpr Fill kStates = kFill == Fill::kPart ? kFill : Fill::kAll;
+    const cudaError_t e = launch_k<Cfg<T, LPC, 2, 16, kStates, true>>(p, stream);
     if (e != cudaSuccess) return e;
   }
   // whole sequences and first chunks need no summary, so the scan may start beside them
   // One channel a lane where every CTA has an SM for itself (1024 tokens of 4864 channels, us,
   // against two channels a lane; bf16 with Ns 4, 8, 32, 64: 37 : 56, 35 : 47, 57 : 82, 98 : 138;
   // fp32: 29 : 47, 31 : 47, but 95 : 74, 182 : 127, where B and C are twice the bytes).
-  if constexpr (!kPad && (sizeof(T) == 2 || LPC <= 4)) {
-    if (p.lone) return launch_k<Cfg<T, LPC, 1, 32, false, false>>(p, stream);
+  if constexpr (kFill != Fill::kPart && (sizeof(T) == 2 || LPC <= 4)) {
+    if (p.lone) return launch_k<Cfg<T, LPC, 1, 32, kFill, false>>(p, stream);
   }
-  return launch_k<Cfg<T, LPC, 2, 16, kPad, false>>(p, stream);
+  return launch_k<Cfg<T, LPC, 2, 16, kFill, false>>(p, stream);
 }
 
 template <typename T>
 cudaError_t launch_scan(const S6Params& p, cudaStream_t stream) {
-  if (p.Ns % 4)  // lanes with fewer than four states
-    return p.Ns < 16   ? launch_l<T, 4, true>(p, stream)
-           : p.Ns < 32 ? launch_l<T, 8, true>(p, stream)
-                       : launch_l<T, 16, true>(p, stream);
-  if (p.Ns <= 4) return launch_l<T, 1, false>(p, stream);
-  if (p.Ns <= 8) return launch_l<T, 2, false>(p, stream);
-  if (p.Ns <= 16) return launch_l<T, 4, false>(p, stream);
-  if (p.Ns <= 32) return launch_l<T, 8, false>(p, stream);
-  return launch_l<T, 16, false>(p, stream);
+  constexpr Fill kAll = Fill::kAll, kSome = Fill::kSome, kPart = Fill::kPart;
+  if (p.Ns % 4)
+    return p.Ns < 16   ? launch_l<T, 4, kPart>(p, stream)
+           : p.Ns < 32 ? launch_l<T, 8, kPart>(p, stream)
+                       : launch_l<T, 16, kPart>(p, stream);
+  switch (p.Ns) {
+    case 4: return launch_l<T, 1, kAll>(p, stream);
+    case 8: return launch_l<T, 2, kAll>(p, stream);
+    case 16: return launch_l<T, 4, kAll>(p, stream);
+    case 32: return launch_l<T, 8, kAll>(p, stream);
+    case 64: return launch_l<T, 16, kAll>(p, stream);
+  }
+  return p.Ns < 16   ? launch_l<T, 4, kSome>(p, stream)
+         : p.Ns < 32 ? launch_l<T, 8, kSome>(p, stream)
+                     : launch_l<T, 16, kSome>(p, stream);
 }
 
 }  // namespace

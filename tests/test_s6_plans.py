@@ -56,3 +56,29 @@ def test_convolution_of_more_sequences_than_tokens(cuda_lib):
         ref, err, st = conv_ref(x, w, None, s0, "silu", spans_of(lens, True, 1))
         assert_within(y, ref, err, torch.bfloat16, "y")
         assert torch.equal(sT.double(), st)
+
+
+# ---- infinite inputs -----------------------------------------------------------------
+
+
+def positive_inputs(T, dim, Ns, dt):
+    """Every term of every sum positive: an infinity stays one in the definition, it never meets its opposite."""
+    g = gen_of(T + Ns)
+    r = lambda *s: torch.rand(*s, generator=g, device="cuda") + 0.5  # noqa: E731
+    return dict(x=r(1, T, dim).to(dt), dt=(0.01 * r(1, T, dim)).to(dt), A=-0.01 * r(dim, Ns), B=r(1, T, Ns).to(dt),
+                C=r(1, T, Ns).to(dt), D=None, z=None, dt_bias=None, h0=None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [50, 1100])  # whole sequences, and split over time
+@pytest.mark.parametrize("Ns", [1, 3, 4, 5, 8, 12, 16, 20, 24, 28, 30, 32, 40, 60, 64])
+def test_infinities_stay_infinite_for_every_state_count(cuda_lib, dtype, T, Ns):
+    """Lanes that hold no state, or fewer than four, add nothing, whatever the step."""
+    for name in ("x", "dt"):
+        x = positive_inputs(T, 64, Ns, DT[dtype])
+        clean, hc = s6_run(cuda_lib, x, False)
+        x[name][0, 20, 3] = float("inf")
+        y, h = s6_run(cuda_lib, x, False)
+        assert (y[0, 20:, 3] == float("inf")).all() and (h[0, 3] == float("inf")).all()
+        y[0, 20:, 3], h[0, 3] = clean[0, 20:, 3], hc[0, 3]
+        assert torch.equal(y, clean) and torch.equal(h, hc)
