@@ -285,8 +285,11 @@ __device__ __forceinline__ void s6_compute(const S6Params& p, const Task& k, flo
         float e0, e1, e2, e3;
         unpack2(mul2(a[j][0], s), e0, e1);
         unpack2(mul2(a[j][1], s), e2, e3);
-        h[j][0] = fma2(pack2(ex2(e0), ex2(e1)), h[j][0], pack2(v.x, v.y));
-        h[j][1] = fma2(pack2(ex2(e2), ex2(e3)), h[j][1], pack2(v.z, v.w));
+        // a decay that would be 0 over the chunk, though no token's is, is 2^-126: an infinite state
+        // stays infinite (0 times infinity is NaN).  What a finite state keeps of it is below any
+        // rounding; where a sum is infinite or NaN, so is the chunk's own state.
+        h[j][0] = fma2(pack2(ex2(fmaxf(e0, -126.f)), ex2(fmaxf(e1, -126.f))), h[j][0], pack2(v.x, v.y));
+        h[j][1] = fma2(pack2(ex2(fmaxf(e2, -126.f)), ex2(fmaxf(e3, -126.f))), h[j][1], pack2(v.z, v.w));
       }
     }
   }

@@ -82,3 +82,27 @@ def test_infinities_stay_infinite_for_every_state_count(cuda_lib, dtype, T, Ns):
         assert (y[0, 20:, 3] == float("inf")).all() and (h[0, 3] == float("inf")).all()
         y[0, 20:, 3], h[0, 3] = clean[0, 20:, 3], hc[0, 3]
         assert torch.equal(y, clean) and torch.equal(h, hc)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Ns", [8, 12, 16])
+def test_infinite_states_outlive_chunks_that_decay_to_nothing(cuda_lib, dtype, Ns):
+    """exp(A times a chunk's steps) underflows where no token's decay does: infinity stays infinity."""
+    dt, T = DT[dtype], 1500
+    assert cuda_lib.gdn_s6_chunk_fwd_workspace_size(1, T, 64, Ns) > 0
+    x = positive_inputs(T, 64, Ns, dt)
+    x["A"], x["dt"] = 1000 * x["A"], 10 * x["dt"]  # decays of e^-0.25 to e^-2.25 a token, e^-32 or less over 128
+    clean, hc = s6_run(cuda_lib, x, False)
+    assert torch.isfinite(clean.float()).all() and torch.isfinite(hc).all()
+    x["x"][0, 20, 3] = float("inf")
+    y, h = s6_run(cuda_lib, x, False)
+    assert (y[0, 20:, 3] == float("inf")).all() and (h[0, 3] == float("inf")).all()
+    x["h0"] = torch.full((1, 64, Ns), float("-inf"), device="cuda")
+    x["x"][0, 20, 3] = 0.5
+    y, h = s6_run(cuda_lib, x, False)
+    assert (y == float("-inf")).all() and (h == float("-inf")).all()
+    x["dt"][0, 700, 5] = float("inf")  # a decay that is 0 for one token: 0 times infinity has no value
+    y, h = s6_run(cuda_lib, x, False)
+    assert torch.isnan(y[0, 700:, 5]).all() and torch.isnan(h[0, 5]).all()
+    y[0, 700:, 5], h[0, 5] = float("-inf"), float("-inf")
+    assert (y == float("-inf")).all() and (h == float("-inf")).all()
