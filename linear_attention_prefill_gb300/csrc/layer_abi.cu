@@ -75,10 +75,14 @@ gdn_status check_conv(const void* x, const float* w, const float* bias, const vo
   if (!aligned(y, elem) || !aligned(s0, elem) || !aligned(sT, elem))
     return fail(GDN_ERR_INVALID_ARG, "y, s0 and sT must be %d-byte aligned", elem);
   const long long states = (long long)N * (W - 1) * D;
-  const Range rx = range_of(x, tokens, x_stride, D, elem), ry = range_of(y, tokens * D, elem);
-  const Range r0 = range_of(s0, states, elem), rT = range_of(sT, states, elem);
-  if (overlap(ry, rx) || overlap(ry, r0) || overlap(ry, rT) || overlap(rT, rx) ||
-      (s0 != sT && overlap(r0, rT)))
+  const Range ry = range_of(y, tokens * D, elem), r0 = range_of(s0, states, elem),
+              rT = range_of(sT, states, elem);
+  const Range in[] = {range_of(x, tokens, x_stride, D, elem), range_of(w, (long long)D * W, 4),
+                      range_of(bias, D, 4), range_of(cu, (long long)N + 1, 4)};
+  for (const Range& r : in)
+    if (overlap(ry, r) || overlap(rT, r))
+      return fail(GDN_ERR_INVALID_ARG, "y and sT must not overlap the inputs (sT may be s0)");
+  if (overlap(ry, r0) || overlap(ry, rT) || (s0 != sT && overlap(r0, rT)))
     return fail(GDN_ERR_INVALID_ARG, "y and sT must not overlap the inputs (sT may be s0)");
   // blocks of 4 or more tokens, one per state; 256 channels a block or more
   if (tokens / 4 + N + 1 > kMaxGrid || D > 65535 * 256)
@@ -145,7 +149,8 @@ gdn_status check_s6(const void* x, const void* dt, const float* A, const void* B
                       range_of(z, tokens, z_stride, dim, elem),
                       range_of(A, (long long)dim * Ns, 4),
                       range_of(D, dim, 4),
-                      range_of(dt_bias, dim, 4)};
+                      range_of(dt_bias, dim, 4),
+                      range_of(cu, (long long)N + 1, 4)};
   for (const Range& r : in)
     if (overlap(ry, r) || overlap(rT, r))
       return fail(GDN_ERR_INVALID_ARG, "y and hT must not overlap the inputs (hT may be h0)");

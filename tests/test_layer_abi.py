@@ -38,6 +38,25 @@ def test_conv_rejects(lib, case, status, f32):
     assert lib.gdn_last_error() != b""
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("case", [
+    dict(w=at(2)), dict(w=at(2, 16)), dict(bias=at(2, 4)), dict(cu=at(2)), dict(cu=at(2, 8), N=3),
+    dict(sT=at(1)), dict(sT=at(1, 16)), dict(bias=at(3), sT=at(3)), dict(cu=at(4, 4), sT=at(4)),
+    dict(cu=at(4), sT=at(4, 4), s0=at(5)),
+])
+def test_conv_outputs_on_parameters_or_borders(lib, case, f32):
+    """y and sT may overlap no input: the filter, the bias and the borders are inputs too."""
+    assert conv(lib, f32=f32, **case) == 1
+    assert b"overlap" in lib.gdn_last_error()
+
+
+def test_conv_step_outputs_on_parameters(lib):
+    for fn in (lib.gdn_short_conv_step, lib.gdn_short_conv_step_f32):
+        for w, bias, s, y in ((2, None, 3, 2), (1, 2, 3, 2), (3, None, 3, 2), (1, 3, 3, 2)):
+            assert fn(at(0), at(w), bias and at(bias), at(s), at(y), 2, 16, 4, 16, 1, None) == 1
+            assert b"overlap" in lib.gdn_last_error()
+
+
 def test_conv_without_work(lib):
     assert conv(lib, N=0, T=0, x=None, y=None, w=None) == 0
     assert conv(lib, N=3, T=0, x=None, y=None, w=None) == 0
@@ -82,6 +101,13 @@ def s6(lib, f32=False, **kw):
 def test_s6_rejects(lib, case, status, f32):
     assert s6(lib, f32=f32, **case) == status
     assert lib.gdn_last_error() != b""
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("case", [dict(cu=at(9)), dict(cu=at(9, 64)), dict(cu=at(10)), dict(cu=at(10, 16), N=2)])
+def test_s6_outputs_on_borders(lib, case, f32):
+    assert s6(lib, f32=f32, **case) == 1
+    assert b"overlap" in lib.gdn_last_error()
 
 
 def test_s6_without_work(lib):
