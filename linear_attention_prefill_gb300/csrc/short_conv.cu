@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   if (p.cu) {
     int lo = 0, hi = p.N;
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
+      const int mid = lo + ((hi - lo) >> 1);  // (lo + hi may pass 31 bits)
       if (min(max(p.cu[mid + 1], 0), p.T) > t0) hi = mid; else lo = mid + 1;
     }
     n = lo;

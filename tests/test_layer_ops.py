@@ -821,3 +821,15 @@ def test_conv_blocks_behind_the_last_sequence_leave_nothing_in_flight(cuda_lib, 
         assert_within(y[:, :end], ref, err, dt, "y")
         assert (y[:, end:] == 7).all() and torch.equal(sT.double(), st)
         assert all(torch.equal(a, b) for scan in scans for a, b in zip(scan, want))
+
+
+def test_conv_of_more_than_2_30_sequences(cuda_lib):
+    """All empty but the last: the search for a token's sequence ends at numbers whose sum passes 31 bits."""
+    g, N, T, bf = gen_of(17), 2 ** 30 + 5, 64, torch.bfloat16
+    x, w = randn(g, 1, T, 8, dtype=bf), randn(g, 8, 4)
+    cu = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+    cu[-1] = T
+    y, sT = cuda_lib.gdn_short_conv_fwd(x, w, cu_seqlens=cu, output_final_state=False)
+    ref, err, _ = conv_ref(x, w, None, None, "silu", [(0, 0, T)])
+    assert sT is None
+    assert_within(y, ref, err, bf, "y")
