@@ -15,6 +15,7 @@ using gdn::cuda_fail;
 using gdn::fail;
 
 constexpr long long kMaxGrid = 0x7fffffffll;
+constexpr int kMaxChannels = 1 << 30;  // of the scan: tiles of 32 are counted in 31 bits
 
 // Bytes from `base` that `rows` rows of `cols` elements, `stride` elements apart, span.
 struct Range {
@@ -128,6 +129,7 @@ gdn_status check_s6(const void* x, const void* dt, const float* A, const void* B
   GDN_TRY(check_tokens(N, T, dim, cu, &tokens));
   if (Ns < 1) return fail(GDN_ERR_INVALID_ARG, "Ns=%d must be > 0", Ns);
   if (Ns > 64) return fail(GDN_ERR_UNSUPPORTED, "Ns=%d: at most 64 states per channel", Ns);
+  if (dim > kMaxChannels) return fail(GDN_ERR_INVALID_ARG, "problem too large: D=%d", dim);
   GDN_TRY(check_rows("x", x, tokens, x_stride, dim, elem));
   GDN_TRY(check_rows("dt", dt, tokens, dt_stride, dim, elem));
   GDN_TRY(check_rows("B", B, tokens, b_stride, Ns, elem));
@@ -226,7 +228,8 @@ gdn_status s6_step(const void* x, const void* dt, const float* A, const void* B,
   GDN_TRY(check_s6(x, dt, A, B, C, D, z, dt_bias, h, y, h, N, 1, dim, Ns, x_stride, dt_stride,
                    b_stride, c_stride, z_stride, dt_softplus, nullptr, f32 ? 4 : 2, &p));
   if (N > 0 && !h) return fail(GDN_ERR_INVALID_ARG, "h must be non-NULL");
-  if ((long long)N * ((long long)dim * 16 / 256 + 1) > kMaxGrid || dim > (1 << 26))
+  // (a lane's four sequences are counted in 31 bits)
+  if ((long long)N * ((long long)dim * 16 / 256 + 1) > kMaxGrid - 4 || dim > (1 << 26))
     return fail(GDN_ERR_INVALID_ARG, "N=%d, D=%d too large", N, dim);
   if (N == 0) return GDN_OK;
   const cudaError_t e = gdn::launch_s6_step(p, f32, reinterpret_cast<cudaStream_t>(stream));
@@ -333,7 +336,8 @@ gdn_status gdn_short_conv_step_f32(const float* x, const float* w, const float* 
 }
 
 size_t gdn_s6_chunk_fwd_workspace_size(int N, int T, int dim, int Ns, int has_cu_seqlens) {
-  if (N < 0 || T < 0 || dim <= 0 || Ns < 1 || Ns > 64 || (has_cu_seqlens && N < 1)) return 0;
+  if (N < 0 || T < 0 || dim <= 0 || dim > kMaxChannels || Ns < 1 || Ns > 64 || (has_cu_seqlens && N < 1))
+    return 0;
   return gdn::s6_split(N, T, dim, Ns, has_cu_seqlens != 0).ws_bytes;
 }
 

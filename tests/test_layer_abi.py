@@ -186,6 +186,21 @@ def test_norm_rejects(lib, case, status, fp8, f32):
     assert lib.gdn_last_error() != b""
 
 
+@pytest.mark.parametrize("f32", [False, True])
+def test_sizes_next_to_31_bits(lib, f32):
+    """Sizes whose roundings up pass 31 bits are refused, before any launch."""
+    most = 2 ** 31 - 1
+    fn = lib.gdn_short_conv_step_f32 if f32 else lib.gdn_short_conv_step
+    assert fn(at(0), at(10), None, at(20), at(40), most, 1, 2, 1, 1, None) == 1
+    a = [at(8 * i) for i in range(12)]
+    fn = lib.gdn_s6_recurrent_step_f32 if f32 else lib.gdn_s6_recurrent_step
+    assert fn(*a[:5], None, None, None, a[8], a[9], most, 1, 1, 1, 1, 1, 1, 1, 1, None) == 1
+    for dim in (most, 2 ** 30 + 1):
+        assert s6(lib, f32, x=a[0], dt=a[1], A=a[2], B=a[3], C=a[4], D=None, z=None, bias=None, h0=None, y=a[9],
+                  hT=a[10], T=1, dim=dim, Ns=1, xs=dim, ds=dim) == 1
+    assert lib.gdn_s6_chunk_fwd_workspace_size(1, 1, most, 1, 0) == 0
+
+
 def test_norm_e4m3_rejects(lib):
     assert norm(lib, True, scales=None) == 1 and norm(lib, True, group=48) == 2
     assert norm(lib, True, scales=at(2)) == 1 and norm(lib, True, scales=at(3, 2)) == 1
