@@ -109,6 +109,16 @@ __device__ __forceinline__ Span span_of(const ConvParams& p, int n) {
   return {b, max(b, e)};
 }
 
+// The first sequence of a packed batch, from number lo on, that ends behind row t (N: none does).
+__device__ __forceinline__ int ends_behind(const ConvParams& p, int lo, long long t) {
+  int hi = p.N;
+  while (lo < hi) {
+    const int mid = lo + ((hi - lo) >> 1);  // (lo + hi may pass 31 bits)
+    if (min(max(p.cu[mid + 1], 0), p.T) > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
 // Row of the window of a token of sequence n, t = an absolute row: an input, or the state.
 template <typename T, int W>
 __device__ __forceinline__ Piece<T> tap(const ConvParams& p, const Span& s, int n, long long t,
@@ -185,17 +195,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
   for (int round = 0; round < (kVec ? kRounds - 1 : 1); ++round) request();
 
   // the sequence of token t0: the first one that ends behind it
-  int n = 0;
-  if (p.cu) {
-    int lo = 0, hi = p.N;
-    while (lo < hi) {
-      const int mid = lo + ((hi - lo) >> 1);  // (lo + hi may pass 31 bits)
-      if (min(max(p.cu[mid + 1], 0), p.T) > t0) hi = mid; else lo = mid + 1;
-    }
-    n = lo;
-  } else {
-    n = (int)(t0 / p.T);
-  }
+  int n = p.cu ? ends_behind(p, 0, t0) : (int)(t0 / p.T);
   if (n >= p.N) {  // behind the last sequence: left as it was
     if constexpr (kVec) cp_async_wait<0>();  // (no thread leaves while its copies are in flight)
     return;
@@ -244,13 +244,15 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p, int 
         const int tt = t + u;
         if (tt >= len) return;
         if (tt >= end) {  // the next sequence that has tokens begins
-          do {
-            if (++n >= p.N) {
-              if constexpr (kVec) cp_async_wait<0>();
-              return;
-            }
-            s = span_of(p, n);
-          } while (t0 + tt >= s.end);
+          if (++n < p.N) s = span_of(p, n);
+          if (n < p.N && t0 + tt >= s.end) {  // an empty one: past all of them
+            n = ends_behind(p, n + 1, t0 + tt);
+            if (n < p.N) s = span_of(p, n);
+          }
+          if (n >= p.N) {
+            if constexpr (kVec) cp_async_wait<0>();
+            return;
+          }
           begin = (int)max(s.begin - t0, 0ll);
           end = (int)min(s.end - t0, (long long)len);
 #pragma unroll
