@@ -1,6 +1,10 @@
 """Build libgdn.so in-tree with nvcc for sm_103a (no torch extension machinery), and beside
 it the Python extension that binds the layer operators (layer_binding.cpp, host C++).
 
+libgdn.so needs nvcc only.  The extension is compiled against the installed torch; without
+one (or with one that has no CUDA) it is left out, and where it does not compile libgdn.so
+is in place before the error is raised.
+
 Every .cu under csrc/ compiles to an object in parallel; the objects link into
 linear_attention_prefill_gb300/libgdn.so with the static CUDA runtime, so the
 library loads on a machine without a GPU driver (exported symbols can be
@@ -40,10 +44,17 @@ def _deps():
         os.path.join(os.path.dirname(PKG), "include", "gdn.h")]
 
 
-def _build_binding() -> str:
-    """Compile the layer operators' binding against the installed torch; returns its compiler
-    messages."""
-    import torch
+def _torch():
+    """The torch to compile the extension against; None without one that has CUDA."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch if torch.version.cuda else None
+
+
+def _build_binding(torch) -> None:
+    """Compile the layer operators' binding against the installed torch."""
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     tmp = BINDING + ".tmp"
@@ -58,18 +69,19 @@ def _build_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
     os.replace(tmp, BINDING)
-    return r.stderr
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    built = [LIB] + ([BINDING] if _torch() else [])
+    if not all(os.path.exists(b) for b in built):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(b) for b in built)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile and link libgdn.so; returns its path.  Raises on a compiler error."""
+    """Compile and link libgdn.so, and the binding; returns libgdn.so's path.  Raises on a compiler
+    error, one in the binding once libgdn.so is in place."""
     if not force and up_to_date():
         return LIB
     nvcc = nvcc_path()
@@ -88,9 +100,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_build_binding)
+        torch = _torch()
+        binding = ex.submit(_build_binding, torch) if torch else None
         results = list(ex.map(compile_one, _sources()))
-        binding.result()
     logs = "".join(err for _, err in results)
     if verbose and logs:
         sys.stderr.write(logs)
@@ -102,6 +114,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     os.replace(tmp, LIB)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write(logs)
+    if binding is not None:
+        binding.result()
+    elif verbose:
+        sys.stderr.write("no torch with CUDA: the layer operators' Python binding is left out\n")
     return LIB
 
 
