@@ -25,6 +25,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING = os.path.join(PKG, "_layer_native.so")
+BINDING_FOR = os.path.join(BUILD, "_layer_native.txt")  # what it was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,17 +45,29 @@ def _deps():
         os.path.join(os.path.dirname(PKG), "include", "gdn.h")]
 
 
-def _torch():
-    """The torch to compile the extension against; None without one that has CUDA."""
+def binding_key():
+    """What the extension is compiled against: torch's version and Python's ABI; None without a
+    torch that has CUDA."""
     try:
         import torch
     except ImportError:
         return None
-    return torch if torch.version.cuda else None
+    if not torch.version.cuda:
+        return None
+    return f"torch {torch.__version__} {torch.version.git_version} {sysconfig.get_config_var('SOABI')}"
 
 
-def _build_binding(torch) -> None:
-    """Compile the layer operators' binding against the installed torch."""
+def binding_built_for():
+    """The binding_key() that the extension in place was compiled against, or None."""
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_FOR):
+        return None
+    with open(BINDING_FOR) as f:
+        return f.read()
+
+
+def _build_binding(key: str) -> None:
+    """Compile the layer operators' binding against the installed torch, whose key it is."""
+    import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc_path()))
     tmp = BINDING + ".tmp"
@@ -68,11 +81,20 @@ def _build_binding(torch) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    if os.path.exists(BINDING_FOR):  # never a new extension beside the old one's key
+        os.remove(BINDING_FOR)
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(key)
 
 
 def up_to_date() -> bool:
-    built = [LIB] + ([BINDING] if _torch() else [])
+    built = [LIB]
+    key = binding_key()
+    if key is not None:
+        if binding_built_for() != key:
+            return False
+        built.append(BINDING)
     if not all(os.path.exists(b) for b in built):
         return False
     t = min(os.path.getmtime(b) for b in built)
@@ -100,8 +122,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        torch = _torch()
-        binding = ex.submit(_build_binding, torch) if torch else None
+        key = binding_key()
+        binding = ex.submit(_build_binding, key) if key is not None else None
         results = list(ex.map(compile_one, _sources()))
     logs = "".join(err for _, err in results)
     if verbose and logs:

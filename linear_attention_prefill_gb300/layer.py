@@ -15,6 +15,7 @@ from typing import Optional
 
 import torch
 
+from . import _build
 from .binding import _check, load_library
 
 _E4M3 = torch.float8_e4m3fn
@@ -31,11 +32,11 @@ def _load():
     """The extension module, told the library's entry points (once)."""
     global _native
     lib = load_library()
-    try:
-        from . import _layer_native
-    except ImportError as e:
-        raise RuntimeError("the layer operators' binding is not built: "
-                           "python -m linear_attention_prefill_gb300._build") from e
+    built_for, key = _build.binding_built_for(), _build.binding_key()
+    if built_for is None or built_for != key:  # another torch's C++ ABI is not to be loaded
+        raise RuntimeError(f"the layer operators' binding is built for {built_for or 'nothing'}, this is {key}: "
+                           "python -m linear_attention_prefill_gb300._build")
+    from . import _layer_native
     _layer_native.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRY_POINTS),
                        _check)
     _native = _layer_native

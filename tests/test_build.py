@@ -1,5 +1,5 @@
-"""What a build needs, on a small source tree: libgdn.so nvcc alone, the layer operators' binding a
-torch with CUDA."""
+"""What a build needs and when it is current, on a small source tree: libgdn.so from nvcc alone, the
+layer operators' binding for the torch and the Python that are there."""
 import os
 import sys
 
@@ -21,13 +21,15 @@ def tree(tmp_path, monkeypatch):
     pkg = str(tmp_path / "pkg")
     for name, value in dict(PKG=pkg, CSRC=str(csrc), BUILD=os.path.join(pkg, "_build"),
                             LIB=os.path.join(pkg, "libgdn.so"), BINDING=os.path.join(pkg, "_layer_native.so"),
-                            BINDING_SRC=str(csrc / "layer_binding.cpp")).items():
+                            BINDING_SRC=str(csrc / "layer_binding.cpp"),
+                            BINDING_FOR=os.path.join(pkg, "_build", "_layer_native.txt")).items():
         monkeypatch.setattr(_build, name, value)
     return csrc
 
 
 def test_library_without_torch(tree, monkeypatch):
     monkeypatch.setitem(sys.modules, "torch", None)  # import torch: ImportError
+    assert _build.binding_key() is None
     assert _build.build() == _build.LIB and os.path.exists(_build.LIB)
     assert not os.path.exists(_build.BINDING) and _build.up_to_date()
 
@@ -45,3 +47,34 @@ def test_library_beside_a_binding_that_does_not_compile(tree):
         _build.build()
     assert os.path.exists(_build.LIB) and not os.path.exists(_build.BINDING)
     assert not _build.up_to_date()
+
+
+def test_binding_is_current_for_one_torch_and_one_python(tree, monkeypatch):
+    import sysconfig
+
+    import torch
+    _build.build()
+    assert _build.up_to_date() and _build.binding_built_for() == _build.binding_key()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1+other")
+        assert not _build.up_to_date()
+    var = sysconfig.get_config_var
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda n: "cpython-399" if n == "SOABI" else var(n))
+        assert not _build.up_to_date()
+    assert _build.up_to_date()
+    os.remove(_build.BINDING_FOR)
+    assert not _build.up_to_date()
+    _build.build()
+    assert _build.up_to_date()
+    os.utime(_build.LIB, (1, 1))
+    assert not _build.up_to_date()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
+    from linear_attention_prefill_gb300 import layer
+    _build.build()
+    monkeypatch.setattr(layer, "_native", None)
+    monkeypatch.setattr(_build, "binding_built_for", lambda: "torch 0.0.1 cpython-399")
+    with pytest.raises(RuntimeError, match="0.0.1"):
+        layer._load()
