@@ -238,7 +238,7 @@ PyObject* conv_fwd(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x");
   const Kind k = kind_of(x, "x", 3);
   const IntArrayRef shape = x.sizes();
-  const int64_t D = shape[2];
+  const int D = small(shape[2], "D");
   int W;
   const float* w = taps(a[1], k.device, D, &W);
   const Batch b = batch_of(shape, a[7], k.device);
@@ -254,7 +254,7 @@ PyObject* conv_fwd(PyObject* const* a) {
                           : Output{nullptr, (Py_INCREF(Py_None), Py_None)};
   Held hs(sT.object);
   run(k.device, [&](gdn_stream_t st) {
-    return lib.conv[k.f32](xr.p, w, bias, s0, y.p, sT.p, b.n, b.t, (int)D, W, xr.stride, act, b.cu, st);
+    return lib.conv[k.f32](xr.p, w, bias, s0, y.p, sT.p, b.n, b.t, D, W, xr.stride, act, b.cu, st);
   });
   PyObject* r = PyTuple_New(2);
   if (!r) throw python_error();
@@ -268,7 +268,8 @@ PyObject* conv_step(PyObject* const* a) {
   const Tensor& x = tensor(a[0], "x");
   const Kind k = kind_of(x, "x", 2);
   const IntArrayRef shape = x.sizes();
-  const int64_t N = shape[0], D = shape[1];
+  const int64_t N = shape[0];
+  const int D = small(shape[1], "D");
   int W;
   const float* w = taps(a[1], k.device, D, &W);
   const Rows xr = rows(a[0], "x", k.type, k.device, shape);
@@ -278,7 +279,7 @@ PyObject* conv_step(PyObject* const* a) {
   const Output y = output(a[4], "y", k.type, k.device, shape);
   Held hy(y.object);
   run(k.device, [&](gdn_stream_t st) {
-    return lib.conv_step[k.f32](xr.p, w, bias, s, y.p, n, (int)D, W, xr.stride, act, st);
+    return lib.conv_step[k.f32](xr.p, w, bias, s, y.p, n, D, W, xr.stride, act, st);
   });
   return hy.take();
 }

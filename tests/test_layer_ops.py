@@ -858,3 +858,19 @@ def test_conv_passes_many_empty_sequences_at_once(cuda_lib, dtype, D):
         assert_within(y, ref, err, dt, "y")
         assert torch.equal(y, want)
     assert min(times) < 5.0  # ms
+
+
+def test_channels_beyond_31_bits_are_refused(cuda_lib):
+    """Never cut down to their low bits."""
+    D, w, A = 2 ** 32 + 64, torch.ones(64, 4, device="cuda"), -torch.ones(64, 16, device="cuda")
+    x = torch.empty(1, 1, D, dtype=torch.bfloat16, device="cuda")
+    s, h = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 64, 16, device="cuda")
+    for call in (lambda: cuda_lib.gdn_short_conv_fwd(x, w), lambda: cuda_lib.gdn_short_conv_step(x[0], w, s)):
+        with pytest.raises(ValueError, match=f"D = {D}"):
+            call()
+    bc = x[..., :16].contiguous()
+    for call in (lambda: cuda_lib.gdn_s6_chunk_fwd(x, x, A, bc, bc),
+                 lambda: cuda_lib.gdn_s6_recurrent_step(x[0], x[0], A, bc[0], bc[0], h),
+                 lambda: cuda_lib.gdn_rms_norm_fwd(x, w[:, 0].contiguous())):
+        with pytest.raises(ValueError):
+            call()
