@@ -409,7 +409,8 @@ gdn_status gdn_short_conv_step_f32(const float* x, const float* w, const float* 
  *   h_t[n] = exp(D_t A[d, n]) h_{t-1}[n] + D_t x_t B_t[n]
  *   y_t    = (sum_n C_t[n] h_t[n] + D[d] x_t) silu(z_t)
  *
- *   x, dt    N rows of T tokens (or one packed row) of dim channels, bf16
+ *   x, dt    N rows of T tokens (or one packed row) of dim channels, bf16; dim at
+ *            most 2^30 (2^26 in the step)
  *   A        [dim, Ns] fp32 (negative: a decay), 16-byte aligned; Ns in 1..64
  *   B, C     rows of Ns, bf16, shared by every channel
  *   D        [dim] fp32 or NULL (no skip);  dt_bias  [dim] fp32 or NULL
@@ -460,6 +461,10 @@ gdn_status gdn_s6_recurrent_step_f32(const float* x, const float* dt, const floa
  *
  *   r = x + residual,   y = r / sqrt(mean(r^2) + eps) * w * silu(gate)
  *
+ * The one form of gate is SiLU behind the norm, a Gated DeltaNet layer's.  Not
+ * offered: a sigmoid gate (Kimi Delta Attention) and a gate before the norm
+ * (Mamba-2); those layers apply theirs themselves and use the norm without.
+ *
  *   x, gate       tokens of `heads` rows of D, x_stride / gate_stride elements
  *                 from token to token (the rows of a token follow each other);
  *                 gate may be NULL
@@ -475,7 +480,9 @@ gdn_status gdn_s6_recurrent_step_f32(const float* x, const float* dt, const floa
  * gdn_rms_norm_fwd_e4m3(_f32): y in 8 bits (e4m3, saturating at 448) with fp32
  * scales [tokens, heads, ceil(D / group)], one per `group` columns (32, 64 or
  * 128), or per row with group = 0: scale = max|y| / 448, at least 2^-126, and 1
- * where every y is 0; the stored value is y / scale rounded to nearest.
+ * where every y is 0; the stored value is y times the scale's reciprocal, rounded
+ * to nearest.  Scale, reciprocal and product are within a few fp32 roundings, so
+ * where y / scale lies that close to a tie the other neighbour may be stored.
  */
 gdn_status gdn_rms_norm_fwd(const void* x, const float* w, const void* residual, const void* gate,
                             void* y, void* residual_out, long long tokens, int heads, int D,

@@ -11,9 +11,11 @@ S6Split s6_split(int N, int T, int dim, int Ns, bool packed) {
   const long long per_seq = (packed ? (long long)T : (long long)N * T) / N;  // packed: their mean
   const long long waves = (ctas + kSms - 1) / kSms;
   // Cycles an SM takes for a token of 32 channels (measured at Ns = 16, bf16, 4096 tokens with
-  // the launch and the ends): 62 with one CTA, 117 with two, 192 with four; 74 for the two passes of a split channel, with four CTAs an SM;
-  // 170 for the two passes along one chunk, and about 10000 for the summaries' launch and the
-  // chunks' beginnings.
+  // the launch and the ends): 62 with one CTA, 117 with two, 192 with four (the rule's 48 n + 20
+  // gives 116 and 212: at four and more a split is taken a little early); 74 for the two passes of
+  // a split channel, with four CTAs an SM; 170 for the two passes along one chunk, and about 10000
+  // for the summaries' launch and the chunks' beginnings.  Other state counts and fp32 go by the
+  // same numbers, which were not measured for them (with 64 states, for one, a single CTA fits an SM).
   const auto cost = [](long long ctas_an_sm) { return ctas_an_sm == 1 ? 62 : 48 * ctas_an_sm + 20; };
   const auto chunk_of = [&](long long parts) {
     parts = parts < 2 ? 2 : parts > 128 ? 128 : parts;

@@ -22,15 +22,17 @@
 // partial sums over n, the skip and the gate into y; and keep the copies of the coming tiles in
 // flight (cp.async, a ring of four).  One barrier a tile.
 //
-// What bounds it is the path between the schedulers and the special-function units and shared
+// What it works against is the path between the schedulers and the special-function units and shared
 // memory: a lane takes 4 bytes a clock and SM from shared memory, whatever lanes share, so the
 // bytes per (channel, state) count.  A lane with four states of two channels reads 6 (D and Dx
 // 16 bytes, B and C 32, for 8 products); one with a single channel 10, or 6 where it takes bf16 B
 // and C as they are.  Cycles an SM takes for a token of 32 channels (Ns = 16, 1.92 GHz, 16384
 // tokens of 4864 channels a sequence): bf16 58 with one CTA an SM (one channel a lane), 54 with
 // two, 46 with four; fp32 62, 55 and 51.  The exponentials alone are 16, the multiply-adds 16,
-// the reads 24 or more.  4096 tokens of 5120 channels take 144 us; their bytes alone would take
-// 25.
+// the reads 24 or more.  4096 tokens of 5120 channels take 145 us; their bytes alone would take
+// 25.  Whole sequences, one CTA an SM, keep neither the issue slots (57 %) nor the shared-memory path
+// (57 %) full: the barrier of every tile, where the two kinds of warps wait for one another, is
+// their first stall.
 //
 // Splitting over time.  A CTA per 32 channels leaves SMs idle when there are few of them.
 // Channels beyond the whole-sequence ones are split over time: a first launch computes the

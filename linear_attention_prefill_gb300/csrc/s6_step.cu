@@ -17,7 +17,10 @@ constexpr int kStepThreads = 256;
 
 // kFull: Ns is 4 LPC and rows of B and C are aligned, so every lane has four states.  Bounds of
 // four blocks an SM: 64 registers have the loads in flight at once (16.5 us; 56 by the compiler's
-// own choice 18.2, bounds of five 17.4, of three 17.5).
+// own choice 18.2, bounds of five 17.4, of three 17.5).  Measured in bf16 with 16 states; fp32 with the
+// same bounds spills 36 to 100 bytes (1 to 4 states off whole vectors: 332) in every variant but
+// whole 16, 32 and 64 states (128 x 5120, events around a call, bf16 and fp32: 16 states 19.9 and
+// 21.6 us, 8 states 14.5 and 20.6).
 template <typename T, int LPC, int kSeqs, bool kFull>
 __global__ void __launch_bounds__(kStepThreads, 4) s6_step_kernel(const S6Params p, int per_row) {
   // sequences a lane prepares and finishes: kOwn from number ln * kOwn on, of the kSeqs

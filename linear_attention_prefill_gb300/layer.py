@@ -140,13 +140,16 @@ def gdn_rms_norm_fwd(x, weight, residual=None, gate=None, y=None, residual_out=N
                      eps: float = 1e-6, out_dtype=None, group: Optional[int] = None, stream=None):
     """RMS norm of the rows of x [..., D]; returns (y, scales, residual_out).
 
-    r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight * silu(gate).  x, residual, gate
-    are bf16 or fp32, all the same; weight [D] fp32.  x and gate may be slices: rows a
-    constant stride apart, or [..., H, D] with dense H D and a constant stride before it.
+    r = x + residual; y = r / sqrt(mean(r^2) + eps) * weight * silu(gate) (the gate of a Gated
+    DeltaNet layer; there is no sigmoid gate and none before the norm).  x, residual, gate
+    are bf16 or fp32, all the same; weight [D] fp32.  x and gate may be slices, both in one of two
+    forms: rows a constant stride apart, or [..., H, D] with dense H D and a constant stride before it.
     residual is contiguous and residual_out (a fresh tensor, or residual itself: in place) takes
     r in x's type.  out_dtype torch.float8_e4m3fn gives y in 8 bits with fp32
     scales [..., ceil(D / group)], one per ``group`` (32, 64, 128) columns or one a row (None):
-    scale = max|y| / 448 (1 for zeros).  scales and residual_out are None where there are none.
+    scale = max|y| / 448 (1 for zeros); a value is y times the scale's reciprocal, rounded to nearest
+    (within a few fp32 roundings of a tie, either way).  scales and residual_out are None where there
+    are none.
     """
     if stream is not None:
         with _on(stream, x):
