@@ -25,7 +25,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING = os.path.join(PKG, "_layer_native.so")
-BINDING_FOR = os.path.join(BUILD, "_layer_native.txt")  # what it was compiled against
+BINDING_FOR = os.path.join(PKG, "_layer_native.txt")  # what it was compiled against, kept beside it
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
