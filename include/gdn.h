@@ -504,6 +504,152 @@ gdn_status gdn_rms_norm_fwd_e4m3_f32(const float* x, const float* w, const float
                                      float eps, gdn_stream_t stream);
 
 /*
+ * gdn_glr_chunk_fwd - gated linear recurrence: the plainest member of the family, one number of
+ * state per channel, with a gate for each token.  Per sequence and channel, tokens in order:
+ *
+ *   h_t = a_t h_{t-1} + s_t x_t,   y_t = h_t,   a_t = exp(L_t)
+ *   L_t = g_t (GDN_GLR_GATE_LOG), log sigmoid(g_t) (.._SIGMOID), rate sigmoid(g_t) (.._RATE)
+ *   s_t = 1 (GDN_GLR_INPUT_PLAIN), 1 - a_t (.._LINEAR), sqrt(1 - a_t^2) (.._SQRT)
+ *
+ *   x, g     N rows of T tokens (or one packed row) of D channels, bf16; D at most 2^30; g <= 0
+ *            with the log gate (a decay)
+ *   rate     [D] fp32, <= 0, with GDN_GLR_GATE_RATE and only with it
+ *   h0, hT   [N, D] fp32, NULL for zeros / to skip; hT may equal h0
+ *   y        [tokens, D] bf16 (fp32 states, rounded once)
+ *   states   [rows, ceil(T / 64), D] fp32 (rows: N, or 1 with cu_seqlens), or NULL: the state before
+ *            every 64th token of a row, for the gradient; before the first token h0 (zeros with
+ *            cu_seqlens); chunks that start behind the last sequence are left as they were
+ *
+ * gdn_glr_recurrent_step: one token per sequence, h [N, D] in place.
+ *
+ * gdn_glr_chunk_bwd - the gradient.  x, g, rate, h0, gate, input_norm, cu_seqlens and states as in
+ * (and from) the forward; dy [tokens, D] (dy_stride) and dhT [N, D] fp32 (or NULL) are the
+ * gradients of y and hT.
+ *
+ *   dx, dg   [tokens, D] bf16;  drate [D] fp32, exactly with rate;  dh0 [N, D] fp32 or NULL
+ *
+ * The states come from fp32 throughout, never from rounded y; sums are fp32 in a fixed order.  With
+ * .._SQRT the weight has no derivative at a_t = 1; its share of dg is left out there.  The rate's
+ * gradient needs gdn_glr_chunk_bwd_workspace_size(...) bytes (0: none), as the S6 scan's workspace.
+ */
+enum { GDN_GLR_GATE_LOG = 0, GDN_GLR_GATE_SIGMOID = 1, GDN_GLR_GATE_RATE = 2 };
+enum { GDN_GLR_INPUT_PLAIN = 0, GDN_GLR_INPUT_LINEAR = 1, GDN_GLR_INPUT_SQRT = 2 };
+gdn_status gdn_glr_chunk_fwd(const void* x, const void* g, const float* rate, const float* h0, void* y, float* hT,
+                             float* states, int N, int T, int D, long long x_stride, long long g_stride, int gate,
+                             int input_norm, const int32_t* cu_seqlens, gdn_stream_t stream);
+gdn_status gdn_glr_chunk_fwd_f32(const float* x, const float* g, const float* rate, const float* h0, float* y,
+                                 float* hT, float* states, int N, int T, int D, long long x_stride,
+                                 long long g_stride, int gate, int input_norm, const int32_t* cu_seqlens,
+                                 gdn_stream_t stream);
+gdn_status gdn_glr_recurrent_step(const void* x, const void* g, const float* rate, float* h, void* y, int N, int D,
+                                  long long x_stride, long long g_stride, int gate, int input_norm,
+                                  gdn_stream_t stream);
+gdn_status gdn_glr_recurrent_step_f32(const float* x, const float* g, const float* rate, float* h, float* y, int N,
+                                      int D, long long x_stride, long long g_stride, int gate, int input_norm,
+                                      gdn_stream_t stream);
+size_t gdn_glr_chunk_bwd_workspace_size(int N, int T, int D, int gate, int has_cu_seqlens);
+gdn_status gdn_glr_chunk_bwd(const void* dy, const void* x, const void* g, const float* rate, const float* h0,
+                             const float* states, const float* dhT, void* dx, void* dg, float* drate, float* dh0,
+                             int N, int T, int D, long long dy_stride, long long x_stride, long long g_stride,
+                             int gate, int input_norm, const int32_t* cu_seqlens, void* workspace,
+                             size_t workspace_bytes, gdn_stream_t stream);
+gdn_status gdn_glr_chunk_bwd_f32(const float* dy, const float* x, const float* g, const float* rate,
+                                 const float* h0, const float* states, const float* dhT, float* dx, float* dg,
+                                 float* drate, float* dh0, int N, int T, int D, long long dy_stride,
+                                 long long x_stride, long long g_stride, int gate, int input_norm,
+                                 const int32_t* cu_seqlens, void* workspace, size_t workspace_bytes,
+                                 gdn_stream_t stream);
+
+/*
+ * gdn_layer_norm_fwd - layer norm of rows of D columns, with the residual's addition:
+ *
+ *   r = x + residual,   y = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * w + b
+ *
+ *   x             rows of D, x_stride elements apart;  D at most 32768;  eps >= 0
+ *   w, b          [D] fp32, each NULL for ones / zeros
+ *   residual      [rows, D], or NULL; residual_out (given exactly with it, may equal it) takes
+ *                 r, rounded once
+ *   y             [rows, D]
+ *
+ * gdn_layer_norm_bwd - the gradient.  x is what was normed (with a residual: residual_out; mean and
+ * variance are taken from it again), dy (dy_stride) the gradient of y, dres [rows, D] (or NULL) a
+ * gradient that is added to dx, as the one that reaches residual_out:
+ *
+ *   xh = (x - mean) rstd,  u = dy w:   dx = rstd (u - mean(u) - xh mean(u xh)) + dres
+ *   dw = sum of dy xh,  db = sum of dy over the rows;  [D] fp32, both or neither (NULL)
+ *
+ * dx [rows, D] may equal dres.  dw and db are fp32 sums in a fixed order, which need a workspace of
+ * gdn_layer_norm_bwd_workspace_size(rows, D) bytes, 256-byte aligned; with workspace NULL the call
+ * takes it from the stream-ordered pool.  Calls that share a workspace must be ordered on one stream.
+ * All tensors are bf16 (_f32: fp32) except those named fp32.
+ */
+gdn_status gdn_layer_norm_fwd(const void* x, const float* w, const float* b, const void* residual, void* y,
+                              void* residual_out, long long rows, int D, long long x_stride, float eps,
+                              gdn_stream_t stream);
+gdn_status gdn_layer_norm_fwd_f32(const float* x, const float* w, const float* b, const float* residual, float* y,
+                                  float* residual_out, long long rows, int D, long long x_stride, float eps,
+                                  gdn_stream_t stream);
+size_t gdn_layer_norm_bwd_workspace_size(long long rows, int D);
+gdn_status gdn_layer_norm_bwd(const void* dy, const void* x, const float* w, const void* dres, void* dx, float* dw,
+                              float* db, long long rows, int D, long long dy_stride, long long x_stride, float eps,
+                              void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+gdn_status gdn_layer_norm_bwd_f32(const float* dy, const float* x, const float* w, const float* dres, float* dx,
+                                  float* dw, float* db, long long rows, int D, long long dy_stride,
+                                  long long x_stride, float eps, void* workspace, size_t workspace_bytes,
+                                  gdn_stream_t stream);
+
+/*
+ * gdn_rotary_fwd - rotary positions of q and k (as before ssd_chunk_fwd or a decode step).  Pair i
+ * of the first R columns of every head is turned by its angle:
+ *
+ *   (x, y) -> magnitude (x cos - y sin, y cos + x sin),   angle = position * turns[i] / 2^64 turns
+ *
+ *   q, k           tokens of Hq, Hk heads of D columns (D at most 1024), q_stride, k_stride elements
+ *                  from token to token; Hk = 0 with k and k_out NULL: none
+ *   q_out, k_out   the same, q_out_stride, k_out_stride; each may be its own input (in place).
+ *                  Columns from R on are passed through
+ *   interleaved    0: pair i is columns i and i + R / 2; else columns 2 i and 2 i + 1
+ *   turns          [R / 2] on the device, from gdn_rotary_turns
+ *   positions      [tokens] int32, or NULL: counted from the first token of each sequence (N rows of
+ *                  T tokens, or cu_seqlens), plus offsets [N] int32 (NULL: zeros)
+ *
+ * The angle is exact modulo one turn (64-bit fixed point) at every position.  Rows behind the last
+ * sequence are left as they were.  gdn_rotary_bwd undoes the turn and scales the same: the gradient
+ * of q and k from those of q_out and k_out.  bf16 (_f32: fp32) in and out, fp32 between.
+ *
+ * gdn_rotary_turns - the table, on the host: base^(-2 i / R) radians a position as 2^64ths of a
+ * turn, and the magnitude (1, but with YARN).  For contexts `factor` (>= 1) times as long:
+ *   GDN_ROTARY_LINEAR  frequencies divided by factor
+ *   GDN_ROTARY_NTK     base times factor^(R / (R - 2))
+ *   GDN_ROTARY_YARN    frequencies that make more than beta_fast (32) turns within original_length stay,
+ *                      those below beta_slow (1) turns are divided by factor, between them a line by
+ *                      index; magnitude 0.1 ln(factor) + 1
+ */
+enum { GDN_ROTARY_PLAIN = 0, GDN_ROTARY_LINEAR = 1, GDN_ROTARY_NTK = 2, GDN_ROTARY_YARN = 3 };
+gdn_status gdn_rotary_turns(int R, double base, int scaling, double factor, double original_length, double beta_fast,
+                            double beta_slow, unsigned long long* turns, float* magnitude);
+gdn_status gdn_rotary_fwd(const void* q, const void* k, const unsigned long long* turns, const int32_t* positions,
+                          const int32_t* offsets, const int32_t* cu_seqlens, void* q_out, void* k_out, int N, int T,
+                          int Hq, int Hk, int D, int R, long long q_stride, long long k_stride,
+                          long long q_out_stride, long long k_out_stride, int interleaved, float magnitude,
+                          gdn_stream_t stream);
+gdn_status gdn_rotary_fwd_f32(const float* q, const float* k, const unsigned long long* turns,
+                              const int32_t* positions, const int32_t* offsets, const int32_t* cu_seqlens,
+                              float* q_out, float* k_out, int N, int T, int Hq, int Hk, int D, int R,
+                              long long q_stride, long long k_stride, long long q_out_stride,
+                              long long k_out_stride, int interleaved, float magnitude, gdn_stream_t stream);
+gdn_status gdn_rotary_bwd(const void* q, const void* k, const unsigned long long* turns, const int32_t* positions,
+                          const int32_t* offsets, const int32_t* cu_seqlens, void* q_out, void* k_out, int N, int T,
+                          int Hq, int Hk, int D, int R, long long q_stride, long long k_stride,
+                          long long q_out_stride, long long k_out_stride, int interleaved, float magnitude,
+                          gdn_stream_t stream);
+gdn_status gdn_rotary_bwd_f32(const float* q, const float* k, const unsigned long long* turns,
+                              const int32_t* positions, const int32_t* offsets, const int32_t* cu_seqlens,
+                              float* q_out, float* k_out, int N, int T, int Hq, int Hk, int D, int R,
+                              long long q_stride, long long k_stride, long long q_out_stride,
+                              long long k_out_stride, int interleaved, float magnitude, gdn_stream_t stream);
+
+/*
  * gdn_device_status - waits for `stream`, then reads and clears the device
  * error word.  The kernels record there (the first record stays until read):
  * a bounded device-side wait that gave up (GDN_ERR_TIMEOUT); a KDA log-decay

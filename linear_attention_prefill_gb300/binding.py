@@ -36,6 +36,13 @@ _S6_ARGS = [_P] * 11 + [_I] * 4 + [_L] * 5 + [_I, _P, _P, _SZ, _P]
 _S6_STEP_ARGS = [_P] * 10 + [_I] * 3 + [_L] * 5 + [_I, _P]
 _NORM_ARGS = [_P] * 6 + [_L, _I, _I, _L, _L, _F, _P]
 _NORM8_ARGS = [_P] * 7 + [_L, _I, _I, _L, _L, _I, _F, _P]
+_GLR_ARGS = [_P] * 7 + [_I] * 3 + [_L] * 2 + [_I] * 2 + [_P, _P]
+_GLR_STEP_ARGS = [_P] * 5 + [_I] * 2 + [_L] * 2 + [_I] * 2 + [_P]
+_GLR_BWD_ARGS = [_P] * 11 + [_I] * 3 + [_L] * 3 + [_I] * 2 + [_P, _P, _SZ, _P]
+_LN_ARGS = [_P] * 6 + [_L, _I, _L, _F, _P]
+_LN_BWD_ARGS = [_P] * 7 + [_L, _I, _L, _L, _F, _P, _SZ, _P]
+_ROTARY_ARGS = [_P] * 8 + [_I] * 6 + [_L] * 4 + [_I, _F, _P]
+_D = ctypes.c_double
 SIGNATURES = {
     "gdn_chunk_fwd": (_I, _FWD_ARGS),
     "gdn_chunk_fwd_ex": (_I, _FWD_ARGS[:-1] + [_U, _P, _SZ, _P]),
@@ -76,6 +83,23 @@ SIGNATURES = {
     "gdn_rms_norm_fwd_f32": (_I, _NORM_ARGS),
     "gdn_rms_norm_fwd_e4m3": (_I, _NORM8_ARGS),
     "gdn_rms_norm_fwd_e4m3_f32": (_I, _NORM8_ARGS),
+    "gdn_glr_chunk_fwd": (_I, _GLR_ARGS),
+    "gdn_glr_chunk_fwd_f32": (_I, _GLR_ARGS),
+    "gdn_glr_recurrent_step": (_I, _GLR_STEP_ARGS),
+    "gdn_glr_recurrent_step_f32": (_I, _GLR_STEP_ARGS),
+    "gdn_glr_chunk_bwd_workspace_size": (_SZ, [_I] * 5),
+    "gdn_glr_chunk_bwd": (_I, _GLR_BWD_ARGS),
+    "gdn_glr_chunk_bwd_f32": (_I, _GLR_BWD_ARGS),
+    "gdn_layer_norm_fwd": (_I, _LN_ARGS),
+    "gdn_layer_norm_fwd_f32": (_I, _LN_ARGS),
+    "gdn_layer_norm_bwd_workspace_size": (_SZ, [_L, _I]),
+    "gdn_layer_norm_bwd": (_I, _LN_BWD_ARGS),
+    "gdn_layer_norm_bwd_f32": (_I, _LN_BWD_ARGS),
+    "gdn_rotary_turns": (_I, [_I, _D, _I, _D, _D, _D, _D, _P, _P]),
+    "gdn_rotary_fwd": (_I, _ROTARY_ARGS),
+    "gdn_rotary_fwd_f32": (_I, _ROTARY_ARGS),
+    "gdn_rotary_bwd": (_I, _ROTARY_ARGS),
+    "gdn_rotary_bwd_f32": (_I, _ROTARY_ARGS),
 }
 
 _lib = None

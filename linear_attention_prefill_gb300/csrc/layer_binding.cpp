@@ -38,6 +38,14 @@ struct Library {
   decltype(&gdn_s6_chunk_fwd_workspace_size) s6_workspace;
   decltype(&gdn_rms_norm_fwd) norm[2];
   decltype(&gdn_rms_norm_fwd_e4m3) norm8[2];
+  decltype(&gdn_glr_chunk_fwd) glr[2];
+  decltype(&gdn_glr_recurrent_step) glr_step[2];
+  decltype(&gdn_glr_chunk_bwd) glr_bwd[2];
+  decltype(&gdn_glr_chunk_bwd_workspace_size) glr_workspace;
+  decltype(&gdn_layer_norm_fwd) ln[2];
+  decltype(&gdn_layer_norm_bwd) ln_bwd[2];
+  decltype(&gdn_layer_norm_bwd_workspace_size) ln_workspace;
+  decltype(&gdn_rotary_fwd) rotary[2][2];  // forward, backward
 } lib;
 PyObject* raise_status = nullptr;  // called with a status that is not GDN_OK
 
@@ -437,6 +445,246 @@ PyObject* norm_fwd(PyObject* const* a) {
   return r;
 }
 
+// ---- gated linear recurrence ---------------------------------------------------------------
+PyObject* none() { return Py_INCREF(Py_None), Py_None; }
+// The caller's output, or a fresh one where `wanted`, or None.
+Output maybe_output(PyObject* o, bool wanted, const char* name, ScalarType type, int device, IntArrayRef shape) {
+  return o != Py_None || wanted ? output(o, name, type, device, shape) : Output{nullptr, none()};
+}
+// A call's scratch: the caller's workspace, or one from the allocator of the current stream, to
+// which it goes back when the call is enqueued.
+struct Scratch {
+  Tensor own;
+  void* p = nullptr;
+  size_t bytes = 0;
+  Scratch(PyObject* o, size_t need, int device) {
+    if (o != Py_None) {
+      const Tensor& t = tensor(o, "workspace");
+      p = dense(t, "workspace", ScalarType::Byte, device, t.sizes());
+      bytes = (size_t)t.numel();
+    } else if (need) {
+      own = fresh({(int64_t)need}, ScalarType::Byte, device);
+      p = own.data_ptr();
+      bytes = need;
+    }
+  }
+};
+template <size_t n>
+PyObject* tuple_of(Held* (&&held)[n]) {
+  PyObject* r = PyTuple_New((Py_ssize_t)n);
+  if (!r) throw python_error();
+  for (size_t i = 0; i < n; ++i) PyTuple_SET_ITEM(r, (Py_ssize_t)i, held[i]->take());
+  return r;
+}
+
+// x, g, rate, h0, y, hT, states, gate, input_norm, cu_seqlens, output_final_state, output_states
+PyObject* glr_fwd(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x");
+  const Kind k = kind_of(x, "x", 3);
+  const int dev = k.device;
+  const IntArrayRef shape = x.sizes();
+  const int D = small(shape[2], "D"), gate = (int)PyLong_AsLong(a[7]), norm = (int)PyLong_AsLong(a[8]);
+  const Batch b = batch_of(shape, a[9], dev);
+  const Rows xr = rows(a[0], "x", k.type, dev, shape), gr = rows(a[1], "g", k.type, dev, shape);
+  const float* rate = param(a[2], "rate", dev, {D});
+  const int64_t states[2] = {b.n, D}, kept[3] = {shape[0], (shape[1] + 63) / 64, D};
+  const float* h0 = param(a[3], "h0", dev, states);
+  const Output y = output(a[4], "y", k.type, dev, shape);
+  Held hy(y.object);
+  const Output hT = maybe_output(a[5], truth(a[10]), "hT", kF32, dev, states);
+  Held hh(hT.object);
+  const Output st = maybe_output(a[6], truth(a[11]), "states", kF32, dev, kept);
+  Held hs(st.object);
+  run(dev, [&](gdn_stream_t s) {
+    return lib.glr[k.f32](xr.p, gr.p, rate, h0, y.p, static_cast<float*>(hT.p), static_cast<float*>(st.p), b.n, b.t, D,
+                          xr.stride, gr.stride, gate, norm, b.cu, s);
+  });
+  return tuple_of({&hy, &hh, &hs});
+}
+
+// x, g, h, rate, y, gate, input_norm
+PyObject* glr_step(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x");
+  const Kind k = kind_of(x, "x", 2);
+  const int dev = k.device;
+  const IntArrayRef shape = x.sizes();
+  const int n = small(shape[0], "the batch"), D = small(shape[1], "D");
+  const int gate = (int)PyLong_AsLong(a[5]), norm = (int)PyLong_AsLong(a[6]);
+  const Rows xr = rows(a[0], "x", k.type, dev, shape), gr = rows(a[1], "g", k.type, dev, shape);
+  float* h = static_cast<float*>(dense(a[2], "h", kF32, dev, shape));
+  const float* rate = param(a[3], "rate", dev, {D});
+  const Output y = output(a[4], "y", k.type, dev, shape);
+  Held hy(y.object);
+  run(dev, [&](gdn_stream_t s) {
+    return lib.glr_step[k.f32](xr.p, gr.p, rate, h, y.p, n, D, xr.stride, gr.stride, gate, norm, s);
+  });
+  return hy.take();
+}
+
+// dy, x, g, states, rate, h0, dhT, dx, dg, drate, dh0, gate, input_norm, cu_seqlens, workspace
+PyObject* glr_bwd(PyObject* const* a) {
+  const Tensor& x = tensor(a[1], "x");
+  const Kind k = kind_of(x, "x", 3);
+  const int dev = k.device;
+  const IntArrayRef shape = x.sizes();
+  const int D = small(shape[2], "D"), gate = (int)PyLong_AsLong(a[11]), norm = (int)PyLong_AsLong(a[12]);
+  const Batch b = batch_of(shape, a[13], dev);
+  const Rows dr = rows(a[0], "dy", k.type, dev, shape), xr = rows(a[1], "x", k.type, dev, shape),
+             gr = rows(a[2], "g", k.type, dev, shape);
+  const int64_t states[2] = {b.n, D}, kept[3] = {shape[0], (shape[1] + 63) / 64, D};
+  const float* st = static_cast<const float*>(dense(a[3], "states", kF32, dev, kept));
+  const float *rate = param(a[4], "rate", dev, {D}), *h0 = param(a[5], "h0", dev, states),
+              *dhT = param(a[6], "dhT", dev, states);
+  if (a[4] == Py_None && a[9] != Py_None) value_error("drate needs a rate");
+  const Output dx = output(a[7], "dx", k.type, dev, shape);
+  Held hx(dx.object);
+  const Output dg = output(a[8], "dg", k.type, dev, shape);
+  Held hg(dg.object);
+  const Output drate = maybe_output(a[9], a[4] != Py_None, "drate", kF32, dev, {D});
+  Held hr(drate.object);
+  const Output dh0 = maybe_output(a[10], a[5] != Py_None, "dh0", kF32, dev, states);
+  Held hh(dh0.object);
+  const Scratch ws(a[14], lib.glr_workspace(b.n, b.t, D, gate, b.cu != nullptr), dev);
+  run(dev, [&](gdn_stream_t s) {
+    return lib.glr_bwd[k.f32](dr.p, xr.p, gr.p, rate, h0, st, dhT, dx.p, dg.p, static_cast<float*>(drate.p),
+                              static_cast<float*>(dh0.p), b.n, b.t, D, dr.stride, xr.stride, gr.stride, gate, norm,
+                              b.cu, ws.p, ws.bytes, s);
+  });
+  return tuple_of({&hx, &hg, &hr, &hh});
+}
+
+// ---- layer norm ------------------------------------------------------------------------------
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+// x, weight, bias, residual, y, residual_out, eps
+PyObject* ln_fwd(PyObject* const* a) {
+  const Tensor& x = tensor(a[0], "x");
+  const Kind k = kind_of(x, "x", -1);
+  const int dev = k.device;
+  const IntArrayRef shape = x.sizes();
+  const int D = small(shape[x.dim() - 1], "D");
+  const Rows xr = rows(a[0], "x", k.type, dev, shape);
+  const float *w = param(a[1], "weight", dev, {D}), *b = param(a[2], "bias", dev, {D});
+  const float eps = (float)number(a[6]);
+  const void* res = maybe(a[3], "residual", k.type, dev, shape);
+  if (a[3] == Py_None && a[5] != Py_None) value_error("residual_out needs a residual");
+  const Output y = output(a[4], "y", k.type, dev, shape);
+  Held hy(y.object);
+  const Output out = maybe_output(a[5], a[3] != Py_None, "residual_out", k.type, dev, shape);
+  Held ho(out.object);
+  const int64_t n = D ? x.numel() / D : 0;
+  run(dev, [&](gdn_stream_t s) {
+    return lib.ln[k.f32](xr.p, w, b, res, y.p, out.p, n, D, xr.stride, eps, s);
+  });
+  return tuple_of({&hy, &ho});
+}
+
+// dy, x, weight, dres, dx, dweight, dbias, eps, param_grads, workspace
+PyObject* ln_bwd(PyObject* const* a) {
+  const Tensor& x = tensor(a[1], "x");
+  const Kind k = kind_of(x, "x", -1);
+  const int dev = k.device;
+  const IntArrayRef shape = x.sizes();
+  const int D = small(shape[x.dim() - 1], "D");
+  const Rows dr = rows(a[0], "dy", k.type, dev, shape), xr = rows(a[1], "x", k.type, dev, shape);
+  const float* w = param(a[2], "weight", dev, {D});
+  const void* res = maybe(a[3], "dres", k.type, dev, shape);
+  const float eps = (float)number(a[7]);
+  const bool grads = truth(a[8]);
+  if (!grads && (a[5] != Py_None || a[6] != Py_None)) value_error("dweight and dbias belong to param_grads");
+  const Output dx = output(a[4], "dx", k.type, dev, shape);
+  Held hx(dx.object);
+  const Output dw = maybe_output(a[5], grads, "dweight", kF32, dev, {D});
+  Held hw(dw.object);
+  const Output db = maybe_output(a[6], grads, "dbias", kF32, dev, {D});
+  Held hb(db.object);
+  const int64_t n = D ? x.numel() / D : 0;
+  const Scratch ws(a[9], grads ? lib.ln_workspace(n, D) : 0, dev);
+  run(dev, [&](gdn_stream_t s) {
+    return lib.ln_bwd[k.f32](dr.p, xr.p, w, res, dx.p, static_cast<float*>(dw.p), static_cast<float*>(db.p), n, D,
+                             dr.stride, xr.stride, eps, ws.p, ws.bytes, s);
+  });
+  return tuple_of({&hx, &hw, &hb});
+}
+
+// ---- rotary positions ------------------------------------------------------------------------
+// A tensor of tokens of [H, D], tokens a constant stride apart.
+Rows token_rows(const Tensor& t, const char* name) {
+  const int64_t stride = stride_of(t, 2);
+  if (stride < 0) value_error(name, " with strides ", t.strides(), ": a token's heads must be dense and tokens a "
+                              "constant stride apart");
+  return {t.data_ptr(), stride};
+}
+// q, k, turns, positions, q_out, k_out, magnitude, interleaved, cu_seqlens, offsets, backward
+PyObject* rotary(PyObject* const* a) {
+  const Tensor& q = tensor(a[0], "q");
+  const Kind kind = kind_of(q, "q", -1);
+  const int dev = kind.device;
+  const IntArrayRef shape = q.sizes();
+  if (q.dim() < 3) value_error("q must be [..., H, D] with tokens before, got ", shape);
+  const int64_t lead = q.dim() - 2;
+  const int Hq = small(shape[lead], "the heads"), D = small(shape[lead + 1], "D");
+  int64_t tokens = 1;
+  for (int64_t i = 0; i < lead; ++i) tokens *= shape[i];
+  const Tensor& turns = tensor(a[2], "turns");
+  if (turns.dim() != 1) value_error("turns must be one row, got ", turns.sizes());
+  const auto* table = static_cast<const unsigned long long*>(
+      dense(turns, "turns", ScalarType::Long, dev, turns.sizes()));
+  const int R = small(2 * turns.numel(), "the rotated columns");
+  const float magnitude = (float)number(a[6]);
+  const int interleaved = truth(a[7]), backward = truth(a[10]);
+  Batch b{1, small(tokens, "the tokens"), nullptr};
+  const int32_t *positions = nullptr, *offsets = nullptr;
+  if (a[3] != Py_None) {
+    if (a[8] != Py_None || a[9] != Py_None)
+      value_error("positions stand for themselves: neither cu_seqlens nor offsets with them");
+    positions = static_cast<const int32_t*>(dense(a[3], "positions", ScalarType::Int, dev, shape.slice(0, lead)));
+  } else {
+    if (q.dim() != 4) value_error("without positions q must be [B, T, H, D], got ", shape);
+    b = batch_of(shape, a[8], dev);
+    offsets = static_cast<const int32_t*>(maybe(a[9], "offsets", ScalarType::Int, dev, {b.n}));
+  }
+  const Rows qr = token_rows(q, "q");
+  Rows kr;
+  int Hk = 0;
+  std::vector<int64_t> kshape(shape.begin(), shape.end());
+  if (a[1] != Py_None) {
+    const Tensor& k = tensor(a[1], "k");
+    if (k.dim() == q.dim()) kshape[lead] = k.size(lead);
+    typed(k, "k", kind.type, dev, kshape);
+    Hk = small(kshape[lead], "the heads of k");
+    if (Hk < 1) value_error("k has no heads: give None");
+    kr = token_rows(k, "k");
+  } else if (a[5] != Py_None) {
+    value_error("k_out needs a k");
+  }
+  // the caller's outputs may be strided, as q and k (in place: q and k themselves)
+  const auto out = [&](PyObject* o, const char* name, IntArrayRef sizes, Rows* r) {
+    if (o == Py_None) {
+      Tensor t = fresh(sizes, kind.type, dev);
+      *r = token_rows(t, name);
+      return wrap(std::move(t));
+    }
+    typed(tensor(o, name), name, kind.type, dev, sizes);
+    *r = token_rows(tensor(o, name), name);
+    Py_INCREF(o);
+    return o;
+  };
+  Rows qo, ko;
+  Held hq(out(a[4], "q_out", shape, &qo));
+  Held hk(Hk ? out(a[5], "k_out", kshape, &ko) : none());
+  run(dev, [&](gdn_stream_t s) {
+    return lib.rotary[backward][kind.f32](qr.p, kr.p, table, positions, offsets, b.cu, const_cast<void*>(qo.p),
+                                          const_cast<void*>(ko.p), b.n, b.t, Hq, Hk, D, R, qr.stride, kr.stride,
+                                          qo.stride, ko.stride, interleaved, magnitude, s);
+  });
+  return tuple_of({&hq, &hk});
+}
+
 // ---- the module ----------------------------------------------------------------------------
 // Positional arguments only: layer.py has the signatures.
 template <PyObject* (*kCall)(PyObject* const*), int kArgs>
@@ -486,6 +734,12 @@ PyMethodDef methods[] = {{"init", init, METH_VARARGS, nullptr},
                          ENTRY("s6_fwd", s6_fwd, 15),
                          ENTRY("s6_step", s6_step, 11),
                          ENTRY("norm_fwd", norm_fwd, 10),
+                         ENTRY("glr_fwd", glr_fwd, 12),
+                         ENTRY("glr_step", glr_step, 7),
+                         ENTRY("glr_bwd", glr_bwd, 15),
+                         ENTRY("ln_fwd", ln_fwd, 7),
+                         ENTRY("ln_bwd", ln_bwd, 10),
+                         ENTRY("rotary", rotary, 11),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_native", nullptr, -1, methods};
 

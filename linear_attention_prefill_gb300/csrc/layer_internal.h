@@ -1,5 +1,6 @@
 // layer_internal.h - launch parameters of the layer operators (short convolution, S6 scan,
-// RMS norm), shared by their C ABI layer (layer_abi.cu) and the kernels.
+// RMS norm, gated linear recurrence, layer norm, rotary positions), shared by their C ABI layer
+// (layer_abi.cu, glr_abi.cu, layer_norm_abi.cu, rotary_abi.cu) and the kernels.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -84,5 +85,70 @@ struct NormParams {
 };
 constexpr int kNormMaxD = 32768;
 cudaError_t launch_norm(const NormParams& p, bool f32, bool fp8, cudaStream_t stream);
+
+// Gated linear recurrence: prompt, its gradient, or one token (h0 == hT, T = 1).
+enum { GLR_LOG = 0, GLR_SIGMOID = 1, GLR_RATE = 2 };    // as GDN_GLR_GATE_*
+enum { GLR_NONE = 0, GLR_LINEAR = 1, GLR_SQRT = 2 };    // as GDN_GLR_INPUT_*
+constexpr int kGlrSpan = 64, kGlrWarps = 8, kGlrMaxCluster = 8;
+struct GlrParams {
+  const void *x, *g, *dy;           // rows of D channels; dy: gradient only
+  const float *rate;                // [D], GLR_RATE only
+  const float *h0, *dhT, *kept;     // [N, D] or nullptr; kept: the forward's states, gradient only
+  void *y, *dx, *dg;                // [tokens, D]
+  float *hT, *states, *dh0;         // [N, D], [rows, chunks, D], [N, D]; nullptr for none
+  float *partial;                   // [rows * cluster, D]: sums of the rate's gradient
+  const int32_t* cu;                // [N + 1] or nullptr (N rows of T tokens)
+  long long x_stride, g_stride, dy_stride;  // elements from token to token
+  long long chunks;                 // 64-token chunks of a row, the last one partial
+  int N, T, D;
+  int gate, norm;
+  int vec;                          // channel pairs are aligned in every tensor, D is even
+  int tiles;                        // of 64 channels
+  int warps, cluster;               // warps of a block, blocks of a cluster: successive tokens
+};
+inline long long glr_units(const GlrParams& p) { return (p.cu ? 1ll : p.N) * p.tiles; }
+inline unsigned glr_grid(const GlrParams& p) { return (unsigned)(glr_units(p) * p.cluster); }
+cudaError_t launch_glr(const GlrParams& p, bool f32, cudaStream_t stream);
+cudaError_t launch_glr_bwd(const GlrParams& p, bool f32, cudaStream_t stream);
+cudaError_t launch_glr_step(const GlrParams& p, bool f32, cudaStream_t stream);
+// The sums over the rows of in [rows, D] into a, or of in [rows, 2, D] into a and b; in a fixed order.
+cudaError_t launch_column_sums(const float* in, float* a, float* b, int rows, int D, cudaStream_t stream);
+
+// Layer norm of rows, or its gradient (dy; residual: the gradient added to dx; y: dx).
+struct LnParams {
+  const void *x, *dy, *residual;    // residual: nullptr for none
+  const float *w, *b;               // [D]; nullptr for ones and zeros
+  void *y, *residual_out;
+  float *dw, *db;                   // [D], both or neither
+  float* partial;                   // [blocks, 2, D], with dw: ln_partials(D) of them are enough
+  long long rows, x_stride, dy_stride;
+  int D;
+  int blocks, slice;                // blocks of a row (1, 2 or 4), columns of each
+  int by;                           // columns of an access (8, 4, 2, 1): D is a multiple, all are aligned
+  float eps, inv_d;
+};
+constexpr int kLnMaxD = 32768, kLnMaxThreads = 512, kLnSlice = 16 * kLnMaxThreads;
+inline int ln_partials(int D) { return (D <= 512 ? 8 : 2) * kSms; }
+cudaError_t launch_layer_norm(const LnParams& p, bool f32, cudaStream_t stream);
+cudaError_t launch_layer_norm_bwd(const LnParams& p, bool f32, cudaStream_t stream);
+
+// Rotary positions of q and k (k: nullptr and Hk = 0 for none).
+struct RotaryParams {
+  const void *q, *k;                // tokens of Hq, Hk heads of D columns
+  void *q_out, *k_out;
+  const unsigned long long* turns;  // [R / 2]: 2^64 is a whole turn
+  const int32_t *positions;         // [tokens], or nullptr: counted from a sequence's first token
+  const int32_t *offsets, *cu;      // [N] or nullptr (zeros), [N + 1] or nullptr (N rows of T)
+  long long q_stride, k_stride, q_out_stride, k_out_stride, tokens;  // elements from token to token
+  int N, T, Hq, Hk, D, R;
+  int interleaved, backward;
+  int by;                           // elements of an access (16 bytes at most): they divide R / 2 and D - R, and
+                                    // are aligned everywhere
+  int q_same, k_same;               // the output is the input
+  int block_tokens;                 // set by the launch
+  float magnitude;
+};
+constexpr int kRotaryMaxD = 1024;
+cudaError_t launch_rotary(const RotaryParams& p, bool f32, cudaStream_t stream);
 
 }  // namespace gdn

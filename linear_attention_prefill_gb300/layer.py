@@ -1,11 +1,12 @@
 """Python binding of the layer operators of libgdn.so: the short causal convolution,
-the S6 scan and the RMS norm.
+the S6 scan, the RMS norm, the gated linear recurrence, layer norm and rotary positions.
 
 As in binding.py the functions carry the C ABI's names; the signatures are here, the checks,
 allocations and calls in the extension module that csrc/layer_binding.cpp builds.  Row operands
 may be slices of a wider projection (the last dimension dense, tokens a constant stride apart);
 parameters, states and outputs are contiguous.  As everywhere in the library the outputs carry
-no gradient.  ``stream`` (a torch stream, or a cudaStream_t as a number) runs a call, and makes
+no gradient; the recurrence, layer norm and rotary positions have theirs as calls of their own
+(``_bwd``).  ``stream`` (a torch stream, or a cudaStream_t as a number) runs a call, and makes
 its allocations, on another stream than the current one.
 """
 from __future__ import annotations
@@ -24,7 +25,12 @@ _ENTRY_POINTS = ("gdn_short_conv_fwd", "gdn_short_conv_fwd_f32", "gdn_short_conv
                  "gdn_short_conv_step_f32", "gdn_s6_chunk_fwd", "gdn_s6_chunk_fwd_f32",
                  "gdn_s6_recurrent_step", "gdn_s6_recurrent_step_f32",
                  "gdn_s6_chunk_fwd_workspace_size", "gdn_rms_norm_fwd", "gdn_rms_norm_fwd_f32",
-                 "gdn_rms_norm_fwd_e4m3", "gdn_rms_norm_fwd_e4m3_f32")
+                 "gdn_rms_norm_fwd_e4m3", "gdn_rms_norm_fwd_e4m3_f32",
+                 "gdn_glr_chunk_fwd", "gdn_glr_chunk_fwd_f32", "gdn_glr_recurrent_step",
+                 "gdn_glr_recurrent_step_f32", "gdn_glr_chunk_bwd", "gdn_glr_chunk_bwd_f32",
+                 "gdn_glr_chunk_bwd_workspace_size", "gdn_layer_norm_fwd", "gdn_layer_norm_fwd_f32",
+                 "gdn_layer_norm_bwd", "gdn_layer_norm_bwd_f32", "gdn_layer_norm_bwd_workspace_size",
+                 "gdn_rotary_fwd", "gdn_rotary_fwd_f32", "gdn_rotary_bwd", "gdn_rotary_bwd_f32")
 _native = None
 
 
@@ -162,3 +168,167 @@ def gdn_rms_norm_fwd(x, weight, residual=None, gate=None, y=None, residual_out=N
         raise ValueError(f"group (of the e4m3 output) must be 32, 64, 128 or None, got {group!r}")
     return (_native or _load()).norm_fwd(x, weight, residual, gate, y, residual_out, scales, eps, fp8,
                                          group or 0)
+
+
+_GATES = {"log": 0, "sigmoid": 1, "rate": 2}
+_INPUT_NORMS = {None: 0, "linear": 1, "sqrt": 2}
+
+
+def _glr_form(gate, input_norm):
+    if gate not in _GATES:
+        raise ValueError(f"gate must be 'log', 'sigmoid' or 'rate', got {gate!r}")
+    if input_norm not in _INPUT_NORMS:
+        raise ValueError(f"input_norm must be None, 'linear' or 'sqrt', got {input_norm!r}")
+    return _GATES[gate], _INPUT_NORMS[input_norm]
+
+
+def gdn_glr_chunk_fwd(x, g, rate=None, h0=None, y=None, hT=None, states=None, *, gate: str = "log",
+                      input_norm: Optional[str] = None, cu_seqlens=None, output_final_state=True,
+                      output_states=False, stream=None):
+    """Gated linear recurrence over a prompt; returns (y, hT, states).
+
+    Per channel h_t = a_t h_{t-1} + s_t x_t, y_t = h_t, with the decay a = exp(g) (gate "log", g <= 0),
+    sigmoid(g) ("sigmoid") or exp(rate sigmoid(g)) ("rate"; rate [D] fp32, <= 0), and the input's weight
+    s = 1 (input_norm None), 1 - a ("linear") or sqrt(1 - a^2) ("sqrt").  x, g [B, T, D] (bf16 or
+    fp32, both the same; each may be a slice of a wider projection); h0 [N, D] fp32 or None; hT may be
+    h0 (in place).  With cu_seqlens (int32 [N+1] on the device) the batch is one packed row, B = 1;
+    rows behind cu_seqlens[N] are left as they were.  output_states: ``states`` [B, ceil(T / 64), D]
+    fp32, the state before every 64th token of a row, which gdn_glr_chunk_bwd takes.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_glr_chunk_fwd(x, g, rate, h0, y, hT, states, gate=gate, input_norm=input_norm,
+                                     cu_seqlens=cu_seqlens, output_final_state=output_final_state,
+                                     output_states=output_states)
+    return (_native or _load()).glr_fwd(x, g, rate, h0, y, hT, states, *_glr_form(gate, input_norm), cu_seqlens,
+                                        output_final_state, output_states)
+
+
+def gdn_glr_recurrent_step(x, g, h, rate=None, y=None, *, gate: str = "log", input_norm: Optional[str] = None,
+                           stream=None):
+    """One token of the gated linear recurrence; updates h [N, D] in place and returns y.
+
+    x, g [N, D]; the rest as in gdn_glr_chunk_fwd.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_glr_recurrent_step(x, g, h, rate, y, gate=gate, input_norm=input_norm)
+    return (_native or _load()).glr_step(x, g, h, rate, y, *_glr_form(gate, input_norm))
+
+
+def gdn_glr_chunk_bwd_workspace_size(N, T, D, gate="log", varlen=False) -> int:
+    """Bytes of workspace the gated recurrence's gradient needs (0: none, or rejected sizes)."""
+    return int(load_library().gdn_glr_chunk_bwd_workspace_size(N, T, D, _glr_form(gate, None)[0], int(bool(varlen))))
+
+
+def gdn_glr_chunk_bwd(dy, x, g, states, rate=None, h0=None, dhT=None, dx=None, dg=None, drate=None, dh0=None, *,
+                      gate: str = "log", input_norm: Optional[str] = None, cu_seqlens=None, stream=None,
+                      workspace=None):
+    """Gradient of the gated linear recurrence; returns (dx, dg, drate, dh0).
+
+    dy [B, T, D] (x's type, may be a slice) and dhT [N, D] fp32 (or None for zeros) are the gradients of
+    y and hT; ``states`` is the forward's, the other inputs and the form are the same as there.
+    drate [D] fp32 is None without a rate, dh0 [N, D] fp32 None without h0 (unless given).
+    ``workspace``: a uint8 device tensor of at least gdn_glr_chunk_bwd_workspace_size bytes, or None for
+    a fresh one where one is needed.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_glr_chunk_bwd(dy, x, g, states, rate, h0, dhT, dx, dg, drate, dh0, gate=gate,
+                                     input_norm=input_norm, cu_seqlens=cu_seqlens, workspace=workspace)
+    return (_native or _load()).glr_bwd(dy, x, g, states, rate, h0, dhT, dx, dg, drate, dh0,
+                                        *_glr_form(gate, input_norm), cu_seqlens, workspace)
+
+
+def gdn_layer_norm_fwd(x, weight=None, bias=None, residual=None, y=None, residual_out=None, *, eps: float = 1e-5,
+                       stream=None):
+    """Layer norm of the rows of x [..., D]; returns (y, residual_out).
+
+    r = x + residual; y = (r - mean(r)) / sqrt(var(r) + eps) * weight + bias (the variance over D).  x
+    and residual are bf16 or fp32, both the same; weight and bias [D] fp32 or None.  x may be a slice
+    (rows a constant stride apart); residual is contiguous and residual_out (a fresh tensor, or residual
+    itself: in place) takes r in x's type, None without a residual.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_layer_norm_fwd(x, weight, bias, residual, y, residual_out, eps=eps)
+    return (_native or _load()).ln_fwd(x, weight, bias, residual, y, residual_out, eps)
+
+
+def gdn_layer_norm_bwd_workspace_size(rows, D) -> int:
+    """Bytes of workspace the gradient of weight and bias needs (0: rejected sizes)."""
+    return int(load_library().gdn_layer_norm_bwd_workspace_size(rows, D))
+
+
+def gdn_layer_norm_bwd(dy, x, weight=None, dres=None, dx=None, dweight=None, dbias=None, *, eps: float = 1e-5,
+                       param_grads: bool = True, stream=None, workspace=None):
+    """Gradient of layer norm; returns (dx, dweight, dbias).
+
+    dy and x [..., D] (each may be a slice); x is what was normed: with a residual the forward's
+    residual_out, whose own gradient ``dres`` (contiguous, or None) is added to dx (which may be dres: in
+    place); dx is then the gradient of x and residual alike.  dweight and dbias [D] fp32, or None without
+    param_grads.  ``workspace``: a uint8 device tensor of at least gdn_layer_norm_bwd_workspace_size
+    bytes, or None for a fresh one.
+    """
+    if stream is not None:
+        with _on(stream, x):
+            return gdn_layer_norm_bwd(dy, x, weight, dres, dx, dweight, dbias, eps=eps, param_grads=param_grads,
+                                      workspace=workspace)
+    return (_native or _load()).ln_bwd(dy, x, weight, dres, dx, dweight, dbias, eps, param_grads, workspace)
+
+
+_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def gdn_rotary_turns(dim: int, base: float = 10000.0, *, scaling: Optional[str] = None, factor: float = 1.0,
+                     original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """The table of gdn_rotary_fwd for ``dim`` rotated columns; returns (turns, magnitude).
+
+    turns [dim / 2] (int64 on ``device``): pair i turns by base^(-2 i / dim) radians a position, kept as
+    2^64ths of a turn; magnitude scales the rotated columns.  For contexts ``factor`` times as long:
+    scaling "linear" divides the frequencies by it, "ntk" raises the base, "yarn" divides those that
+    make few turns within ``original_length`` (below beta_slow) and keeps those that make many (above
+    beta_fast), with a magnitude of 0.1 ln(factor) + 1.
+    """
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if not 0 < dim <= 1 << 20:
+        raise ValueError(f"dim = {dim} is out of range")
+    table = torch.empty(max(dim // 2, 1), dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    s = load_library().gdn_rotary_turns(dim, base, _SCALINGS[scaling], factor, original_length, beta_fast, beta_slow,
+                                        table.data_ptr(), ctypes.addressof(magnitude))
+    if s != 0:
+        _check(s)
+    return table.to(device), magnitude.value
+
+
+def gdn_rotary_fwd(q, k, turns, positions=None, q_out=None, k_out=None, *, magnitude: float = 1.0,
+                   interleaved: bool = False, cu_seqlens=None, offsets=None, stream=None):
+    """Rotary positions of q [..., Hq, D] and k [..., Hk, D] (or None); returns (q_out, k_out).
+
+    The first 2 len(turns) columns of every head are turned in pairs (i, i + R/2), or (2i, 2i + 1) with
+    ``interleaved``, by position times ``turns`` (gdn_rotary_turns), and scaled by ``magnitude``; the
+    others are passed through.  q and k are bf16 or fp32, both the same; each may be a slice of a
+    projection whose tokens are a constant stride apart, and its own output (in place).  positions: int32,
+    q's shape without [H, D].  Without them q is [B, T, H, D] and a token's position is counted from
+    its sequence's first (cu_seqlens: one packed row, B = 1; rows behind the last sequence are left as
+    they were), plus offsets [N] int32 (or None).
+    """
+    if stream is not None:
+        with _on(stream, q):
+            return gdn_rotary_fwd(q, k, turns, positions, q_out, k_out, magnitude=magnitude,
+                                  interleaved=interleaved, cu_seqlens=cu_seqlens, offsets=offsets)
+    return (_native or _load()).rotary(q, k, turns, positions, q_out, k_out, magnitude, interleaved, cu_seqlens,
+                                       offsets, False)
+
+
+def gdn_rotary_bwd(dq, dk, turns, positions=None, dq_out=None, dk_out=None, *, magnitude: float = 1.0,
+                   interleaved: bool = False, cu_seqlens=None, offsets=None, stream=None):
+    """Gradient of gdn_rotary_fwd: from those of q_out and k_out to those of q and k; arguments as there."""
+    if stream is not None:
+        with _on(stream, dq):
+            return gdn_rotary_bwd(dq, dk, turns, positions, dq_out, dk_out, magnitude=magnitude,
+                                  interleaved=interleaved, cu_seqlens=cu_seqlens, offsets=offsets)
+    return (_native or _load()).rotary(dq, dk, turns, positions, dq_out, dk_out, magnitude, interleaved, cu_seqlens,
+                                       offsets, True)
