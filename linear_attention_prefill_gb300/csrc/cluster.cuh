@@ -1,8 +1,7 @@
 // cluster.cuh - thread-block clusters: barriers, stores into a neighbour's shared memory, launches.
 #pragma once
 
-#include <cuda_runtime.h>
-#include <stdint.h>
+#include "gdn_common.cuh"
 
 namespace gdn {
 
@@ -33,14 +32,56 @@ __device__ __forceinline__ void store_to_rank(void* local, unsigned rank, unsign
   asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(there), "l"(a), "l"(b) : "memory");
 }
 
-// A launch in clusters of `blocks` (1: none) neighbouring blocks.
+// The same, counted as 16 bytes by the barrier `bar` of that block: the receiver waits for its barrier,
+// and nothing of the sender's other accesses is waited for, as a cluster's barrier does.
+__device__ __forceinline__ void send_to_rank(void* local, uint64_t* bar, unsigned rank, unsigned long long a,
+                                             unsigned long long b) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+  const uint32_t of = static_cast<uint32_t>(__cvta_generic_to_shared(bar));
+  uint32_t there, its;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(its) : "r"(of), "r"(rank));
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(there),
+               "l"(a), "l"(b), "r"(its)
+               : "memory");
+}
+// Wait for phase `parity` of `bar`, whose bytes come from the cluster; gives up after about a second and
+// records that, and from then on (`dead`) no wait of the block lasts.
+__device__ __forceinline__ void wait_for_ranks(uint64_t* bar, unsigned parity, unsigned* err, volatile int* dead) {
+  const auto done = [&] {
+    unsigned ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar))), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return;
+  const long long t0 = clock64();
+  while (!done()) {
+    if (*dead || clock64() - t0 > (1ll << 31)) {
+      if (!*dead) record_error(err, kErrWaitTimeout);
+      *dead = 1;
+      return;
+    }
+  }
+}
+
+// A launch in clusters of `blocks` (1: none) neighbouring blocks, with `smem` bytes of dynamic memory.
 template <typename Kernel, typename Params>
 cudaError_t launch_clusters(Kernel kernel, unsigned grid, unsigned threads, unsigned blocks, const Params& p,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, size_t smem = 0) {
+  if (smem) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = blocks;

@@ -67,6 +67,17 @@ int pairs(const GlrParams& p, long long tokens, int elem, std::initializer_list<
   for (const void* q : floats) ok = ok && aligned(q, 8);
   return ok;
 }
+// The widest pieces that rows of x and g (and dy) can be copied in.
+int piece_of(const GlrParams& p, long long tokens, int elem, std::initializer_list<const void*> rows) {
+  for (const int piece : {16, 4}) {
+    const int n = piece / elem;
+    bool ok = p.D % n == 0 &&
+              (tokens <= 1 || (p.x_stride % n == 0 && p.g_stride % n == 0 && p.dy_stride % n == 0));
+    for (const void* q : rows) ok = ok && aligned(q, piece);
+    if (ok) return piece;
+  }
+  return 2;
+}
 
 gdn_status forward(const void* x, const void* g, const float* rate, const float* h0, void* y, float* hT,
                    float* states, int N, int T, int D, long long x_stride, long long g_stride, int gate, int norm,
@@ -93,6 +104,7 @@ gdn_status forward(const void* x, const void* g, const float* rate, const float*
   if (N == 0 || (tokens == 0 && !hT)) return GDN_OK;
   p.h0 = h0; p.y = y; p.hT = hT; p.states = states;
   p.vec = pairs(p, tokens, elem, {x, g, y}, {rate, h0, hT, states});
+  p.piece = piece_of(p, tokens, elem, {x, g});
   const cudaError_t e = gdn::launch_glr(p, f32, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the gated recurrence");
 }
@@ -160,6 +172,7 @@ gdn_status backward(const void* dy, const void* x, const void* g, const float* r
   }
   p.dy = dy; p.dy_stride = dy_stride; p.h0 = h0; p.kept = states; p.dhT = dhT; p.dx = dx; p.dg = dg; p.dh0 = dh0;
   p.vec = pairs(p, tokens, elem, {x, g, dy, dx, dg}, {rate, h0, states, dhT, dh0});
+  p.piece = piece_of(p, tokens, elem, {x, g, dy});
   const size_t need = partial_bytes(p);
   void* pool = nullptr;
   if (need) {

@@ -1,0 +1,261 @@
+// glr_bwd.cuh - the gradient of the gated linear recurrence over a prompt.
+//
+// With lambda_t the gradient that reaches h_t and m_t = a_t lambda_t what it passes on:
+//
+//   lambda_t = dy_t + m_{t+1} (a sequence's last token: dhT),   dx_t = s_t lambda_t,
+//   dL_t = lambda_t (a_t h_{t-1} + (ds/dL) x_t),   ds/dL = 0, -a or -a^2 / s,
+//   dg_t = dL_t (log), dL_t (1 - a_t) (sigmoid), dL_t rate sig (1 - sig) (rate),
+//   drate = sum of dL_t sig,   dh0 = m of the sequence's first token.
+//
+// One pass from the last tokens to the first, laid out as the forward is (glr_fwd.cuh): m runs
+// backwards over the same stretches, m_t = a_t (dy_t + m_{t+1}), and is exchanged the same way.
+// h_{t-1} comes forwards again from the fp32 state that the forward left before the block's 64 tokens,
+// so that no rounded y enters the gates' gradient and y itself is not read.  x, g and dy are
+// read once, dx and dg written once: HBM bandwidth bounds it.  Where s = 0 (a = 1 exactly) the weight
+// has no derivative; its share is left out.
+//
+// drate is summed by threads over their tokens, then over warps, blocks and rows in a fixed order.
+#pragma once
+
+#include "glr_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kStages = 3;
+
+// lambda of a sequence's last token without what comes from behind: dy + dhT
+__device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end, int t, long long c, bool c0,
+                                           bool c1) {
+  if (!p.dhT) return dy;
+  return add2(dy, load_f32(p.dhT + (long long)sequence_of(p.cu, p.N, end, t) * p.D + c, p.vec, c0, c1));
+}
+
+template <typename T, int kGate, int kNorm, bool kPacked>
+__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bwd_kernel(const GlrParams p) {
+  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][64 tokens][64 channels]
+  __shared__ ulonglong2 s_ahead[2][kGlrWarps][32], s_back[2][kGlrWarps][32];
+  __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
+  __shared__ uint64_t s_bar[2];
+  __shared__ int s_dead;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const unsigned K = p.cluster, rank = K > 1 ? cluster_rank() : 0;
+  if (K > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(&s_bar[0], 1);
+      mbar_init(&s_bar[1], 1);
+      mbar_fence_init();
+      s_dead = 0;
+    }
+    __syncwarp();
+    cluster_arrive();
+  }
+  const unsigned unit = blockIdx.x / K;
+  const long long row = unit / p.tiles;
+  const int tile = (int)(unit - (unsigned)row * p.tiles);
+  const bool vec = p.vec;
+  const long long c = (long long)tile * 64 + 2 * lane;
+  const bool c0 = c < p.D, c1 = c + 1 < p.D;
+  const unsigned end = kPacked ? min(max(p.cu[p.N], 0), p.T) : p.T;
+  const unsigned span = warps * kGlrRun, round = K * span;
+  const unsigned rounds = end ? (end - 1) / round + 1 : 0;
+  const f32x2 rate = kGate == GLR_RATE ? load_f32(p.rate + c, vec, c0, c1) : 0ull;
+  f32x2 carry = !kPacked && p.dhT ? load_f32(p.dhT + row * p.D + c, vec, c0, c1) : 0ull;
+  f32x2 drate = 0ull;
+
+  T* tiles = reinterpret_cast<T*>(s_tiles);
+  const int cols = (int)min(64ll, p.D - (long long)tile * 64);
+  const auto fetch = [&](unsigned r) {  // round r, counted from the last tokens, into its stage
+    if (r < rounds) {
+      const unsigned first = (rounds - 1 - r) * round + rank * span;
+      const long long at = row * p.T + first;
+      T* to = tiles + r % kStages * (3 * 64 * 64);
+      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, first, end, span, cols,
+                p.piece);
+      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, first, end,
+                span, cols, p.piece);
+      copy_tile(to + 2 * 64 * 64, static_cast<const T*>(p.dy) + at * p.dy_stride + tile * 64ll, p.dy_stride, first,
+                end, span, cols, p.piece);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int r = 0; r < kStages - 1; ++r) fetch(r);
+  unsigned t = (rounds - 1) * round + rank * span + warp * kGlrRun;  // this thread's first token
+  // the state before the block's tokens, of this round and the next
+  const auto state_before = [&](unsigned first) {
+    return first < end ? load_f32(p.kept + (row * p.chunks + first / kGlrSpan) * p.D + c, vec, c0, c1) : 0ull;
+  };
+  f32x2 before = rounds ? state_before(t - warp * kGlrRun) : 0ull;
+  if (K > 1) cluster_wait();
+  for (unsigned r = 0; r < rounds; ++r, t -= round) {
+    const int turn = r & 1;
+    if (K > 1 && threadIdx.x == 0) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
+    cp_async_wait<kStages - 2>();
+    __syncthreads();
+    fetch(r + kStages - 1);
+    const T* xs = tiles + r % kStages * (3 * 64 * 64) + warp * kGlrRun * 64;
+    const T *gs = xs + 64 * 64, *ds = gs + 64 * 64;
+    const int n = t < end ? (int)min(end - t, (unsigned)kGlrRun) : 0;  // tokens that exist
+    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t) : 0u;
+    f32x2 h = before;
+    if (r + 1 < rounds) before = state_before(t - warp * kGlrRun - round);
+    f32x2 a[kGlrRun], s[kGlrRun];
+    f32x2 A = dup2(1.f), H = 0ull;
+    bool cut = false;
+#pragma unroll
+    for (int i = 0; i < kGlrRun; ++i) {
+      gate2<kGate, kNorm>(pair_at(gs, i, lane), rate, a[i], s[i]);
+      const f32x2 x = pair_at(xs, i, lane), b = kNorm == GLR_NONE ? x : mul2(s[i], x);
+      if (kPacked && borders >> i & 1) {
+        f32x2 first = 0ull;
+        if (p.h0 && i < n)
+          first = load_f32(p.h0 + (long long)sequence_of(p.cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
+        H = fma2(a[i], first, b);
+        cut = true;
+      } else {
+        H = fma2(a[i], H, b);
+        A = mul2(A, a[i]);
+      }
+    }
+    s_ahead[turn][warp][lane] = make_ulonglong2(kPacked && cut ? 0ull : at_least_tiny(A), H);
+    // backwards: m before these tokens from m behind them; tokens that do not exist pass it on
+    A = dup2(1.f);
+    f32x2 M = 0ull;
+    cut = false;
+#pragma unroll
+    for (int i = kGlrRun - 1; i >= 0; --i) {
+      const f32x2 dy = pair_at(ds, i, lane);
+      if (i >= n) {
+        a[i] = dup2(1.f);
+      } else if (kPacked && borders >> (i + 1) & 1) {
+        M = mul2(a[i], with_last(p, dy, (int)end, (int)t + i, c, c0, c1));
+        cut = true;
+        continue;
+      }
+      M = mul2(a[i], add2(dy, M));
+      A = mul2(A, a[i]);
+    }
+    A = kPacked && cut ? 0ull : at_least_tiny(A);
+    s_back[turn][warp][lane] = make_ulonglong2(A, M);
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+      const ulonglong2 v = s_ahead[turn][w][lane];
+      h = through<kPacked>(v.x, v.y, h);
+    }
+    f32x2 sA = dup2(1.f), sM = 0ull;
+#pragma unroll 4
+    for (int w = warps - 1; w >= 0; --w) {
+      if (w == warp) A = sA, M = sM;
+      const ulonglong2 v = s_back[turn][w][lane];
+      follow<kPacked>(sA, sM, v.x, v.y);
+    }
+    f32x2 m = carry;
+    if (K > 1) {
+      if (warp < (int)K) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], warp, sA, sM);
+      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, &s_dead);
+      f32x2 now = carry;
+      for (int k = (int)K - 1; k >= 0; --k) {
+        if (k == (int)rank) m = now;
+        const ulonglong2 v = s_rank[turn][k][lane];
+        now = through<kPacked>(v.x, v.y, now);
+      }
+      carry = now;
+    } else {
+      carry = through<kPacked>(sA, sM, carry);
+    }
+    m = through<kPacked>(A, M, m);
+    f32x2 hp[kGlrRun];  // the state before each token
+#pragma unroll
+    for (int i = 0; i < kGlrRun; ++i) {
+      if (kPacked && borders >> i & 1) {
+        h = 0ull;
+        if (p.h0 && i < n)
+          h = load_f32(p.h0 + (long long)sequence_of(p.cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
+      }
+      hp[i] = h;
+      const f32x2 x = pair_at(xs, i, lane);
+      h = fma2(a[i], h, kNorm == GLR_NONE ? x : mul2(s[i], x));
+    }
+    T* dx = static_cast<T*>(p.dx) + (row * p.T + t) * p.D + c;
+    T* dg = static_cast<T*>(p.dg) + (row * p.T + t) * p.D + c;
+#pragma unroll
+    for (int i = kGlrRun - 1; i >= 0; --i) {
+      if (i >= n) continue;
+      const f32x2 x = pair_at(xs, i, lane), dy = pair_at(ds, i, lane);
+      const f32x2 lam = kPacked && borders >> (i + 1) & 1 ? with_last(p, dy, (int)end, (int)t + i, c, c0, c1)
+                                                          : add2(dy, m);
+      Raw2<T> o;
+      o.set(kNorm == GLR_NONE ? lam : mul2(s[i], lam));
+      o.store(dx + i * (long long)p.D, vec, c0, c1);
+      // dL / (a lambda): h_{t-1} and the weight's share
+      f32x2 slope = hp[i];
+      if (kNorm == GLR_LINEAR) slope = add2(slope, neg2(x));
+      if (kNorm == GLR_SQRT) {
+        const f32x2 inv = each(s[i], [](float v) { return v > 0.f ? rcp(v) : 0.f; });
+        slope = fma2(neg2(mul2(a[i], inv)), x, slope);
+      }
+      m = mul2(a[i], lam);
+      f32x2 d = mul2(m, slope);
+      if (kGate == GLR_SIGMOID) {
+        d = mul2(d, kNorm == GLR_LINEAR ? s[i] : mul2(exp_neg(pair_at(gs, i, lane)), a[i]));
+      } else if (kGate == GLR_RATE) {
+        const f32x2 e = exp_neg(pair_at(gs, i, lane)), sig = rcp2(add2(e, dup2(1.f)));
+        d = mul2(d, sig);
+        drate = add2(drate, d);
+        d = mul2(mul2(d, rate), mul2(e, sig));
+      }
+      o.set(d);
+      o.store(dg + i * (long long)p.D, vec, c0, c1);
+      if (kPacked ? borders >> i & 1 : t + i == 0) {
+        if (p.dh0) {
+          const long long q = kPacked ? sequence_of(p.cu, p.N, (int)end, (int)t + i) : row;
+          store_f32(p.dh0 + q * p.D + c, m, vec, c0, c1);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  if (K > 1) cluster_sync();  // no block leaves before its neighbours have sent what they send
+  if (kGate == GLR_RATE) {  // the block's sum, its warps in order
+    __syncthreads();
+    f32x2* sum = reinterpret_cast<f32x2*>(&s_ahead[0][0][0]);
+    sum[warp * 32 + lane] = drate;
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < warps; ++w) drate = add2(drate, sum[w * 32 + lane]);
+      store_f32(p.partial + (row * K + rank) * p.D + c, drate, vec, c0, c1);
+    }
+  }
+  if (!p.dh0) return;
+  if (!kPacked) {
+    if (rounds == 0 && rank == 0 && warp == 0) store_f32(p.dh0 + row * p.D + c, carry, vec, c0, c1);
+    return;
+  }
+  for (long long q = rank * warps + warp; q < p.N; q += K * warps) {  // sequences without tokens
+    if (min(max(p.cu[q + 1], 0), (int)end) > min(max(p.cu[q], 0), (int)end)) continue;
+    const f32x2 d = p.dhT ? load_f32(p.dhT + q * p.D + c, vec, c0, c1) : 0ull;
+    store_f32(p.dh0 + q * p.D + c, d, vec, c0, c1);
+  }
+}
+
+template <typename T, int kGate, int kNorm>
+cudaError_t launch(const GlrParams& p, cudaStream_t stream) {
+  const auto kernel = p.cu ? glr_bwd_kernel<T, kGate, kNorm, true> : glr_bwd_kernel<T, kGate, kNorm, false>;
+  return launch_clusters(kernel, glr_grid(p), 32 * p.warps, p.cluster, p, stream, kStages * 3 * 64 * 64 * sizeof(T));
+}
+template <typename T, int kGate>
+cudaError_t launch_gate(const GlrParams& p, cudaStream_t stream) {
+  return p.norm == GLR_NONE     ? launch<T, kGate, GLR_NONE>(p, stream)
+         : p.norm == GLR_LINEAR ? launch<T, kGate, GLR_LINEAR>(p, stream)
+                                : launch<T, kGate, GLR_SQRT>(p, stream);
+}
+template <typename T>
+cudaError_t launch_type(const GlrParams& p, cudaStream_t stream) {
+  return p.gate == GLR_LOG       ? launch_gate<T, GLR_LOG>(p, stream)
+         : p.gate == GLR_SIGMOID ? launch_gate<T, GLR_SIGMOID>(p, stream)
+                                 : launch_gate<T, GLR_RATE>(p, stream);
+}
+
+}  // namespace
+}  // namespace gdn

@@ -20,8 +20,7 @@ constexpr int kGlrRun = kGlrSpan / kGlrWarps;  // tokens of a thread in a round
 constexpr float kTiny = 1.17549435e-38f;       // 2^-126
 
 // ---- two channels of a row ---------------------------------------------------------------
-// Aligned rows: channels 2 lane, 2 lane + 1 of the 64 in one access; others: channels lane and
-// lane + 32 in an access each (so that a warp's accesses are dense).
+// Channels 2 lane, 2 lane + 1 of a warp's 64: in one access where rows are aligned to pairs (vec).
 template <typename T>
 struct Raw2;
 template <>
@@ -32,7 +31,7 @@ struct Raw2<__nv_bfloat16> {
       v = c0 ? *reinterpret_cast<const uint32_t*>(p) : 0u;
     } else {
       const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-      v = (c0 ? (uint32_t)q[0] : 0u) | (c1 ? (uint32_t)q[32] << 16 : 0u);
+      v = (c0 ? (uint32_t)q[0] : 0u) | (c1 ? (uint32_t)q[1] << 16 : 0u);
     }
   }
   __device__ __forceinline__ void store(__nv_bfloat16* p, bool vec, bool c0, bool c1) const {
@@ -41,7 +40,7 @@ struct Raw2<__nv_bfloat16> {
     } else {
       uint16_t* q = reinterpret_cast<uint16_t*>(p);
       if (c0) q[0] = (uint16_t)v;
-      if (c1) q[32] = (uint16_t)(v >> 16);
+      if (c1) q[1] = (uint16_t)(v >> 16);
     }
   }
   __device__ __forceinline__ f32x2 get() const {
@@ -54,14 +53,13 @@ struct Raw2<__nv_bfloat16> {
     unpack2(x, a, b);
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(b), "f"(a));
   }
-  __device__ __forceinline__ void zero() { v = 0u; }
 };
 template <>
 struct Raw2<float> {
   f32x2 v;
   __device__ __forceinline__ void load(const float* p, bool vec, bool c0, bool c1) {
     if (vec) v = c0 ? *reinterpret_cast<const f32x2*>(p) : 0ull;
-    else v = pack2(c0 ? p[0] : 0.f, c1 ? p[32] : 0.f);
+    else v = pack2(c0 ? p[0] : 0.f, c1 ? p[1] : 0.f);
   }
   __device__ __forceinline__ void store(float* p, bool vec, bool c0, bool c1) const {
     if (vec) {
@@ -70,12 +68,11 @@ struct Raw2<float> {
       float a, b;
       unpack2(v, a, b);
       if (c0) p[0] = a;
-      if (c1) p[32] = b;
+      if (c1) p[1] = b;
     }
   }
   __device__ __forceinline__ f32x2 get() const { return v; }
   __device__ __forceinline__ void set(f32x2 x) { v = x; }
-  __device__ __forceinline__ void zero() { v = 0ull; }
 };
 __device__ __forceinline__ f32x2 load_f32(const float* p, bool vec, bool c0, bool c1) {
   Raw2<float> r;
@@ -86,6 +83,52 @@ __device__ __forceinline__ void store_f32(float* p, f32x2 x, bool vec, bool c0, 
   Raw2<float> r;
   r.v = x;
   r.store(p, vec, c0, c1);
+}
+// A tile's pair in shared memory, tokens of 64 channels.
+template <typename T>
+__device__ __forceinline__ f32x2 pair_at(const T* tile, int token, int lane) {
+  Raw2<T> r;
+  r.load(tile + token * 64 + 2 * lane, true, true, true);
+  return r.get();
+}
+
+// ---- tiles on their way into shared memory ---------------------------------------------------
+// Bytes of an access: 16 and 4 are asynchronous copies, 2 plain loads (odd rows of bf16).
+template <int kBytes>
+__device__ __forceinline__ void copy_piece(void* to, const void* from, bool ok) {
+  if constexpr (kBytes == 16) {
+    cp_async16(to, from, ok);
+  } else if constexpr (kBytes == 4) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(ok ? 4 : 0)
+                 : "memory");
+  } else {
+    *static_cast<uint16_t*>(to) = ok ? *static_cast<const uint16_t*>(from) : (uint16_t)0;
+  }
+}
+template <int kBytes, typename T>
+__device__ __forceinline__ void copy_rows(T* tile, const T* src, long long stride, unsigned first, unsigned end,
+                                          int tokens, int cols) {
+  constexpr int kCols = kBytes / (int)sizeof(T), kPieces = 64 / kCols;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < tokens * kPieces; i += blockDim.x) {
+    const int row = i / kPieces, col = i % kPieces * kCols;
+    const bool ok = col < cols && first + row < end;
+    copy_piece<kBytes>(tile + row * 64 + col, ok ? src + row * stride + col : src, ok);
+  }
+}
+// `tokens` rows of 64 channels from src (token `first` of a row; `cols` channels exist), zeros for what
+// is behind `end` or does not exist, by all threads of the block; rows are made of, and aligned to, pieces
+// of so many bytes.
+template <typename T>
+__device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, unsigned first, unsigned end,
+                                          int tokens, int cols, int piece) {
+  if (piece == 16) {
+    copy_rows<16>(tile, src, stride, first, end, tokens, cols);
+  } else if (sizeof(T) == 4 || piece == 4) {
+    copy_rows<4>(tile, src, stride, first, end, tokens, cols);
+  } else if constexpr (sizeof(T) == 2) {
+    copy_rows<2>(tile, src, stride, first, end, tokens, cols);
+  }
 }
 
 // ---- gates -------------------------------------------------------------------------------
@@ -119,14 +162,6 @@ __device__ __forceinline__ f32x2 expm1_small(f32x2 u) {
   r = fma2(r, u, dup2(1.f));
   return mul2(r, u);
 }
-// 1 - e^u where e = e^u is known: the difference loses what small |u| have, the series does not.
-__device__ __forceinline__ f32x2 one_less(f32x2 u, f32x2 e) {
-  float s0, s1, u0, u1, d0, d1;
-  unpack2(neg2(expm1_small(u)), s0, s1);
-  unpack2(u, u0, u1);
-  unpack2(add2(dup2(1.f), neg2(e)), d0, d1);
-  return pack2(fabsf(u0) < 0.5f ? s0 : d0, fabsf(u1) < 0.5f ? s1 : d1);
-}
 // e^-g, at most 2^126 so that its product with sigmoid(g) = 1 / (1 + e^-g) is 1 - sigmoid(g)
 // for every g
 __device__ __forceinline__ f32x2 exp_neg(f32x2 g) {
@@ -136,23 +171,35 @@ __device__ __forceinline__ f32x2 rcp2(f32x2 x) {
   return each(x, [](float v) { return rcp(v); });
 }
 
-// The decay a and the input's weight s of a token.
+// small where |u| < 1/2, else large
+__device__ __forceinline__ f32x2 by_size(f32x2 u, f32x2 small, f32x2 large) {
+  float u0, u1, s0, s1, l0, l1;
+  unpack2(u, u0, u1);
+  unpack2(small, s0, s1);
+  unpack2(large, l0, l1);
+  return pack2(fabsf(u0) < 0.5f ? s0 : l0, fabsf(u1) < 0.5f ? s1 : l1);
+}
+
+// The decay a and the input's weight s of a token.  Decays next to 1 come from 1 - a, which keeps its
+// digits there: a then is off by one rounding, not by the error of 2^x, whose like sign over the
+// thousand tokens that such a decay remembers would show in fp32 sums.
 template <int kGate, int kNorm>
 __device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
-  const auto root = [](f32x2 v) { return each(v, [](float x) { return sqrt_ftz(x); }); };
-  s = dup2(1.f);
+  const f32x2 one = dup2(1.f);
+  f32x2 left;  // 1 - a
   if (kGate == GLR_SIGMOID) {
-    const f32x2 e = exp_neg(g);
-    a = rcp2(add2(e, dup2(1.f)));
-    const f32x2 left = mul2(e, a);  // 1 - a
-    if (kNorm == GLR_LINEAR) s = left;
-    if (kNorm == GLR_SQRT) s = root(fma2(left, a, left));
+    const f32x2 e = exp_neg(g), q = rcp2(add2(e, one));
+    left = mul2(e, q);
+    a = by_size(left, add2(one, neg2(left)), q);
   } else {
-    const f32x2 log = kGate == GLR_LOG ? g : mul2(rate, rcp2(add2(exp_neg(g), dup2(1.f))));
-    a = each(mul2(log, dup2(kLog2e)), [](float v) { return ex2(v); });
-    if (kNorm == GLR_LINEAR) s = one_less(log, a);
-    if (kNorm == GLR_SQRT) s = root(one_less(add2(log, log), mul2(a, a)));
+    const f32x2 log = kGate == GLR_LOG ? g : mul2(rate, rcp2(add2(exp_neg(g), one)));
+    const f32x2 e = each(mul2(log, dup2(kLog2e)), [](float v) { return ex2(v); }), small = expm1_small(log);
+    a = by_size(log, add2(one, small), e);
+    if (kNorm != GLR_NONE) left = by_size(log, neg2(small), add2(one, neg2(e)));
   }
+  if (kNorm == GLR_NONE) s = one;
+  if (kNorm == GLR_LINEAR) s = left;
+  if (kNorm == GLR_SQRT) s = each(fma2(left, a, left), [](float v) { return sqrt_ftz(v); });
 }
 
 // ---- stretches of time ---------------------------------------------------------------------
@@ -162,7 +209,9 @@ __device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
 __device__ __forceinline__ f32x2 at_least_tiny(f32x2 a) {
   return each(a, [](float v) { return fmaxf(v, kTiny); });
 }
+template <bool kBorders>
 __device__ __forceinline__ f32x2 through(f32x2 A, f32x2 H, f32x2 h) {  // A h + H
+  if (!kBorders) return fma2(A, h, H);
   float a0, a1, b0, b1, r0, r1;
   unpack2(A, a0, a1);
   unpack2(H, b0, b1);
@@ -170,13 +219,19 @@ __device__ __forceinline__ f32x2 through(f32x2 A, f32x2 H, f32x2 h) {  // A h + 
   return pack2(a0 == 0.f ? b0 : r0, a1 == 0.f ? b1 : r1);
 }
 // (A, H) followed by (B, G)
+template <bool kBorders>
 __device__ __forceinline__ void follow(f32x2& A, f32x2& H, f32x2 B, f32x2 G) {
-  H = through(B, G, H);
-  float a0, a1, b0, b1;
+  H = through<kBorders>(B, G, H);
+  const f32x2 product = at_least_tiny(mul2(A, B));
+  if (!kBorders) {
+    A = product;
+    return;
+  }
+  float a0, a1, b0, b1, p0, p1;
   unpack2(A, a0, a1);
   unpack2(B, b0, b1);
-  A = pack2(a0 == 0.f || b0 == 0.f ? 0.f : fmaxf(a0 * b0, kTiny),
-            a1 == 0.f || b1 == 0.f ? 0.f : fmaxf(a1 * b1, kTiny));
+  unpack2(product, p0, p1);
+  A = pack2(a0 == 0.f || b0 == 0.f ? 0.f : p0, a1 == 0.f || b1 == 0.f ? 0.f : p1);
 }
 
 // ---- sequence borders of a packed row ------------------------------------------------------
@@ -197,12 +252,12 @@ __device__ __forceinline__ int first_border_above(const int32_t* cu, int N, int 
   }
   return (int)lo;
 }
-// The sequence that holds token v.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int N, int end, int v) {
+// The sequence that holds token v.  (Not inlined: the loops over a thread's tokens are unrolled.)
+static __device__ __noinline__ int sequence_of(const int32_t* cu, int N, int end, int v) {
   return min(max(first_border_above(cu, N, end, v) - 1, 0), N - 1);
 }
 // Bit i: a sequence starts at token t + i, or the last one ends before it (i <= kGlrRun).
-__device__ __forceinline__ unsigned borders_of(const int32_t* cu, int N, int end, int t) {
+static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int end, int t) {
   int m = first_border_above(cu, N, end, t);
   unsigned bits = m > 0 && min(max(cu[m - 1], 0), end) == t ? 1u : 0u;
   while (m <= N) {

@@ -103,13 +103,18 @@ struct GlrParams {
   int N, T, D;
   int gate, norm;
   int vec;                          // channel pairs are aligned in every tensor, D is even
+  int piece;                        // rows are made of, and aligned to, 16, 4 or 2 bytes
+  unsigned* err;                    // device error word: bounded waits record a timeout here (set
+                                    // by the launch that has them)
   int tiles;                        // of 64 channels
   int warps, cluster;               // warps of a block, blocks of a cluster: successive tokens
 };
 inline long long glr_units(const GlrParams& p) { return (p.cu ? 1ll : p.N) * p.tiles; }
 inline unsigned glr_grid(const GlrParams& p) { return (unsigned)(glr_units(p) * p.cluster); }
-cudaError_t launch_glr(const GlrParams& p, bool f32, cudaStream_t stream);
-cudaError_t launch_glr_bwd(const GlrParams& p, bool f32, cudaStream_t stream);
+cudaError_t launch_glr_f32(const GlrParams& p, bool step, cudaStream_t stream);
+cudaError_t launch_glr_bwd_f32(const GlrParams& p, cudaStream_t stream);
+cudaError_t launch_glr(GlrParams p, bool f32, cudaStream_t stream);
+cudaError_t launch_glr_bwd(GlrParams p, bool f32, cudaStream_t stream);
 cudaError_t launch_glr_step(const GlrParams& p, bool f32, cudaStream_t stream);
 // The sums over the rows of in [rows, D] into a, or of in [rows, 2, D] into a and b; in a fixed order.
 cudaError_t launch_column_sums(const float* in, float* a, float* b, int rows, int D, cudaStream_t stream);
