@@ -1,4 +1,5 @@
 // glr_abi.cu - the extern "C" boundary of the gated linear recurrence (declared in include/gdn.h).
+#include <stdlib.h>
 #include <initializer_list>
 
 #include "layer_check.h"
@@ -19,16 +20,16 @@ bool known(int gate, int norm) {
          norm <= GDN_GLR_INPUT_SQRT;
 }
 
-// How a prompt is cut: a block's warps take 8 tokens each, 64 together where there are as many, and
-// a cluster's blocks go on in time where the channels and rows alone do not fill the GPU with two
-// blocks an SM.
+// How a prompt is cut: a block's warps take 16 tokens each, 64 together where there are as many, and
+// a cluster's blocks go on in time.
 void plan(GlrParams* p) {
   p->tiles = (p->D - 1) / 64 + 1;
   p->chunks = ((long long)p->T + gdn::kGlrSpan - 1) / gdn::kGlrSpan;
   const int run = gdn::kGlrSpan / gdn::kGlrWarps;
   p->warps = p->T >= gdn::kGlrSpan ? gdn::kGlrWarps : p->T > run ? (p->T - 1) / run + 1 : 1;
   p->cluster = 1;
-  while (p->cluster < gdn::kGlrMaxCluster && gdn::glr_units(*p) * p->cluster < 2 * gdn::kSms &&
+  const long long want = getenv("GLR_WANT") ? atoll(getenv("GLR_WANT")) : 2 * gdn::kSms;
+  while (p->cluster < gdn::kGlrMaxCluster && gdn::glr_units(*p) * p->cluster < want &&
          (long long)p->cluster * gdn::kGlrSpan < p->T)
     p->cluster *= 2;
 }

@@ -22,7 +22,8 @@
 namespace gdn {
 namespace {
 
-constexpr int kStages = 3;
+// Two rounds' tiles: three would leave two blocks an SM instead of three.
+constexpr int kStages = 2;
 
 // lambda of a sequence's last token without what comes from behind: dy + dhT
 __device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end, int t, long long c, bool c0,
@@ -32,13 +33,15 @@ __device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end
 }
 
 template <typename T, int kGate, int kNorm, bool kPacked>
-__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bwd_kernel(const GlrParams p) {
+__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bwd_kernel(const GlrParams p) {
   extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][64 tokens][64 channels]
   __shared__ ulonglong2 s_ahead[2][kGlrWarps][32], s_back[2][kGlrWarps][32];
   __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  volatile int* const dead = &s_dead;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (known to be the warp's)
   const unsigned K = p.cluster, rank = K > 1 ? cluster_rank() : 0;
   if (K > 1) {
     if (threadIdx.x == 0) {
@@ -68,14 +71,13 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bw
   const auto fetch = [&](unsigned r) {  // round r, counted from the last tokens, into its stage
     if (r < rounds) {
       const unsigned first = (rounds - 1 - r) * round + rank * span;
+      const int left = first < end ? (int)min(end - first, 64u) : 0;  // rows that exist
       const long long at = row * p.T + first;
       T* to = tiles + r % kStages * (3 * 64 * 64);
-      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, first, end, span, cols,
-                p.piece);
-      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, first, end,
+      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
+      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
+      copy_tile(to + 2 * 64 * 64, static_cast<const T*>(p.dy) + at * p.dy_stride + tile * 64ll, p.dy_stride, left,
                 span, cols, p.piece);
-      copy_tile(to + 2 * 64 * 64, static_cast<const T*>(p.dy) + at * p.dy_stride + tile * 64ll, p.dy_stride, first,
-                end, span, cols, p.piece);
     }
     cp_async_commit();
   };
@@ -90,7 +92,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bw
   if (K > 1) cluster_wait();
   for (unsigned r = 0; r < rounds; ++r, t -= round) {
     const int turn = r & 1;
-    if (K > 1 && threadIdx.x == 0) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
+    // (a block that has given up a wait neither expects nor sends: its neighbours give up, too)
+    if (K > 1 && threadIdx.x == 0 && !*dead) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
     cp_async_wait<kStages - 2>();
     __syncthreads();
     fetch(r + kStages - 1);
@@ -120,7 +123,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bw
     }
     s_ahead[turn][warp][lane] = make_ulonglong2(kPacked && cut ? 0ull : at_least_tiny(A), H);
     // backwards: m before these tokens from m behind them; tokens that do not exist pass it on
-    A = dup2(1.f);
+    const bool same = !kPacked && n == kGlrRun;  // (then the decays' product is the one forwards)
+    if (!same) A = dup2(1.f);
     f32x2 M = 0ull;
     cut = false;
 #pragma unroll
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bw
         continue;
       }
       M = mul2(a[i], add2(dy, M));
-      A = mul2(A, a[i]);
+      if (!same) A = mul2(A, a[i]);
     }
     A = kPacked && cut ? 0ull : at_least_tiny(A);
     s_back[turn][warp][lane] = make_ulonglong2(A, M);
@@ -152,8 +156,10 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bw
     }
     f32x2 m = carry;
     if (K > 1) {
-      if (warp < (int)K) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], warp, sA, sM);
-      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, &s_dead);
+      if (!*dead) {
+        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], k, sA, sM);
+      }
+      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
       f32x2 now = carry;
       for (int k = (int)K - 1; k >= 0; --k) {
         if (k == (int)rank) m = now;
@@ -198,12 +204,15 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 2 : 1) glr_bw
       m = mul2(a[i], lam);
       f32x2 d = mul2(m, slope);
       if (kGate == GLR_SIGMOID) {
-        d = mul2(d, kNorm == GLR_LINEAR ? s[i] : mul2(exp_neg(pair_at(gs, i, lane)), a[i]));
+        f32x2 sig, rest = s[i];
+        if (kNorm != GLR_LINEAR) sigmoid2(pair_at(gs, i, lane), sig, rest);
+        d = mul2(d, rest);
       } else if (kGate == GLR_RATE) {
-        const f32x2 e = exp_neg(pair_at(gs, i, lane)), sig = rcp2(add2(e, dup2(1.f)));
+        f32x2 sig, rest;
+        sigmoid2(pair_at(gs, i, lane), sig, rest);
         d = mul2(d, sig);
         drate = add2(drate, d);
-        d = mul2(mul2(d, rate), mul2(e, sig));
+        d = mul2(mul2(d, rate), rest);
       }
       o.set(d);
       o.store(dg + i * (long long)p.D, vec, c0, c1);

@@ -105,29 +105,43 @@ __device__ __forceinline__ void copy_piece(void* to, const void* from, bool ok) 
     *static_cast<uint16_t*>(to) = ok ? *static_cast<const uint16_t*>(from) : (uint16_t)0;
   }
 }
+// Up to 64 rows (`tokens`) of 64 channels, `cols` of which exist, from src; zeros for rows from `rows` on
+// and for channels that do not exist.
 template <int kBytes, typename T>
-__device__ __forceinline__ void copy_rows(T* tile, const T* src, long long stride, unsigned first, unsigned end,
-                                          int tokens, int cols) {
+__device__ __forceinline__ void copy_rows(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
   constexpr int kCols = kBytes / (int)sizeof(T), kPieces = 64 / kCols;
+  if (kBytes == 16 && blockDim.x == 128 && rows >= 64) {  // a whole tile, by a whole block
+    constexpr int kStep = 128 / kPieces;
+    const int row = threadIdx.x / kPieces, col = threadIdx.x % kPieces * kCols;
+    const T* from = src + row * stride + col;
+    const bool ok = col < cols;
+    if (!ok) from = src;
+    const long long step = ok ? kStep * stride : 0;
+    tile += row * 64 + col;
+#pragma unroll
+    for (int i = 0; i < 64 / kStep; ++i) {
+      copy_piece<kBytes>(tile + i * kStep * 64, from, ok);
+      from += step;
+    }
+    return;
+  }
 #pragma unroll 4
   for (int i = threadIdx.x; i < tokens * kPieces; i += blockDim.x) {
     const int row = i / kPieces, col = i % kPieces * kCols;
-    const bool ok = col < cols && first + row < end;
+    const bool ok = col < cols && row < rows;
     copy_piece<kBytes>(tile + row * 64 + col, ok ? src + row * stride + col : src, ok);
   }
 }
-// `tokens` rows of 64 channels from src (token `first` of a row; `cols` channels exist), zeros for what
-// is behind `end` or does not exist, by all threads of the block; rows are made of, and aligned to, pieces
-// of so many bytes.
+// By all threads of the block; rows are made of, and aligned to, pieces of so many bytes.
 template <typename T>
-__device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, unsigned first, unsigned end,
-                                          int tokens, int cols, int piece) {
+__device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, int rows, int tokens, int cols,
+                                          int piece) {
   if (piece == 16) {
-    copy_rows<16>(tile, src, stride, first, end, tokens, cols);
+    copy_rows<16>(tile, src, stride, rows, tokens, cols);
   } else if (sizeof(T) == 4 || piece == 4) {
-    copy_rows<4>(tile, src, stride, first, end, tokens, cols);
+    copy_rows<4>(tile, src, stride, rows, tokens, cols);
   } else if constexpr (sizeof(T) == 2) {
-    copy_rows<2>(tile, src, stride, first, end, tokens, cols);
+    copy_rows<2>(tile, src, stride, rows, tokens, cols);
   }
 }
 
@@ -136,11 +150,6 @@ __device__ __forceinline__ float sqrt_ftz(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
 }
 template <typename F>
 __device__ __forceinline__ f32x2 each(f32x2 x, F f) {
@@ -162,13 +171,22 @@ __device__ __forceinline__ f32x2 expm1_small(f32x2 u) {
   r = fma2(r, u, dup2(1.f));
   return mul2(r, u);
 }
-// e^-g, at most 2^126 so that its product with sigmoid(g) = 1 / (1 + e^-g) is 1 - sigmoid(g)
-// for every g
-__device__ __forceinline__ f32x2 exp_neg(f32x2 g) {
-  return each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(min_nan(v, 126.f)); });
-}
 __device__ __forceinline__ f32x2 rcp2(f32x2 x) {
   return each(x, [](float v) { return rcp(v); });
+}
+// sigmoid(g) and 1 - sigmoid(g), each to its last digits: with e = e^-g and q = 1 / (1 + e) they are q and
+// e q, but what is nearer to 1 is 1 less the other.
+__device__ __forceinline__ void sigmoid2(f32x2 g, f32x2& sig, f32x2& rest) {
+  const f32x2 one = dup2(1.f), e = each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(v); });
+  const f32x2 q = rcp2(add2(e, one)), eq = mul2(e, q);
+  float e0, e1, q0, q1, p0, p1, l0, l1, r0, r1;
+  unpack2(e, e0, e1);
+  unpack2(q, q0, q1);
+  unpack2(eq, p0, p1);
+  unpack2(fma2(neg2(e), q, one), l0, l1);
+  unpack2(add2(one, neg2(q)), r0, r1);
+  sig = pack2(e0 < 1.f ? l0 : q0, e1 < 1.f ? l1 : q1);
+  rest = pack2(e0 < 1.f ? p0 : r0, e1 < 1.f ? p1 : r1);
 }
 
 // small where |u| < 1/2, else large
@@ -188,11 +206,11 @@ __device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
   const f32x2 one = dup2(1.f);
   f32x2 left;  // 1 - a
   if (kGate == GLR_SIGMOID) {
-    const f32x2 e = exp_neg(g), q = rcp2(add2(e, one));
-    left = mul2(e, q);
-    a = by_size(left, add2(one, neg2(left)), q);
+    sigmoid2(g, a, left);
   } else {
-    const f32x2 log = kGate == GLR_LOG ? g : mul2(rate, rcp2(add2(exp_neg(g), one)));
+    f32x2 log = g;
+    if (kGate == GLR_RATE)
+      log = mul2(rate, rcp2(add2(each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(v); }), one)));
     const f32x2 e = each(mul2(log, dup2(kLog2e)), [](float v) { return ex2(v); }), small = expm1_small(log);
     a = by_size(log, add2(one, small), e);
     if (kNorm != GLR_NONE) left = by_size(log, neg2(small), add2(one, neg2(e)));

@@ -4,8 +4,8 @@
 //
 // One pass: a token's x and gate are read once, its decay and weighted input stay in registers
 // until the state before them is known.  In a round the blocks of a cluster take 64 tokens each of
-// the same 64 channels: every thread reduces its 8 tokens to (A, H), the warps exchange these through
-// shared memory and the blocks through each other's, and a second walk over the 8 tokens, now
+// the same 64 channels: every thread reduces its 16 tokens to (A, H), the warps exchange these through
+// shared memory and the blocks through each other's, and a second walk over the 16 tokens, now
 // from the right state, writes y.  Tiles arrive by asynchronous copies, two rounds ahead.
 //
 // State, products and sums are fp32; y is rounded once.
@@ -19,13 +19,15 @@ namespace {
 constexpr int kStages = 3;
 
 template <typename T, int kGate, int kNorm, bool kPacked>
-__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_fwd_kernel(const GlrParams p) {
+__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 4 : 2) glr_fwd_kernel(const GlrParams p) {
   extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][64 tokens][64 channels]
   __shared__ ulonglong2 s_warp[2][kGlrWarps][32];
   __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  volatile int* const dead = &s_dead;
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (known to be the warp's)
   const unsigned K = p.cluster, rank = K > 1 ? cluster_rank() : 0;
   if (K > 1) {
     if (threadIdx.x == 0) {
@@ -54,12 +56,11 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_fw
   const auto fetch = [&](unsigned r) {  // round r into its stage
     if (r < rounds) {
       const unsigned first = r * round + rank * span;
+      const int left = first < end ? (int)min(end - first, 64u) : 0;  // rows that exist
       const long long at = row * p.T + first;
       T* to = tiles + r % kStages * (2 * 64 * 64);
-      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, first, end, span, cols,
-                p.piece);
-      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, first, end,
-                span, cols, p.piece);
+      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
+      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
     }
     cp_async_commit();
   };
@@ -70,7 +71,8 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_fw
   if (K > 1) cluster_wait();
   for (unsigned r = 0; r < rounds; ++r, t += round) {
     const int turn = r & 1;
-    if (K > 1 && threadIdx.x == 0) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
+    // (a block that has given up a wait neither expects nor sends: its neighbours give up, too)
+    if (K > 1 && threadIdx.x == 0 && !*dead) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
     cp_async_wait<kStages - 2>();
     __syncthreads();
     fetch(r + kStages - 1);
@@ -113,8 +115,10 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_fw
     }
     f32x2 h = carry;
     if (K > 1) {
-      if (warp < (int)K) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], warp, sA, sH);
-      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, &s_dead);
+      if (!*dead) {
+        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], k, sA, sH);
+      }
+      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
       f32x2 now = carry;
       for (unsigned k = 0; k < K; ++k) {
         if (k == rank) h = now;
@@ -128,6 +132,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_fw
     if (p.states && warp == 0 && n)
       store_f32(p.states + (row * p.chunks + t / kGlrSpan) * p.D + c, h, vec, c0, c1);
     h = through<kPacked>(A, H, h);
+    const int last = t + n == end ? n : 0;  // (1 and on: the row's last token is among these)
 #pragma unroll
     for (int i = 0; i < kGlrRun; ++i) {
       h = kPacked && borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_fw
         o.set(h);
         o.store(y + i * (long long)p.D, vec, c0, c1);
       }
-      if (kPacked ? i < n && borders >> (i + 1) & 1 : t + i + 1 == end) {
+      if (kPacked ? i < n && borders >> (i + 1) & 1 : i + 1 == last) {
         if (p.hT) {
           const long long q = kPacked ? sequence_of(p.cu, p.N, (int)end, (int)t + i) : row;
           store_f32(p.hT + q * p.D + c, h, vec, c0, c1);

@@ -89,7 +89,7 @@ cudaError_t launch_norm(const NormParams& p, bool f32, bool fp8, cudaStream_t st
 // Gated linear recurrence: prompt, its gradient, or one token (h0 == hT, T = 1).
 enum { GLR_LOG = 0, GLR_SIGMOID = 1, GLR_RATE = 2 };    // as GDN_GLR_GATE_*
 enum { GLR_NONE = 0, GLR_LINEAR = 1, GLR_SQRT = 2 };    // as GDN_GLR_INPUT_*
-constexpr int kGlrSpan = 64, kGlrWarps = 8, kGlrMaxCluster = 8;
+constexpr int kGlrSpan = 64, kGlrWarps = 4, kGlrMaxCluster = 8;
 struct GlrParams {
   const void *x, *g, *dy;           // rows of D channels; dy: gradient only
   const float *rate;                // [D], GLR_RATE only
