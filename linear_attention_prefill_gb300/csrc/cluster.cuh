@@ -70,25 +70,37 @@ __device__ __forceinline__ void wait_for_ranks(uint64_t* bar, unsigned parity, u
 }
 
 // A launch in clusters of `blocks` (1: none) neighbouring blocks, with `smem` bytes of dynamic memory.
+template <typename Kernel>
+cudaError_t allow_clusters(Kernel kernel, unsigned blocks, size_t smem) {
+  cudaError_t e = cudaSuccess;
+  if (smem) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // more than 8 is more than every GPU of the family takes
+  if (e == cudaSuccess && blocks > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return e;
+}
+struct ClusterConfig {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  ClusterConfig(unsigned grid, unsigned threads, unsigned blocks, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = blocks > 1 ? 1 : 0;
+  }
+};
 template <typename Kernel, typename Params>
 cudaError_t launch_clusters(Kernel kernel, unsigned grid, unsigned threads, unsigned blocks, const Params& p,
                             cudaStream_t stream, size_t smem = 0) {
-  if (smem) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = blocks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = allow_clusters(kernel, blocks, smem);
+  if (e != cudaSuccess) return e;
+  const ClusterConfig c(grid, threads, blocks, smem, stream);
+  return cudaLaunchKernelEx(&c.cfg, kernel, p);
 }
 
 }  // namespace gdn

@@ -1,5 +1,4 @@
 // glr_abi.cu - the extern "C" boundary of the gated linear recurrence (declared in include/gdn.h).
-#include <stdlib.h>
 #include <initializer_list>
 
 #include "layer_check.h"
@@ -20,20 +19,6 @@ bool known(int gate, int norm) {
          norm <= GDN_GLR_INPUT_SQRT;
 }
 
-// How a prompt is cut: a block's warps take 16 tokens each, 64 together where there are as many, and
-// a cluster's blocks go on in time.
-void plan(GlrParams* p) {
-  p->tiles = (p->D - 1) / 64 + 1;
-  p->chunks = ((long long)p->T + gdn::kGlrSpan - 1) / gdn::kGlrSpan;
-  const int run = gdn::kGlrSpan / gdn::kGlrWarps;
-  p->warps = p->T >= gdn::kGlrSpan ? gdn::kGlrWarps : p->T > run ? (p->T - 1) / run + 1 : 1;
-  p->cluster = 1;
-  const long long want = getenv("GLR_WANT") ? atoll(getenv("GLR_WANT")) : 2 * gdn::kSms;
-  while (p->cluster < gdn::kGlrMaxCluster && gdn::glr_units(*p) * p->cluster < want &&
-         (long long)p->cluster * gdn::kGlrSpan < p->T)
-    p->cluster *= 2;
-}
-
 // What every call shares.
 gdn_status check(const void* x, const void* g, const float* rate, int N, int T, int D, long long x_stride,
                  long long g_stride, int gate, int norm, const int32_t* cu, int elem, long long* tokens,
@@ -50,8 +35,9 @@ gdn_status check(const void* x, const void* g, const float* rate, int N, int T, 
   p->x = x; p->g = g; p->rate = rate; p->cu = cu;
   p->x_stride = x_stride; p->g_stride = g_stride;
   p->N = N; p->T = T; p->D = D; p->gate = gate; p->norm = norm;
-  plan(p);
-  if (gdn::glr_units(*p) * p->cluster > gdn::kMaxGrid)
+  p->tiles = (D - 1) / 64 + 1;
+  p->chunks = ((long long)T + gdn::kGlrChunk - 1) / gdn::kGlrChunk;
+  if (gdn::glr_units(*p) * gdn::glr_most_blocks(*p) > gdn::kMaxGrid)
     return fail(GDN_ERR_INVALID_ARG, "problem too large: N=%d D=%d", N, D);
   return GDN_OK;
 }
@@ -134,7 +120,7 @@ gdn_status step(const void* x, const void* g, const float* rate, float* h, void*
 }
 
 size_t partial_bytes(const GlrParams& p) {
-  return p.gate == GDN_GLR_GATE_RATE ? (size_t)(p.cu ? 1 : p.N) * p.cluster * p.D * 4 : 0;
+  return p.gate == GDN_GLR_GATE_RATE ? (size_t)(p.cu ? 1 : p.N) * gdn::glr_most_blocks(p) * p.D * 4 : 0;
 }
 
 gdn_status backward(const void* dy, const void* x, const void* g, const float* rate, const float* h0,
@@ -165,7 +151,7 @@ gdn_status backward(const void* dy, const void* x, const void* g, const float* r
     for (int j = 0; j < i; ++j)
       if (gdn::overlap(outs[i], outs[j])) return fail(GDN_ERR_INVALID_ARG, "the outputs must not overlap each other");
   }
-  if (rows * p.cluster > gdn::kMaxGrid) return fail(GDN_ERR_INVALID_ARG, "problem too large: N=%d", N);
+  if (rows * gdn::glr_most_blocks(p) > gdn::kMaxGrid) return fail(GDN_ERR_INVALID_ARG, "problem too large: N=%d", N);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (N == 0 || (tokens == 0 && !dh0)) {  // the rate's gradient is a sum over nothing
     const cudaError_t e = drate ? cudaMemsetAsync(drate, 0, (size_t)D * 4, st) : cudaSuccess;
@@ -188,9 +174,8 @@ gdn_status backward(const void* dy, const void* x, const void* g, const float* r
     }
     p.partial = static_cast<float*>(ws);
   }
-  cudaError_t e = gdn::launch_glr_bwd(p, f32, st);
-  if (e == cudaSuccess && need)
-    e = gdn::launch_column_sums(p.partial, drate, nullptr, (int)(rows * p.cluster), D, st);
+  p.drate = drate;
+  const cudaError_t e = gdn::launch_glr_bwd(p, f32, st);
   const cudaError_t ef = pool ? cudaFreeAsync(pool, st) : cudaSuccess;
   if (e != cudaSuccess) return cuda_fail(e, "launching the gated recurrence's gradient");
   return ef == cudaSuccess ? GDN_OK : cuda_fail(ef, "freeing the workspace");
@@ -234,7 +219,6 @@ size_t gdn_glr_chunk_bwd_workspace_size(int N, int T, int D, int gate, int has_c
   const int32_t some = 0;
   p.N = N; p.T = T; p.D = D; p.gate = gate;
   p.cu = has_cu_seqlens ? &some : nullptr;
-  plan(&p);
   return partial_bytes(p);
 }
 

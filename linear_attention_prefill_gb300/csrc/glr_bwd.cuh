@@ -23,7 +23,8 @@ namespace gdn {
 namespace {
 
 // Two rounds' tiles: three would leave two blocks an SM instead of three.
-constexpr int kStages = 2;
+constexpr int kMinBlocks = kGlrBwdBlocks, kStages = 2, kRun = kGlrBwdRun, kWarps = kGlrBwdWarps;
+constexpr int kTile = kRun * kWarps * 64;  // of a tensor's tokens in shared memory
 
 // lambda of a sequence's last token without what comes from behind: dy + dhT
 __device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end, int t, long long c, bool c0,
@@ -33,9 +34,9 @@ __device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end
 }
 
 template <typename T, int kGate, int kNorm, bool kPacked>
-__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bwd_kernel(const GlrParams p) {
-  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][64 tokens][64 channels]
-  __shared__ ulonglong2 s_ahead[2][kGlrWarps][32], s_back[2][kGlrWarps][32];
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) glr_bwd_kernel(const GlrParams p) {
+  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][tokens][64 channels]
+  __shared__ ulonglong2 s_ahead[2][kWarps][32], s_back[2][kWarps][32];
   __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
   const long long c = (long long)tile * 64 + 2 * lane;
   const bool c0 = c < p.D, c1 = c + 1 < p.D;
   const unsigned end = kPacked ? min(max(p.cu[p.N], 0), p.T) : p.T;
-  const unsigned span = warps * kGlrRun, round = K * span;
+  const unsigned span = warps * kRun, round = K * span;
   const unsigned rounds = end ? (end - 1) / round + 1 : 0;
   const f32x2 rate = kGate == GLR_RATE ? load_f32(p.rate + c, vec, c0, c1) : 0ull;
   f32x2 carry = !kPacked && p.dhT ? load_f32(p.dhT + row * p.D + c, vec, c0, c1) : 0ull;
@@ -71,24 +72,27 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
   const auto fetch = [&](unsigned r) {  // round r, counted from the last tokens, into its stage
     if (r < rounds) {
       const unsigned first = (rounds - 1 - r) * round + rank * span;
-      const int left = first < end ? (int)min(end - first, 64u) : 0;  // rows that exist
+      const int left = first < end ? (int)min(end - first, (unsigned)(kRun * kWarps)) : 0;  // rows that exist
       const long long at = row * p.T + first;
-      T* to = tiles + r % kStages * (3 * 64 * 64);
-      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
-      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
-      copy_tile(to + 2 * 64 * 64, static_cast<const T*>(p.dy) + at * p.dy_stride + tile * 64ll, p.dy_stride, left,
+      T* to = tiles + r % kStages * (3 * kTile);
+      copy_tile<kRun * kWarps, 32 * kWarps>(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
+      copy_tile<kRun * kWarps, 32 * kWarps>(to + kTile, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
+      copy_tile<kRun * kWarps, 32 * kWarps>(to + 2 * kTile, static_cast<const T*>(p.dy) + at * p.dy_stride + tile * 64ll, p.dy_stride, left,
                 span, cols, p.piece);
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int r = 0; r < kStages - 1; ++r) fetch(r);
-  unsigned t = (rounds - 1) * round + rank * span + warp * kGlrRun;  // this thread's first token
-  // the state before the block's tokens, of this round and the next
-  const auto state_before = [&](unsigned first) {
-    return first < end ? load_f32(p.kept + (row * p.chunks + first / kGlrSpan) * p.D + c, vec, c0, c1) : 0ull;
+  unsigned t = (rounds - 1) * round + rank * span + warp * kRun;  // this thread's first token
+  // the state before the chunk of 64 tokens that t lies in, of this round and the next; the chunk's warps
+  // before this one lead on from it
+  static_assert(kRun * kWarps % kGlrChunk == 0, "blocks of whole chunks");
+  const auto state_before = [&](unsigned t) {
+    return t < end ? load_f32(p.kept + (row * p.chunks + t / kGlrChunk) * p.D + c, vec, c0, c1) : 0ull;
   };
-  f32x2 before = rounds ? state_before(t - warp * kGlrRun) : 0ull;
+  f32x2 before = rounds ? state_before(t) : 0ull;
+  constexpr int kChunkWarps = kGlrChunk / kRun;
   if (K > 1) cluster_wait();
   for (unsigned r = 0; r < rounds; ++r, t -= round) {
     const int turn = r & 1;
@@ -97,17 +101,17 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
     cp_async_wait<kStages - 2>();
     __syncthreads();
     fetch(r + kStages - 1);
-    const T* xs = tiles + r % kStages * (3 * 64 * 64) + warp * kGlrRun * 64;
-    const T *gs = xs + 64 * 64, *ds = gs + 64 * 64;
-    const int n = t < end ? (int)min(end - t, (unsigned)kGlrRun) : 0;  // tokens that exist
-    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t) : 0u;
+    const T* xs = tiles + r % kStages * (3 * kTile) + warp * kRun * 64;
+    const T *gs = xs + kTile, *ds = gs + kTile;
+    const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist
+    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t, kRun) : 0u;
     f32x2 h = before;
-    if (r + 1 < rounds) before = state_before(t - warp * kGlrRun - round);
-    f32x2 a[kGlrRun], s[kGlrRun];
+    if (r + 1 < rounds) before = state_before(t - round);
+    f32x2 a[kRun], s[kRun];
     f32x2 A = dup2(1.f), H = 0ull;
     bool cut = false;
 #pragma unroll
-    for (int i = 0; i < kGlrRun; ++i) {
+    for (int i = 0; i < kRun; ++i) {
       gate2<kGate, kNorm>(pair_at(gs, i, lane), rate, a[i], s[i]);
       const f32x2 x = pair_at(xs, i, lane), b = kNorm == GLR_NONE ? x : mul2(s[i], x);
       if (kPacked && borders >> i & 1) {
@@ -123,12 +127,12 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
     }
     s_ahead[turn][warp][lane] = make_ulonglong2(kPacked && cut ? 0ull : at_least_tiny(A), H);
     // backwards: m before these tokens from m behind them; tokens that do not exist pass it on
-    const bool same = !kPacked && n == kGlrRun;  // (then the decays' product is the one forwards)
+    const bool same = !kPacked && n == kRun;  // (then the decays' product is the one forwards)
     if (!same) A = dup2(1.f);
     f32x2 M = 0ull;
     cut = false;
 #pragma unroll
-    for (int i = kGlrRun - 1; i >= 0; --i) {
+    for (int i = kRun - 1; i >= 0; --i) {
       const f32x2 dy = pair_at(ds, i, lane);
       if (i >= n) {
         a[i] = dup2(1.f);
@@ -143,17 +147,21 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
     A = kPacked && cut ? 0ull : at_least_tiny(A);
     s_back[turn][warp][lane] = make_ulonglong2(A, M);
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
+    for (int w = warp / kChunkWarps * kChunkWarps; w < warp; ++w) {
       const ulonglong2 v = s_ahead[turn][w][lane];
       h = through<kPacked>(v.x, v.y, h);
     }
     f32x2 sA = dup2(1.f), sM = 0ull;
+    const auto lead = [&](int from, int to) {  // warps from - 1 down to `to`
 #pragma unroll 4
-    for (int w = warps - 1; w >= 0; --w) {
-      if (w == warp) A = sA, M = sM;
-      const ulonglong2 v = s_back[turn][w][lane];
-      follow<kPacked>(sA, sM, v.x, v.y);
-    }
+      for (int w = from - 1; w >= to; --w) {
+        const ulonglong2 v = s_back[turn][w][lane];
+        follow<kPacked>(sA, sM, v.x, v.y);
+      }
+    };
+    lead(warps, warp + 1);
+    A = sA, M = sM;
+    lead(warp + 1, 0);
     f32x2 m = carry;
     if (K > 1) {
       if (!*dead) {
@@ -161,19 +169,24 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
       }
       wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
       f32x2 now = carry;
-      for (int k = (int)K - 1; k >= 0; --k) {
-        if (k == (int)rank) m = now;
-        const ulonglong2 v = s_rank[turn][k][lane];
-        now = through<kPacked>(v.x, v.y, now);
-      }
+      const auto pass = [&](int from, int to) {
+#pragma unroll 4
+        for (int k = from - 1; k >= to; --k) {
+          const ulonglong2 v = s_rank[turn][k][lane];
+          now = through<kPacked>(v.x, v.y, now);
+        }
+      };
+      pass((int)K, (int)rank + 1);
+      m = now;
+      pass((int)rank + 1, 0);
       carry = now;
     } else {
       carry = through<kPacked>(sA, sM, carry);
     }
     m = through<kPacked>(A, M, m);
-    f32x2 hp[kGlrRun];  // the state before each token
+    f32x2 hp[kRun];  // the state before each token
 #pragma unroll
-    for (int i = 0; i < kGlrRun; ++i) {
+    for (int i = 0; i < kRun; ++i) {
       if (kPacked && borders >> i & 1) {
         h = 0ull;
         if (p.h0 && i < n)
@@ -183,23 +196,24 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
       const f32x2 x = pair_at(xs, i, lane);
       h = fma2(a[i], h, kNorm == GLR_NONE ? x : mul2(s[i], x));
     }
-    T* dx = static_cast<T*>(p.dx) + (row * p.T + t) * p.D + c;
-    T* dg = static_cast<T*>(p.dg) + (row * p.T + t) * p.D + c;
+    T* dx = static_cast<T*>(p.dx) + (row * p.T + t + kRun) * p.D + c;
+    T* dg = static_cast<T*>(p.dg) + (row * p.T + t + kRun) * p.D + c;
 #pragma unroll
-    for (int i = kGlrRun - 1; i >= 0; --i) {
+    for (int i = kRun - 1; i >= 0; --i) {
+      dx -= p.D, dg -= p.D;
       if (i >= n) continue;
       const f32x2 x = pair_at(xs, i, lane), dy = pair_at(ds, i, lane);
       const f32x2 lam = kPacked && borders >> (i + 1) & 1 ? with_last(p, dy, (int)end, (int)t + i, c, c0, c1)
                                                           : add2(dy, m);
       Raw2<T> o;
       o.set(kNorm == GLR_NONE ? lam : mul2(s[i], lam));
-      o.store(dx + i * (long long)p.D, vec, c0, c1);
+      o.store(dx, vec, c0, c1);
       // dL / (a lambda): h_{t-1} and the weight's share
       f32x2 slope = hp[i];
-      if (kNorm == GLR_LINEAR) slope = add2(slope, neg2(x));
+      if (kNorm == GLR_LINEAR) slope = fma2(x, dup2(-1.f), slope);
       if (kNorm == GLR_SQRT) {
-        const f32x2 inv = each(s[i], [](float v) { return v > 0.f ? rcp(v) : 0.f; });
-        slope = fma2(neg2(mul2(a[i], inv)), x, slope);
+        const f32x2 inv = each(s[i], [](float v) { return v > 0.f ? -rcp(v) : 0.f; });
+        slope = fma2(mul2(a[i], inv), x, slope);
       }
       m = mul2(a[i], lam);
       f32x2 d = mul2(m, slope);
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
         d = mul2(mul2(d, rate), rest);
       }
       o.set(d);
-      o.store(dg + i * (long long)p.D, vec, c0, c1);
+      o.store(dg, vec, c0, c1);
       if (kPacked ? borders >> i & 1 : t + i == 0) {
         if (p.dh0) {
           const long long q = kPacked ? sequence_of(p.cu, p.N, (int)end, (int)t + i) : row;
@@ -248,10 +262,20 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 3 : 2) glr_bw
   }
 }
 
+template <auto kKernel, typename T>
+cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
+  const size_t smem = kStages * 3 * kTile * sizeof(T);
+  const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
+  cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
+  if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
+  if (e == cudaSuccess) e = launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, smem);
+  if (e != cudaSuccess || !p.drate) return e;
+  return launch_column_sums(p.partial, p.drate, nullptr, (p.cu ? 1 : p.N) * p.cluster, p.D, stream);
+}
 template <typename T, int kGate, int kNorm>
 cudaError_t launch(const GlrParams& p, cudaStream_t stream) {
-  const auto kernel = p.cu ? glr_bwd_kernel<T, kGate, kNorm, true> : glr_bwd_kernel<T, kGate, kNorm, false>;
-  return launch_clusters(kernel, glr_grid(p), 32 * p.warps, p.cluster, p, stream, kStages * 3 * 64 * 64 * sizeof(T));
+  return p.cu ? launch_prompt<glr_bwd_kernel<T, kGate, kNorm, true>, T>(p, stream)
+              : launch_prompt<glr_bwd_kernel<T, kGate, kNorm, false>, T>(p, stream);
 }
 template <typename T, int kGate>
 cudaError_t launch_gate(const GlrParams& p, cudaStream_t stream) {

@@ -6,9 +6,12 @@
 //   weight    s = 1 (none), 1 - a (linear), sqrt(1 - a^2) (sqrt)
 //
 // A stretch of tokens maps the state before it to A h + H.  Stretches compose, so time is cut
-// everywhere: a thread has kGlrRun tokens of two channels, a warp 64 channels, a block's warps
+// everywhere: a thread has kRun tokens of two channels, a warp 64 channels, a block's warps
 // follow each other in time, and so do the blocks of a cluster.
 #pragma once
+
+#include <stdlib.h>
+#include <atomic>
 
 #include "cluster.cuh"
 #include "layer_common.cuh"
@@ -16,8 +19,7 @@
 
 namespace gdn {
 
-constexpr int kGlrRun = kGlrSpan / kGlrWarps;  // tokens of a thread in a round
-constexpr float kTiny = 1.17549435e-38f;       // 2^-126
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
 // ---- two channels of a row ---------------------------------------------------------------
 // Channels 2 lane, 2 lane + 1 of a warp's 64: in one access where rows are aligned to pairs (vec).
@@ -105,13 +107,13 @@ __device__ __forceinline__ void copy_piece(void* to, const void* from, bool ok) 
     *static_cast<uint16_t*>(to) = ok ? *static_cast<const uint16_t*>(from) : (uint16_t)0;
   }
 }
-// Up to 64 rows (`tokens`) of 64 channels, `cols` of which exist, from src; zeros for rows from `rows` on
-// and for channels that do not exist.
-template <int kBytes, typename T>
+// Up to kTokens rows (`tokens`) of 64 channels, `cols` of which exist, from src; zeros for rows from
+// `rows` on and for channels that do not exist.
+template <int kBytes, int kTokens, int kThreads, typename T>
 __device__ __forceinline__ void copy_rows(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
   constexpr int kCols = kBytes / (int)sizeof(T), kPieces = 64 / kCols;
-  if (kBytes == 16 && blockDim.x == 128 && rows >= 64) {  // a whole tile, by a whole block
-    constexpr int kStep = 128 / kPieces;
+  if (kBytes == 16 && blockDim.x == kThreads && rows >= kTokens) {  // a whole tile, by a whole block
+    constexpr int kStep = kThreads / kPieces;
     const int row = threadIdx.x / kPieces, col = threadIdx.x % kPieces * kCols;
     const T* from = src + row * stride + col;
     const bool ok = col < cols;
@@ -119,7 +121,7 @@ __device__ __forceinline__ void copy_rows(T* tile, const T* src, long long strid
     const long long step = ok ? kStep * stride : 0;
     tile += row * 64 + col;
 #pragma unroll
-    for (int i = 0; i < 64 / kStep; ++i) {
+    for (int i = 0; i < kTokens / kStep; ++i) {
       copy_piece<kBytes>(tile + i * kStep * 64, from, ok);
       from += step;
     }
@@ -133,15 +135,15 @@ __device__ __forceinline__ void copy_rows(T* tile, const T* src, long long strid
   }
 }
 // By all threads of the block; rows are made of, and aligned to, pieces of so many bytes.
-template <typename T>
+template <int kTokens, int kThreads, typename T>
 __device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, int rows, int tokens, int cols,
                                           int piece) {
   if (piece == 16) {
-    copy_rows<16>(tile, src, stride, rows, tokens, cols);
+    copy_rows<16, kTokens, kThreads>(tile, src, stride, rows, tokens, cols);
   } else if (sizeof(T) == 4 || piece == 4) {
-    copy_rows<4>(tile, src, stride, rows, tokens, cols);
+    copy_rows<4, kTokens, kThreads>(tile, src, stride, rows, tokens, cols);
   } else if constexpr (sizeof(T) == 2) {
-    copy_rows<2>(tile, src, stride, rows, tokens, cols);
+    copy_rows<2, kTokens, kThreads>(tile, src, stride, rows, tokens, cols);
   }
 }
 
@@ -174,28 +176,22 @@ __device__ __forceinline__ f32x2 expm1_small(f32x2 u) {
 __device__ __forceinline__ f32x2 rcp2(f32x2 x) {
   return each(x, [](float v) { return rcp(v); });
 }
+__device__ __forceinline__ f32x2 exp_neg(f32x2 g) {
+  return each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(v); });
+}
 // sigmoid(g) and 1 - sigmoid(g), each to its last digits: with e = e^-g and q = 1 / (1 + e) they are q and
 // e q, but what is nearer to 1 is 1 less the other.
 __device__ __forceinline__ void sigmoid2(f32x2 g, f32x2& sig, f32x2& rest) {
-  const f32x2 one = dup2(1.f), e = each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(v); });
-  const f32x2 q = rcp2(add2(e, one)), eq = mul2(e, q);
+  const f32x2 one = dup2(1.f), minus = dup2(-1.f), e = exp_neg(g);
+  const f32x2 nq = rcp2(fma2(e, minus, minus));  // -q
   float e0, e1, q0, q1, p0, p1, l0, l1, r0, r1;
   unpack2(e, e0, e1);
-  unpack2(q, q0, q1);
-  unpack2(eq, p0, p1);
-  unpack2(fma2(neg2(e), q, one), l0, l1);
-  unpack2(add2(one, neg2(q)), r0, r1);
-  sig = pack2(e0 < 1.f ? l0 : q0, e1 < 1.f ? l1 : q1);
-  rest = pack2(e0 < 1.f ? p0 : r0, e1 < 1.f ? p1 : r1);
-}
-
-// small where |u| < 1/2, else large
-__device__ __forceinline__ f32x2 by_size(f32x2 u, f32x2 small, f32x2 large) {
-  float u0, u1, s0, s1, l0, l1;
-  unpack2(u, u0, u1);
-  unpack2(small, s0, s1);
-  unpack2(large, l0, l1);
-  return pack2(fabsf(u0) < 0.5f ? s0 : l0, fabsf(u1) < 0.5f ? s1 : l1);
+  unpack2(nq, q0, q1);
+  unpack2(mul2(e, nq), p0, p1);
+  unpack2(fma2(e, nq, one), l0, l1);
+  unpack2(add2(one, nq), r0, r1);
+  sig = pack2(e0 < 1.f ? l0 : -q0, e1 < 1.f ? l1 : -q1);
+  rest = pack2(e0 < 1.f ? -p0 : r0, e1 < 1.f ? -p1 : r1);
 }
 
 // The decay a and the input's weight s of a token.  Decays next to 1 come from 1 - a, which keeps its
@@ -209,11 +205,17 @@ __device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
     sigmoid2(g, a, left);
   } else {
     f32x2 log = g;
-    if (kGate == GLR_RATE)
-      log = mul2(rate, rcp2(add2(each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(v); }), one)));
+    if (kGate == GLR_RATE) log = mul2(rate, rcp2(add2(exp_neg(g), one)));
     const f32x2 e = each(mul2(log, dup2(kLog2e)), [](float v) { return ex2(v); }), small = expm1_small(log);
-    a = by_size(log, add2(one, small), e);
-    if (kNorm != GLR_NONE) left = by_size(log, neg2(small), add2(one, neg2(e)));
+    float u0, u1, s0, s1, a0, a1, e0, e1, d0, d1;
+    unpack2(log, u0, u1);
+    unpack2(small, s0, s1);
+    unpack2(add2(one, small), a0, a1);
+    unpack2(e, e0, e1);
+    unpack2(fma2(e, dup2(-1.f), one), d0, d1);
+    const bool near0 = fabsf(u0) < 0.5f, near1 = fabsf(u1) < 0.5f;
+    a = pack2(near0 ? a0 : e0, near1 ? a1 : e1);
+    left = pack2(near0 ? -s0 : d0, near1 ? -s1 : d1);
   }
   if (kNorm == GLR_NONE) s = one;
   if (kNorm == GLR_LINEAR) s = left;
@@ -274,18 +276,53 @@ __device__ __forceinline__ int first_border_above(const int32_t* cu, int N, int 
 static __device__ __noinline__ int sequence_of(const int32_t* cu, int N, int end, int v) {
   return min(max(first_border_above(cu, N, end, v) - 1, 0), N - 1);
 }
-// Bit i: a sequence starts at token t + i, or the last one ends before it (i <= kGlrRun).
-static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int end, int t) {
+// Bit i: a sequence starts at token t + i, or the last one ends before it (i <= run).
+static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int end, int t, int run) {
   int m = first_border_above(cu, N, end, t);
   unsigned bits = m > 0 && min(max(cu[m - 1], 0), end) == t ? 1u : 0u;
   while (m <= N) {
     const int b = min(max(cu[m], 0), end);  // above t, and above the one before
-    if (b - t > kGlrRun) break;
+    if (b - t > run) break;
     bits |= 1u << (b - t);
     if (b >= end) break;
     m = first_border_above(cu, N, end, b);
   }
   return bits;
+}
+
+// ---- launches --------------------------------------------------------------------------------
+// Blocks of a cluster: they go on together through a row's `spans`, and as many clusters as there is room
+// for run at once, which depends on the size (of 256 threads at two blocks an SM, 36 clusters of 8 but only
+// 14 of 14 fit this GPU).  The size with the fewest rounds over all waves of clusters is taken.  The GPU is
+// asked once for each kernel and size.
+template <auto kKernel>
+cudaError_t choose_cluster(GlrParams* p, unsigned threads, size_t smem, long long spans) {
+  static std::atomic<int> room[kGlrMaxCluster + 1];
+  const long long units = glr_units(*p);
+  long long best = -1;
+  const int force = getenv("GLR_K") ? atoi(getenv("GLR_K")) : 0;
+  for (int k = 1; k <= kGlrMaxCluster && (k == 1 || k <= spans); ++k) {
+    int n = room[k].load(std::memory_order_relaxed);
+    if (!n) {
+      cudaError_t e = allow_clusters(kKernel, k, smem);
+      if (e != cudaSuccess) return e;
+      const ClusterConfig c(k, threads, k, smem, nullptr);
+      if (k == 1) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, threads, smem);
+        n *= kSms;
+      } else {
+        e = cudaOccupancyMaxActiveClusters(&n, kKernel, &c.cfg);
+      }
+      if (e != cudaSuccess) return e;
+      n = n < 1 ? -1 : n;
+      room[k].store(n, std::memory_order_relaxed);
+    }
+    if (n < 0) continue;
+    // (a wave's start costs about two rounds)
+    const long long cost = ((units + n - 1) / n) * ((spans + k - 1) / k + 2);
+    if (best < 0 || cost < best || k == force) best = k == force ? 0 : cost, p->cluster = k;
+  }
+  return best < 0 ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
 
 }  // namespace gdn

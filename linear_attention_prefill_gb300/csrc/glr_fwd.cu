@@ -3,9 +3,7 @@
 
 namespace gdn {
 
-cudaError_t launch_glr(GlrParams p, bool f32, cudaStream_t stream) {
-  const cudaError_t e = p.cluster > 1 ? device_error_word(&p.err) : cudaSuccess;
-  if (e != cudaSuccess) return e;
+cudaError_t launch_glr(const GlrParams& p, bool f32, cudaStream_t stream) {
   return f32 ? launch_glr_f32(p, false, stream) : launch_type<__nv_bfloat16>(p, false, stream);
 }
 cudaError_t launch_glr_step(const GlrParams& p, bool f32, cudaStream_t stream) {

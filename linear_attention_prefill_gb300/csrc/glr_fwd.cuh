@@ -16,12 +16,13 @@
 namespace gdn {
 namespace {
 
-constexpr int kStages = 3;
+constexpr int kMinBlocks = kGlrFwdBlocks, kStages = 2, kRun = kGlrFwdRun, kWarps = kGlrFwdWarps;
+constexpr int kTile = kRun * kWarps * 64;  // of a tensor's tokens in shared memory
 
 template <typename T, int kGate, int kNorm, bool kPacked>
-__global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 4 : 2) glr_fwd_kernel(const GlrParams p) {
-  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][64 tokens][64 channels]
-  __shared__ ulonglong2 s_warp[2][kGlrWarps][32];
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) glr_fwd_kernel(const GlrParams p) {
+  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][tokens][64 channels]
+  __shared__ ulonglong2 s_warp[2][kWarps][32];
   __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 4 : 2) glr_fw
   const long long c = (long long)tile * 64 + 2 * lane;
   const bool c0 = c < p.D, c1 = c + 1 < p.D;
   const unsigned end = kPacked ? min(max(p.cu[p.N], 0), p.T) : p.T;
-  const unsigned span = warps * kGlrRun, round = K * span;
+  const unsigned span = warps * kRun, round = K * span;
   const unsigned rounds = end ? (end - 1) / round + 1 : 0;
   const f32x2 rate = kGate == GLR_RATE ? load_f32(p.rate + c, vec, c0, c1) : 0ull;
   f32x2 carry = !kPacked && p.h0 ? load_f32(p.h0 + row * p.D + c, vec, c0, c1) : 0ull;
@@ -56,17 +57,17 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 4 : 2) glr_fw
   const auto fetch = [&](unsigned r) {  // round r into its stage
     if (r < rounds) {
       const unsigned first = r * round + rank * span;
-      const int left = first < end ? (int)min(end - first, 64u) : 0;  // rows that exist
+      const int left = first < end ? (int)min(end - first, (unsigned)(kRun * kWarps)) : 0;  // rows that exist
       const long long at = row * p.T + first;
-      T* to = tiles + r % kStages * (2 * 64 * 64);
-      copy_tile(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
-      copy_tile(to + 64 * 64, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
+      T* to = tiles + r % kStages * (2 * kTile);
+      copy_tile<kRun * kWarps, 32 * kWarps>(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
+      copy_tile<kRun * kWarps, 32 * kWarps>(to + kTile, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int r = 0; r < kStages - 1; ++r) fetch(r);
-  unsigned t = rank * span + warp * kGlrRun;  // this thread's first token
+  unsigned t = rank * span + warp * kRun;  // this thread's first token
   T* y = static_cast<T*>(p.y) + (row * p.T + t) * p.D + c;
   if (K > 1) cluster_wait();
   for (unsigned r = 0; r < rounds; ++r, t += round) {
@@ -76,15 +77,15 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 4 : 2) glr_fw
     cp_async_wait<kStages - 2>();
     __syncthreads();
     fetch(r + kStages - 1);
-    const T* xs = tiles + r % kStages * (2 * 64 * 64) + warp * kGlrRun * 64;
-    const T* gs = xs + 64 * 64;
-    const int n = t < end ? (int)min(end - t, (unsigned)kGlrRun) : 0;  // tokens that exist
-    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t) : 0u;
-    f32x2 a[kGlrRun], b[kGlrRun];
+    const T* xs = tiles + r % kStages * (2 * kTile) + warp * kRun * 64;
+    const T* gs = xs + kTile;
+    const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist
+    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t, kRun) : 0u;
+    f32x2 a[kRun], b[kRun];
     f32x2 A = dup2(1.f), H = 0ull;
     bool cut = false;
 #pragma unroll
-    for (int i = 0; i < kGlrRun; ++i) {
+    for (int i = 0; i < kRun; ++i) {
       f32x2 s;
       gate2<kGate, kNorm>(pair_at(gs, i, lane), rate, a[i], s);
       b[i] = pair_at(xs, i, lane);
@@ -107,42 +108,60 @@ __global__ void __launch_bounds__(32 * kGlrWarps, sizeof(T) == 2 ? 4 : 2) glr_fw
     __syncthreads();
     // all the warps' stretches in order; (A, H) becomes what lies before this warp's
     f32x2 sA = dup2(1.f), sH = 0ull;
+    const auto lead = [&](int from, int to) {
 #pragma unroll 4
-    for (int w = 0; w < warps; ++w) {
-      if (w == warp) A = sA, H = sH;
-      const ulonglong2 v = s_warp[turn][w][lane];
-      follow<kPacked>(sA, sH, v.x, v.y);
-    }
+      for (int w = from; w < to; ++w) {
+        const ulonglong2 v = s_warp[turn][w][lane];
+        follow<kPacked>(sA, sH, v.x, v.y);
+      }
+    };
+    lead(0, warp);
+    A = sA, H = sH;
     f32x2 h = carry;
     if (K > 1) {
+      lead(warp, warps);
       if (!*dead) {
         for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], k, sA, sH);
       }
       wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
       f32x2 now = carry;
-      for (unsigned k = 0; k < K; ++k) {
-        if (k == rank) h = now;
-        const ulonglong2 v = s_rank[turn][k][lane];
-        now = through<kPacked>(v.x, v.y, now);
-      }
+      const auto pass = [&](unsigned from, unsigned to) {
+#pragma unroll 4
+        for (unsigned k = from; k < to; ++k) {
+          const ulonglong2 v = s_rank[turn][k][lane];
+          now = through<kPacked>(v.x, v.y, now);
+        }
+      };
+      pass(0, rank);
+      h = now;
+      pass(rank, K);
       carry = now;
     } else {
+      lead(warp, warps);
       carry = through<kPacked>(sA, sH, carry);
     }
-    if (p.states && warp == 0 && n)
-      store_f32(p.states + (row * p.chunks + t / kGlrSpan) * p.D + c, h, vec, c0, c1);
     h = through<kPacked>(A, H, h);
-    const int last = t + n == end ? n : 0;  // (1 and on: the row's last token is among these)
+    if (p.states && t % kGlrChunk == 0 && n)
+      store_f32(p.states + (row * p.chunks + t / kGlrChunk) * p.D + c, h, vec, c0, c1);
+    if (!kPacked && n == kRun && t + kRun != end) {
+      T* to = y;
 #pragma unroll
-    for (int i = 0; i < kGlrRun; ++i) {
-      h = kPacked && borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
-      if (i < n) {
+      for (int i = 0; i < kRun; ++i, to += p.D) {
+        h = fma2(a[i], h, b[i]);
         Raw2<T> o;
         o.set(h);
-        o.store(y + i * (long long)p.D, vec, c0, c1);
+        o.store(to, vec, c0, c1);
       }
-      if (kPacked ? i < n && borders >> (i + 1) & 1 : i + 1 == last) {
-        if (p.hT) {
+    } else {  // the last tokens of sequences among them, or fewer tokens
+      T* to = y;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i, to += p.D) {
+        if (i >= n) break;
+        h = kPacked && borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
+        Raw2<T> o;
+        o.set(h);
+        o.store(to, vec, c0, c1);
+        if (p.hT && (kPacked ? (borders >> (i + 1) & 1) != 0 : t + i + 1 == end)) {
           const long long q = kPacked ? sequence_of(p.cu, p.N, (int)end, (int)t + i) : row;
           store_f32(p.hT + q * p.D + c, h, vec, c0, c1);
         }
@@ -184,14 +203,22 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrParams p) {
   store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
 }
 
+template <auto kKernel, typename T>
+cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
+  const size_t smem = kStages * 2 * kTile * sizeof(T);
+  const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
+  cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
+  if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
+  return e == cudaSuccess ? launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, smem) : e;
+}
 template <typename T, int kGate, int kNorm>
 cudaError_t launch(const GlrParams& p, bool step, cudaStream_t stream) {
   if (step) {
     glr_step_kernel<T, kGate, kNorm><<<(unsigned)(((long long)p.N * p.tiles + 3) / 4), 128, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  const auto kernel = p.cu ? glr_fwd_kernel<T, kGate, kNorm, true> : glr_fwd_kernel<T, kGate, kNorm, false>;
-  return launch_clusters(kernel, glr_grid(p), 32 * p.warps, p.cluster, p, stream, kStages * 2 * 64 * 64 * sizeof(T));
+  return p.cu ? launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true>, T>(p, stream)
+              : launch_prompt<glr_fwd_kernel<T, kGate, kNorm, false>, T>(p, stream);
 }
 template <typename T, int kGate>
 cudaError_t launch_gate(const GlrParams& p, bool step, cudaStream_t stream) {

@@ -89,14 +89,17 @@ cudaError_t launch_norm(const NormParams& p, bool f32, bool fp8, cudaStream_t st
 // Gated linear recurrence: prompt, its gradient, or one token (h0 == hT, T = 1).
 enum { GLR_LOG = 0, GLR_SIGMOID = 1, GLR_RATE = 2 };    // as GDN_GLR_GATE_*
 enum { GLR_NONE = 0, GLR_LINEAR = 1, GLR_SQRT = 2 };    // as GDN_GLR_INPUT_*
-constexpr int kGlrSpan = 64, kGlrWarps = 4, kGlrMaxCluster = 8;
+constexpr int kGlrChunk = 64;                           // tokens between the states that are kept
+constexpr int kGlrFwdRun = 16, kGlrFwdWarps = 4, kGlrFwdBlocks = 4;  // tokens of a thread, warps of a block,
+constexpr int kGlrBwdRun = 8, kGlrBwdWarps = 8, kGlrBwdBlocks = 2;   // blocks an SM (bf16; one of fp32)
+constexpr int kGlrMaxCluster = 16;
 struct GlrParams {
   const void *x, *g, *dy;           // rows of D channels; dy: gradient only
   const float *rate;                // [D], GLR_RATE only
   const float *h0, *dhT, *kept;     // [N, D] or nullptr; kept: the forward's states, gradient only
   void *y, *dx, *dg;                // [tokens, D]
   float *hT, *states, *dh0;         // [N, D], [rows, chunks, D], [N, D]; nullptr for none
-  float *partial;                   // [rows * cluster, D]: sums of the rate's gradient
+  float *drate, *partial;           // [D] and [rows * cluster, D]: the rate's gradient, its blocks' sums
   const int32_t* cu;                // [N + 1] or nullptr (N rows of T tokens)
   long long x_stride, g_stride, dy_stride;  // elements from token to token
   long long chunks;                 // 64-token chunks of a row, the last one partial
@@ -107,14 +110,19 @@ struct GlrParams {
   unsigned* err;                    // device error word: bounded waits record a timeout here (set
                                     // by the launch that has them)
   int tiles;                        // of 64 channels
-  int warps, cluster;               // warps of a block, blocks of a cluster: successive tokens
+  int cluster;                      // blocks of a cluster: successive tokens (set by the launch)
 };
 inline long long glr_units(const GlrParams& p) { return (p.cu ? 1ll : p.N) * p.tiles; }
+// at most so many blocks a cluster
+inline int glr_most_blocks(const GlrParams& p) {
+  const int span = kGlrBwdRun * kGlrBwdWarps;
+  return p.T <= span ? 1 : p.T > span * (kGlrMaxCluster - 1) ? kGlrMaxCluster : (p.T - 1) / span + 1;
+}
 inline unsigned glr_grid(const GlrParams& p) { return (unsigned)(glr_units(p) * p.cluster); }
 cudaError_t launch_glr_f32(const GlrParams& p, bool step, cudaStream_t stream);
 cudaError_t launch_glr_bwd_f32(const GlrParams& p, cudaStream_t stream);
-cudaError_t launch_glr(GlrParams p, bool f32, cudaStream_t stream);
-cudaError_t launch_glr_bwd(GlrParams p, bool f32, cudaStream_t stream);
+cudaError_t launch_glr(const GlrParams& p, bool f32, cudaStream_t stream);
+cudaError_t launch_glr_bwd(const GlrParams& p, bool f32, cudaStream_t stream);
 cudaError_t launch_glr_step(const GlrParams& p, bool f32, cudaStream_t stream);
 // The sums over the rows of in [rows, D] into a, or of in [rows, 2, D] into a and b; in a fixed order.
 cudaError_t launch_column_sums(const float* in, float* a, float* b, int rows, int D, cudaStream_t stream);
