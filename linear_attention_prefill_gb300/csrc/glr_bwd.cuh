@@ -73,17 +73,17 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     if (r < rounds) {
       const unsigned first = (rounds - 1 - r) * round + rank * span;
       const int left = first < end ? (int)min(end - first, (unsigned)(kRun * kWarps)) : 0;  // rows that exist
-      const long long at = row * p.T + first;
       T* to = tiles + r % kStages * (3 * kTile);
-      copy_tile<kRun * kWarps, 32 * kWarps>(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
-      copy_tile<kRun * kWarps, 32 * kWarps>(to + kTile, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
-      copy_tile<kRun * kWarps, 32 * kWarps>(to + 2 * kTile, static_cast<const T*>(p.dy) + at * p.dy_stride + tile * 64ll, p.dy_stride, left,
-                span, cols, p.piece);
+#pragma unroll 1
+      for (int k = 0; k < 3; ++k, to += kTile) {
+        const void* from = k == 0 ? p.x : k == 1 ? p.g : p.dy;
+        const long long stride = k == 0 ? p.x_stride : k == 1 ? p.g_stride : p.dy_stride;
+        copy_tile(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
+                  p.piece);
+      }
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int r = 0; r < kStages - 1; ++r) fetch(r);
   unsigned t = (rounds - 1) * round + rank * span + warp * kRun;  // this thread's first token
   // the state before the chunk of 64 tokens that t lies in, of this round and the next; the chunk's warps
   // before this one lead on from it
@@ -94,13 +94,15 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   f32x2 before = rounds ? state_before(t) : 0ull;
   constexpr int kChunkWarps = kGlrChunk / kRun;
   if (K > 1) cluster_wait();
+  fetch(0);
+  static_assert(kStages == 2, "a round's tiles are on their way while the one before is worked on");
   for (unsigned r = 0; r < rounds; ++r, t -= round) {
     const int turn = r & 1;
     // (a block that has given up a wait neither expects nor sends: its neighbours give up, too)
     if (K > 1 && threadIdx.x == 0 && !*dead) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
-    cp_async_wait<kStages - 2>();
+    cp_async_wait<0>();
     __syncthreads();
-    fetch(r + kStages - 1);
+    fetch(r + 1);
     const T* xs = tiles + r % kStages * (3 * kTile) + warp * kRun * 64;
     const T *gs = xs + kTile, *ds = gs + kTile;
     const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist
@@ -217,16 +219,20 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       }
       m = mul2(a[i], lam);
       f32x2 d = mul2(m, slope);
-      if (kGate == GLR_SIGMOID) {
-        f32x2 sig, rest = s[i];
-        if (kNorm != GLR_LINEAR) sigmoid2(pair_at(gs, i, lane), sig, rest);
-        d = mul2(d, rest);
-      } else if (kGate == GLR_RATE) {
-        f32x2 sig, rest;
-        sigmoid2(pair_at(gs, i, lane), sig, rest);
-        d = mul2(d, sig);
-        drate = add2(drate, d);
-        d = mul2(mul2(d, rate), rest);
+      if (kGate != GLR_LOG) {
+        float g0, g1, sig0, sig1, rest0, rest1;
+        unpack2(s[i], rest0, rest1);
+        if (kGate == GLR_RATE || kNorm != GLR_LINEAR) {
+          unpack2(pair_at(gs, i, lane), g0, g1);
+          sigmoid_of(g0, sig0, rest0);
+          sigmoid_of(g1, sig1, rest1);
+        }
+        if (kGate == GLR_RATE) {
+          d = mul2(d, pack2(sig0, sig1));
+          drate = add2(drate, d);
+          d = mul2(d, rate);
+        }
+        d = mul2(d, pack2(rest0, rest1));
       }
       o.set(d);
       o.store(dg, vec, c0, c1);

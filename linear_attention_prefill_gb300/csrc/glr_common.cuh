@@ -95,56 +95,63 @@ __device__ __forceinline__ f32x2 pair_at(const T* tile, int token, int lane) {
 }
 
 // ---- tiles on their way into shared memory ---------------------------------------------------
-// Bytes of an access: 16 and 4 are asynchronous copies, 2 plain loads (odd rows of bf16).
-template <int kBytes>
-__device__ __forceinline__ void copy_piece(void* to, const void* from, bool ok) {
-  if constexpr (kBytes == 16) {
-    cp_async16(to, from, ok);
-  } else if constexpr (kBytes == 4) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(ok ? 4 : 0)
-                 : "memory");
-  } else {
-    *static_cast<uint16_t*>(to) = ok ? *static_cast<const uint16_t*>(from) : (uint16_t)0;
+// A tile of `tokens` rows of 64 channels from src, `cols` of which exist: zeros for rows
+// from `rows` on and for channels that do not exist.
+//
+// 16 bytes an asynchronous copy where rows are made of, and aligned to, them.  The others are apart from
+// the kernels' loop, and not inlined: they are rare, and the loop is to stay in the instruction cache.
+template <typename T>
+__device__ __forceinline__ void copy_wide(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
+  constexpr int kCols = 16 / (int)sizeof(T), kPieces = 64 / kCols;
+  const int row0 = threadIdx.x / kPieces, col = threadIdx.x % kPieces * kCols, step = blockDim.x / kPieces;
+  const T* from = src + row0 * stride + col;
+  const long long by = step * stride;
+  tile += row0 * 64 + col;
+#pragma unroll 4
+  for (int row = row0; row < tokens; row += step) {
+    const bool ok = col < cols && row < rows;
+    cp_async16(tile, ok ? from : src, ok);
+    from += by;
+    tile += step * 64;
   }
 }
-// Up to kTokens rows (`tokens`) of 64 channels, `cols` of which exist, from src; zeros for rows from
-// `rows` on and for channels that do not exist.
-template <int kBytes, int kTokens, int kThreads, typename T>
-__device__ __forceinline__ void copy_rows(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
-  constexpr int kCols = kBytes / (int)sizeof(T), kPieces = 64 / kCols;
-  if (kBytes == 16 && blockDim.x == kThreads && rows >= kTokens) {  // a whole tile, by a whole block
-    constexpr int kStep = kThreads / kPieces;
-    const int row = threadIdx.x / kPieces, col = threadIdx.x % kPieces * kCols;
-    const T* from = src + row * stride + col;
-    const bool ok = col < cols;
-    if (!ok) from = src;
-    const long long step = ok ? kStep * stride : 0;
-    tile += row * 64 + col;
-#pragma unroll
-    for (int i = 0; i < kTokens / kStep; ++i) {
-      copy_piece<kBytes>(tile + i * kStep * 64, from, ok);
-      from += step;
-    }
-    return;
-  }
+// 4 bytes an asynchronous copy.
+template <typename T>
+__device__ __noinline__ void copy_words(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
+  constexpr int kCols = 4 / (int)sizeof(T), kPieces = 64 / kCols;
 #pragma unroll 4
   for (int i = threadIdx.x; i < tokens * kPieces; i += blockDim.x) {
     const int row = i / kPieces, col = i % kPieces * kCols;
     const bool ok = col < cols && row < rows;
-    copy_piece<kBytes>(tile + row * 64 + col, ok ? src + row * stride + col : src, ok);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(tile + row * 64 + col)),
+                 "l"(ok ? src + row * stride + col : src), "r"(ok ? 4 : 0)
+                 : "memory");
   }
 }
-// By all threads of the block; rows are made of, and aligned to, pieces of so many bytes.
-template <int kTokens, int kThreads, typename T>
+// Odd rows of bf16: plain loads, 16 under way at a time.
+static __device__ __noinline__ void copy_halves(uint16_t* tile, const uint16_t* src, long long stride, int rows,
+                                                int tokens, int cols) {
+  for (int i = threadIdx.x; i < tokens * 64; i += 16 * blockDim.x) {
+    uint16_t v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int at = i + k * blockDim.x, row = at / 64, c = at % 64;
+      v[k] = row < rows && c < cols ? src[row * stride + c] : (uint16_t)0;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int at = i + k * blockDim.x;
+      if (at < tokens * 64) tile[at] = v[k];
+    }
+  }
+}
+// piece: bytes that rows are made of and aligned to
+template <typename T>
 __device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, int rows, int tokens, int cols,
                                           int piece) {
-  if (piece == 16) {
-    copy_rows<16, kTokens, kThreads>(tile, src, stride, rows, tokens, cols);
-  } else if (sizeof(T) == 4 || piece == 4) {
-    copy_rows<4, kTokens, kThreads>(tile, src, stride, rows, tokens, cols);
-  } else if constexpr (sizeof(T) == 2) {
-    copy_rows<2, kTokens, kThreads>(tile, src, stride, rows, tokens, cols);
-  }
+  if (piece == 16) copy_wide(tile, src, stride, rows, tokens, cols);
+  else if (sizeof(T) == 4 || piece == 4) copy_words(tile, src, stride, rows, tokens, cols);
+  else copy_halves(reinterpret_cast<uint16_t*>(tile), reinterpret_cast<const uint16_t*>(src), stride, rows, tokens, cols);
 }
 
 // ---- gates -------------------------------------------------------------------------------
@@ -159,67 +166,57 @@ __device__ __forceinline__ f32x2 each(f32x2 x, F f) {
   unpack2(x, a, b);
   return pack2(f(a), f(b));
 }
-__device__ __forceinline__ f32x2 neg2(f32x2 x) { return x ^ 0x8000000080000000ull; }
+
+// The gates are computed channel by channel: their constants are operands of scalar instructions, while
+// packed ones would need each of them in a pair of registers (8 x 2048 x 2560 training: 180 us packed,
+// GATES_US as they are).
 
 // e^u - 1 for |u| < 1/2: u times the polynomial of degree 6 with the least relative error there
 // (3.0e-9, by Remez's exchange; 1.2e-7 with the roundings).
-__device__ __forceinline__ f32x2 expm1_small(f32x2 u) {
-  f32x2 r = dup2(0.000198411915f);
-  r = fma2(r, u, dup2(0.00139973243f));
-  r = fma2(r, u, dup2(0.00833363459f));
-  r = fma2(r, u, dup2(0.0416653194f));
-  r = fma2(r, u, dup2(0.166666627f));
-  r = fma2(r, u, dup2(0.50000006f));
-  r = fma2(r, u, dup2(1.f));
-  return mul2(r, u);
-}
-__device__ __forceinline__ f32x2 rcp2(f32x2 x) {
-  return each(x, [](float v) { return rcp(v); });
-}
-__device__ __forceinline__ f32x2 exp_neg(f32x2 g) {
-  return each(mul2(g, dup2(-kLog2e)), [](float v) { return ex2(v); });
+__device__ __forceinline__ float expm1_small(float u) {
+  float r = 0.000198411915f;
+  r = fmaf(r, u, 0.00139973243f);
+  r = fmaf(r, u, 0.00833363459f);
+  r = fmaf(r, u, 0.0416653194f);
+  r = fmaf(r, u, 0.166666627f);
+  r = fmaf(r, u, 0.50000006f);
+  r = fmaf(r, u, 1.f);
+  return r * u;
 }
 // sigmoid(g) and 1 - sigmoid(g), each to its last digits: with e = e^-g and q = 1 / (1 + e) they are q and
 // e q, but what is nearer to 1 is 1 less the other.
-__device__ __forceinline__ void sigmoid2(f32x2 g, f32x2& sig, f32x2& rest) {
-  const f32x2 one = dup2(1.f), minus = dup2(-1.f), e = exp_neg(g);
-  const f32x2 nq = rcp2(fma2(e, minus, minus));  // -q
-  float e0, e1, q0, q1, p0, p1, l0, l1, r0, r1;
-  unpack2(e, e0, e1);
-  unpack2(nq, q0, q1);
-  unpack2(mul2(e, nq), p0, p1);
-  unpack2(fma2(e, nq, one), l0, l1);
-  unpack2(add2(one, nq), r0, r1);
-  sig = pack2(e0 < 1.f ? l0 : -q0, e1 < 1.f ? l1 : -q1);
-  rest = pack2(e0 < 1.f ? -p0 : r0, e1 < 1.f ? -p1 : r1);
+__device__ __forceinline__ void sigmoid_of(float g, float& sig, float& rest) {
+  const float e = ex2(-kLog2e * g), q = rcp(1.f + e);
+  const float less = e < 1.f ? e * q : q, more = 1.f - less;
+  sig = e < 1.f ? more : less;
+  rest = e < 1.f ? less : more;
 }
-
 // The decay a and the input's weight s of a token.  Decays next to 1 come from 1 - a, which keeps its
 // digits there: a then is off by one rounding, not by the error of 2^x, whose like sign over the
 // thousand tokens that such a decay remembers would show in fp32 sums.
 template <int kGate, int kNorm>
-__device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
-  const f32x2 one = dup2(1.f);
-  f32x2 left;  // 1 - a
+__device__ __forceinline__ void gate_of(float g, float rate, float& a, float& s) {
+  float left;  // 1 - a
   if (kGate == GLR_SIGMOID) {
-    sigmoid2(g, a, left);
+    sigmoid_of(g, a, left);
   } else {
-    f32x2 log = g;
-    if (kGate == GLR_RATE) log = mul2(rate, rcp2(add2(exp_neg(g), one)));
-    const f32x2 e = each(mul2(log, dup2(kLog2e)), [](float v) { return ex2(v); }), small = expm1_small(log);
-    float u0, u1, s0, s1, a0, a1, e0, e1, d0, d1;
-    unpack2(log, u0, u1);
-    unpack2(small, s0, s1);
-    unpack2(add2(one, small), a0, a1);
-    unpack2(e, e0, e1);
-    unpack2(fma2(e, dup2(-1.f), one), d0, d1);
-    const bool near0 = fabsf(u0) < 0.5f, near1 = fabsf(u1) < 0.5f;
-    a = pack2(near0 ? a0 : e0, near1 ? a1 : e1);
-    left = pack2(near0 ? -s0 : d0, near1 ? -s1 : d1);
+    const float log = kGate == GLR_LOG ? g : rate * rcp(1.f + ex2(-kLog2e * g));
+    const float e = ex2(kLog2e * log), small = expm1_small(log);
+    const bool near = fabsf(log) < 0.5f;
+    a = near ? 1.f + small : e;
+    if (kNorm != GLR_NONE) left = near ? -small : 1.f - e;
   }
-  if (kNorm == GLR_NONE) s = one;
-  if (kNorm == GLR_LINEAR) s = left;
-  if (kNorm == GLR_SQRT) s = each(fma2(left, a, left), [](float v) { return sqrt_ftz(v); });
+  s = kNorm == GLR_NONE ? 1.f : kNorm == GLR_LINEAR ? left : sqrt_ftz(fmaf(left, a, left));
+}
+template <int kGate, int kNorm>
+__device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
+  float g0, g1, r0, r1, a0, a1, s0, s1;
+  unpack2(g, g0, g1);
+  unpack2(rate, r0, r1);
+  gate_of<kGate, kNorm>(g0, r0, a0, s0);
+  gate_of<kGate, kNorm>(g1, r1, a1, s1);
+  a = pack2(a0, a1);
+  s = pack2(s0, s1);
 }
 
 // ---- stretches of time ---------------------------------------------------------------------

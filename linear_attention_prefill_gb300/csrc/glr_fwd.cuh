@@ -58,25 +58,29 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     if (r < rounds) {
       const unsigned first = r * round + rank * span;
       const int left = first < end ? (int)min(end - first, (unsigned)(kRun * kWarps)) : 0;  // rows that exist
-      const long long at = row * p.T + first;
       T* to = tiles + r % kStages * (2 * kTile);
-      copy_tile<kRun * kWarps, 32 * kWarps>(to, static_cast<const T*>(p.x) + at * p.x_stride + tile * 64ll, p.x_stride, left, span, cols, p.piece);
-      copy_tile<kRun * kWarps, 32 * kWarps>(to + kTile, static_cast<const T*>(p.g) + at * p.g_stride + tile * 64ll, p.g_stride, left, span, cols, p.piece);
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k, to += kTile) {
+        const void* from = k ? p.g : p.x;
+        const long long stride = k ? p.g_stride : p.x_stride;
+        copy_tile(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
+                  p.piece);
+      }
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int r = 0; r < kStages - 1; ++r) fetch(r);
   unsigned t = rank * span + warp * kRun;  // this thread's first token
   T* y = static_cast<T*>(p.y) + (row * p.T + t) * p.D + c;
   if (K > 1) cluster_wait();
+  fetch(0);
+  static_assert(kStages == 2, "a round's tiles are on their way while the one before is worked on");
   for (unsigned r = 0; r < rounds; ++r, t += round) {
     const int turn = r & 1;
     // (a block that has given up a wait neither expects nor sends: its neighbours give up, too)
     if (K > 1 && threadIdx.x == 0 && !*dead) mbar_expect_tx(&s_bar[turn], K * 32 * 16);
-    cp_async_wait<kStages - 2>();
+    cp_async_wait<0>();
     __syncthreads();
-    fetch(r + kStages - 1);
+    fetch(r + 1);
     const T* xs = tiles + r % kStages * (2 * kTile) + warp * kRun * 64;
     const T* gs = xs + kTile;
     const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist

@@ -91,7 +91,7 @@ enum { GLR_LOG = 0, GLR_SIGMOID = 1, GLR_RATE = 2 };    // as GDN_GLR_GATE_*
 enum { GLR_NONE = 0, GLR_LINEAR = 1, GLR_SQRT = 2 };    // as GDN_GLR_INPUT_*
 constexpr int kGlrChunk = 64;                           // tokens between the states that are kept
 constexpr int kGlrFwdRun = 16, kGlrFwdWarps = 4, kGlrFwdBlocks = 4;  // tokens of a thread, warps of a block,
-constexpr int kGlrBwdRun = 8, kGlrBwdWarps = 8, kGlrBwdBlocks = 2;   // blocks an SM (bf16; one of fp32)
+constexpr int kGlrBwdRun = 16, kGlrBwdWarps = 4, kGlrBwdBlocks = 3;   // blocks an SM (bf16; one of fp32)
 constexpr int kGlrMaxCluster = 16;
 struct GlrParams {
   const void *x, *g, *dy;           // rows of D channels; dy: gradient only
