@@ -137,11 +137,13 @@ struct LnParams {
   long long rows, x_stride, dy_stride;
   int D;
   int blocks, slice;                // blocks of a row (1, 2 or 4), columns of each
-  int by;                           // columns of an access (8, 4, 2, 1): D is a multiple, all are aligned
+  int whole;                        // vectors of 8 columns: D is a multiple, all are 16 bytes aligned
   float eps, inv_d;
+  unsigned* err;                    // device error word: bounded waits record a timeout here (set
+                                    // by the launch that has them)
 };
-constexpr int kLnMaxD = 32768, kLnMaxThreads = 512, kLnSlice = 16 * kLnMaxThreads;
-inline int ln_partials(int D) { return (D <= 512 ? 8 : 2) * kSms; }
+constexpr int kLnMaxD = 32768, kLnMaxThreads = 1024, kLnSlice = 8 * kLnMaxThreads;
+inline int ln_partials(int D) { return (D <= 2560 ? 8 : 2) * kSms; }
 cudaError_t launch_layer_norm(const LnParams& p, bool f32, cudaStream_t stream);
 cudaError_t launch_layer_norm_bwd(const LnParams& p, bool f32, cudaStream_t stream);
 

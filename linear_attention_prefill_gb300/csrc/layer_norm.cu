@@ -11,13 +11,13 @@
 namespace gdn {
 namespace {
 
-template <typename T, bool kWhole, int G, int NV>
-__global__ void __launch_bounds__(G ? 128 : kLnMaxThreads) ln_fwd_kernel(const LnParams p) {
+template <typename T, bool kWhole, int G, int NV, int kThreads>
+__global__ void __launch_bounds__(kThreads) ln_fwd_kernel(const LnParams p) {
   __shared__ LnShared s;
+  __shared__ __align__(16) float scratch[kWhole ? 4 : kThreads * 8];
   const unsigned blocks = G ? 1 : p.blocks, rank = !G && blocks > 1 ? cluster_rank() : 0;
   if (!G && blocks > 1) cluster_arrive();
-  const LnColumns<G, NV> col(p, rank);
-  const int by = kWhole ? 8 : p.by, step = LnColumns<G, NV>::step() * 8;
+  const LnColumns<kWhole, G, NV> col(p, rank, scratch);
   const long long per_block = G ? 128 / (G ? G : 1) : 1;
   const long long rows = (long long)(gridDim.x / blocks) * per_block;
   const long long row0 = blockIdx.x / blocks * per_block + (G ? threadIdx.x / (G ? G : 1) : 0);
@@ -26,79 +26,169 @@ __global__ void __launch_bounds__(G ? 128 : kLnMaxThreads) ln_fwd_kernel(const L
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[i][j] = dup2(1.f), b[i][j] = 0ull;
-    if (col.n[i] <= 0) continue;
-    if (p.w) pairs_of(load8(p.w + col.first + i * step, col.n[i], by), w[i]);
-    if (p.b) pairs_of(load8(p.b + col.first + i * step, col.n[i], by), b[i]);
+    if (p.w) col.vector(col.load(p.w, i), i, w[i]);
+    if (p.b) col.vector(col.load(p.b, i), i, b[i]);
   }
   Raw8<T> x[NV], res[NV];
   auto load = [&](long long row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (col.n[i] <= 0) continue;
-      x[i] = load8(static_cast<const T*>(p.x) + row * p.x_stride + col.first + i * step, col.n[i], by);
-      if (p.residual)
-        res[i] = load8(static_cast<const T*>(p.residual) + row * p.D + col.first + i * step, col.n[i], by);
+      x[i] = col.load(static_cast<const T*>(p.x) + row * p.x_stride, i);
+      if (p.residual) res[i] = col.load(static_cast<const T*>(p.residual) + row * p.D, i);
     }
   };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i].zero(), res[i].zero();
   if (row0 < p.rows) load(row0);
   int turn = 0;
   if (!G && blocks > 1) cluster_wait();
   // every lane of a warp stays for the sums
   for (long long row = row0; row - (G ? threadIdx.x / (G ? G : 1) : 0) < p.rows; row += rows) {
     const bool some = row < p.rows;
-    f32x2 r[NV][4], sum = 0ull;
+    f32x2 r[NV][4];
+    float v[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!some || col.n[i] <= 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[i][j] = 0ull;
-        continue;
-      }
-      pairs_of(x[i], r[i]);
+      col.vector(x[i], i, r[i]);
       if (p.residual) {
         f32x2 q[4];
-        pairs_of(res[i], q);
+        col.vector(res[i], i, q);
 #pragma unroll
         for (int j = 0; j < 4; ++j) r[i][j] = add2(r[i][j], q[j]);
-        store8(static_cast<T*>(p.residual_out) + row * p.D + col.first + i * step, raw_of<T>(r[i]), col.n[i], by);
+        col.store(static_cast<T*>(p.residual_out) + row * p.D, i, r[i], some);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum = add2(sum, r[i][j]);
+      v[0] += sum8(r[i]);
     }
     if (row + rows < p.rows) load(row + rows);
-    float v[1] = {both(sum)};
     sum_row<G>(v, &s, turn, blocks);
     const f32x2 mean = dup2(-v[0] * p.inv_d);
-    sum = 0ull;
+    v[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!some || col.n[i] <= 0) continue;
+      f32x2 sum = 0ull;
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[i][j] = add2(r[i][j], mean);
-      mask<kWhole>(r[i], col.n[i]);
+      col.mask(r[i], i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) sum = fma2(r[i][j], r[i][j], sum);
+      v[0] += both(sum);
     }
-    v[0] = both(sum);
     sum_row<G>(v, &s, turn, blocks);
     const f32x2 rstd = dup2(rsqrtf(v[0] * p.inv_d + p.eps));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (!some || col.n[i] <= 0) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) r[i][j] = fma2(mul2(r[i][j], rstd), w[i][j], b[i][j]);
-      store8(static_cast<T*>(p.y) + row * p.D + col.first + i * step, raw_of<T>(r[i]), col.n[i], by);
+      col.store(static_cast<T*>(p.y) + row * p.D, i, r[i], some);
     }
   }
 }
 
-template <typename T, bool kWhole, int G, int NV>
+// Many whole rows, through the ring.
+template <typename T, int kRows>
+__global__ void __launch_bounds__(1024) ln_fwd_ring_kernel(const LnParams p, const LnRing shape) {
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ uint64_t full[kLnRingSlots];
+  __shared__ int s_lost;
+  __shared__ LnShared s;
+  LnFeed<T, 1> feed{p, ring, full, shape};
+  const int c = threadIdx.x * 8;
+  const bool here = c < p.D;
+  f32x2 w[4], b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = dup2(1.f), b[j] = 0ull;
+  if (here && p.w) pairs_of(load8(p.w + c, 8, 8), w);
+  if (here && p.b) pairs_of(load8(p.b + c, 8, 8), b);
+  if (threadIdx.x == 0) s_lost = 0, feed.start();
+  __syncthreads();
+  int slot = 0, turn = 0;
+  unsigned phase = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += (long long)kRows * gridDim.x) {
+    f32x2 r[kRows][4];
+    float v[kRows];
+    int from[kRows];
+    bool lost = false;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long at = row + (long long)k * gridDim.x;
+      v[k] = 0.f;
+      from[k] = slot;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[k][j] = 0ull;
+      if (at >= p.rows) continue;
+      lost = lost || !mbar_wait(&full[slot], phase, p.err);
+      if (here) {
+        const T* in = feed.row_of(slot) + c;
+        Raw8<T> x;
+        x.load(in);
+        pairs_of(x, r[k]);
+        if (p.residual) {
+          f32x2 q[4];
+          x.load(in + p.D);
+          pairs_of(x, q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[k][j] = add2(r[k][j], q[j]);
+          raw_of<T>(r[k]).store(static_cast<T*>(p.residual_out) + at * p.D + c);
+        }
+        v[k] = sum8(r[k]);
+      }
+      if (++slot == shape.slots) slot = 0, phase ^= 1;
+    }
+    if (lost) s_lost = 1;
+    sum_block(v, &s, turn);
+    // a copy that does not arrive within about a second is recorded, and ends the block's work (the sum's
+    // barrier tells all threads) once the other copies in flight have arrived
+    if (s_lost) {
+      feed.drain(row, kRows, slot, phase);
+      return;
+    }
+    if (threadIdx.x == 0) {  // every thread has read the slots
+      fence_proxy_async();
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) feed.fetch(row + ((long long)k + shape.slots) * gridDim.x, from[k]);
+    }
+    float q[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const f32x2 mean = dup2(-v[k] * p.inv_d);
+      f32x2 sum = 0ull;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[k][j] = add2(r[k][j], mean);
+        sum = fma2(r[k][j], r[k][j], sum);
+      }
+      q[k] = here ? both(sum) : 0.f;
+    }
+    sum_block(q, &s, turn);
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long at = row + (long long)k * gridDim.x;
+      if (at >= p.rows || !here) continue;
+      const f32x2 rstd = dup2(rsqrtf(q[k] * p.inv_d + p.eps));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r[k][j] = fma2(mul2(r[k][j], rstd), w[j], b[j]);
+      raw_of<T>(r[k]).store(static_cast<T*>(p.y) + at * p.D + c);
+    }
+  }
+}
+
+template <typename T, bool kWhole, int G, int NV, int kThreads = 128>
 cudaError_t launch(const LnParams& p, cudaStream_t stream) {
   const int threads = G ? 128 : ((p.slice + 8 * NV - 1) / (8 * NV) + 31) / 32 * 32;
   unsigned grid;
-  const auto kernel = ln_fwd_kernel<T, kWhole, G, NV>;
-  const cudaError_t e = ln_grid(kernel, p, G, threads, &grid);
-  return e == cudaSuccess ? launch_clusters(kernel, grid, threads, p.blocks, p, stream) : e;
+  const cudaError_t e = ln_grid<ln_fwd_kernel<T, kWhole, G, NV, kThreads>>(p, G, threads, &grid);
+  return e == cudaSuccess ? launch_clusters(ln_fwd_kernel<T, kWhole, G, NV, kThreads>, grid, threads, p.blocks, p, stream) : e;
+}
+template <typename T, int kRows>
+cudaError_t launch_ring(LnParams p, const LnRing& shape, cudaStream_t stream) {
+  const auto kernel = ln_fwd_ring_kernel<T, kRows>;
+  const int threads = (p.D / 8 + 31) / 32 * 32, smem = shape.slots * shape.slot_bytes;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = device_error_word(&p.err);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)shape.blocks * kSms;
+  kernel<<<(unsigned)(p.rows < most ? p.rows : most), threads, smem, stream>>>(p, shape);
+  return cudaGetLastError();
 }
 template <typename T, bool kWhole>
 cudaError_t launch_t(const LnParams& p, cudaStream_t stream) {
@@ -106,14 +196,20 @@ cudaError_t launch_t(const LnParams& p, cudaStream_t stream) {
   if (p.D <= 128) return launch<T, kWhole, 16, 1>(p, stream);
   if (p.D <= 256) return launch<T, kWhole, 32, 1>(p, stream);
   if (p.D <= 512) return launch<T, kWhole, 32, 2>(p, stream);
-  return p.slice <= 8 * kLnMaxThreads ? launch<T, kWhole, 0, 1>(p, stream) : launch<T, kWhole, 0, 2>(p, stream);
+  if (kWhole && p.blocks == 1 && p.rows >= kLnRingRows) {
+    const LnRing shape = ln_ring<T>(p, p.residual ? 2 : 1);
+    if (shape.slots >= 4) return launch_ring<T, 2>(p, shape, stream);
+    return launch_ring<T, 1>(p, shape, stream);
+  }
+  if (p.slice <= 8 * 512) return launch<T, kWhole, 0, 1, 512>(p, stream);
+  return launch<T, kWhole, 0, 1, kLnMaxThreads>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_layer_norm(const LnParams& p, bool f32, cudaStream_t stream) {
-  if (f32) return p.by == 8 ? launch_t<float, true>(p, stream) : launch_t<float, false>(p, stream);
-  return p.by == 8 ? launch_t<__nv_bfloat16, true>(p, stream) : launch_t<__nv_bfloat16, false>(p, stream);
+  if (f32) return p.whole ? launch_t<float, true>(p, stream) : launch_t<float, false>(p, stream);
+  return p.whole ? launch_t<__nv_bfloat16, true>(p, stream) : launch_t<__nv_bfloat16, false>(p, stream);
 }
 
 }  // namespace gdn

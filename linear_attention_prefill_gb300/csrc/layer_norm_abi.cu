@@ -18,18 +18,14 @@ gdn_status check(const void* x, long long rows, int D, long long x_stride, float
   return gdn::check_rows("x", x, rows, x_stride, D, elem);
 }
 
-// The widest accesses that every tensor allows: of 8, 4 or 2 columns, 16 bytes at most.
-int widest(const LnParams& p, int elem) {
-  for (int by = 8; by > 1; by /= 2) {
-    const size_t wide = by * elem < 16 ? by * elem : 16, of_w = by * 4 < 16 ? by * 4 : 16;
-    bool ok = p.D % by == 0 && aligned(p.w, of_w) && aligned(p.b, of_w);
-    for (const void* q : {p.x, p.dy, p.residual, (const void*)p.y, (const void*)p.residual_out})
-      ok = ok && aligned(q, wide);
-    for (const long long s : {p.x_stride, p.dy_stride})
-      ok = ok && (p.rows <= 1 || s * elem % (long long)wide == 0);
-    if (ok) return by;
-  }
-  return 1;
+// Whether rows are made of vectors of 8 columns, 16 bytes aligned in every tensor.
+int whole(const LnParams& p, int elem) {
+  bool ok = p.D % 8 == 0;
+  for (const void* q : {p.x, p.dy, p.residual, (const void*)p.y, (const void*)p.residual_out, (const void*)p.w,
+                        (const void*)p.b})
+    ok = ok && aligned(q, 16);
+  for (const long long s : {p.x_stride, p.dy_stride}) ok = ok && (p.rows <= 1 || s * elem % 16 == 0);
+  return ok;
 }
 // Blocks of a row, and the columns of each (whole vectors of 8).
 void cut(LnParams* p) {
@@ -61,7 +57,7 @@ gdn_status forward(const void* x, const float* w, const float* b, const void* re
   p.x = x; p.w = w; p.b = b; p.residual = residual; p.y = y; p.residual_out = residual_out;
   p.rows = rows; p.x_stride = x_stride; p.D = D; p.eps = eps;
   cut(&p);
-  p.by = widest(p, elem);
+  p.whole = whole(p, elem);
   const cudaError_t e = gdn::launch_layer_norm(p, f32, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the layer norm");
 }
@@ -95,7 +91,7 @@ gdn_status backward(const void* dy, const void* x, const float* w, const void* d
   p.x = x; p.dy = dy; p.w = w; p.residual = dres; p.y = dx; p.dw = dw; p.db = db;
   p.rows = rows; p.x_stride = x_stride; p.dy_stride = dy_stride; p.D = D; p.eps = eps;
   cut(&p);
-  p.by = widest(p, elem);
+  p.whole = whole(p, elem);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t need = dw ? partial_bytes(rows, D) : 0;
   void* pool = nullptr;

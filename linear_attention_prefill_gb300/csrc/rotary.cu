@@ -71,16 +71,16 @@ __device__ __forceinline__ bool position_of(const RotaryParams& p, long long tok
 }
 
 // blockDim.x threads of a head: R / 2 / V of them have V pairs each, the others 2 V columns that are
-// passed through; blockDim.y heads at a time.
-constexpr int kRotaryThreads = 256, kAhead = 4;
+// passed through.  blockDim.y is the block's tokens times some heads of each: a thread stays with its
+// token, whose cosines and sines it keeps, and takes every so many of its heads, kAhead loads ahead.
+constexpr int kRotaryThreads = 256, kAhead = 4, kMinBlocks = 3;
 template <typename T, int V, bool kNext>
-__global__ void __launch_bounds__(V > 1 ? 256 : 512) rotary_kernel(const RotaryParams p) {
-  extern __shared__ float2 s_turn[];  // [tokens of the block][R / 2]: m cos, m sin
+__global__ void __launch_bounds__(V > 1 ? 256 : 512, V > 1 ? kMinBlocks : 1) rotary_kernel(const RotaryParams p) {
+  extern __shared__ __align__(16) float2 s_turn[];  // [tokens of the block][R / 2]: m cos, m sin
   const int half = p.R / 2, pairs = half / V;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
   const long long token0 = (long long)blockIdx.x * p.block_tokens;
   const int here = (int)min((long long)p.block_tokens, p.tokens - token0);
-  const int heads = p.Hq + p.Hk, units = here * heads;
   const bool rotates = (int)threadIdx.x < pairs;
   // the thread's two pieces of a head
   const int rest = p.R + ((int)threadIdx.x - pairs) * 2 * V;
@@ -88,29 +88,29 @@ __global__ void __launch_bounds__(V > 1 ? 256 : 512) rotary_kernel(const RotaryP
   const int at1 = rotates ? (kNext ? at0 + V : at0 + half) : rest + V;
   const bool two = rotates || at1 < p.D;
   const long long end = p.cu && !p.positions ? min((long long)p.cu[p.N], p.tokens) : p.tokens;
+  const int mine = threadIdx.y % p.block_tokens, step = blockDim.y / p.block_tokens;
+  const long long t = token0 + mine;
+  const int heads = mine < here && t < end ? p.Hq + p.Hk : 0;
 
+  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
+  const T* k = static_cast<const T*>(p.k) + t * p.k_stride - (long long)p.Hq * p.D;
+  T* q_out = static_cast<T*>(p.q_out) + t * p.q_out_stride;
+  T* k_out = static_cast<T*>(p.k_out) + t * p.k_out_stride - (long long)p.Hq * p.D;
+  // passed through in place already
+  const auto moves = [&](int h) { return h < heads && (rotates || !(h < p.Hq ? p.q_same : p.k_same)); };
   Piece<T, V> a[kAhead], b[kAhead];
-  T* out[kAhead];
-  int token[kAhead];
-  auto load = [&](int unit, int i) {  // piece pair i: `unit` counts heads of the block's tokens
-    out[i] = nullptr;
-    if (unit >= units) return;
-    token[i] = unit / heads;
-    int h = unit - token[i] * heads;
-    const long long t = token0 + token[i];
-    if (t >= end) return;
-    const bool of_k = h >= p.Hq;
-    if (of_k) h -= p.Hq;
-    if (!rotates && (of_k ? p.k_same : p.q_same)) return;  // in place already
-    const T* x = of_k ? static_cast<const T*>(p.k) + t * p.k_stride : static_cast<const T*>(p.q) + t * p.q_stride;
-    T* o = of_k ? static_cast<T*>(p.k_out) + t * p.k_out_stride : static_cast<T*>(p.q_out) + t * p.q_out_stride;
-    x += (long long)h * p.D;
-    out[i] = o + (long long)h * p.D;
-    a[i].load(x + at0);
-    if (two) b[i].load(x + at1);
-  };
+  const auto load = [&](int first) {
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(threadIdx.y + i * blockDim.y, i);
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = first + i * step;
+      if (!moves(h)) continue;
+      const T* x = (h < p.Hq ? q : k) + (long long)h * p.D;
+      a[i].load(x + at0);
+      if (two) b[i].load(x + at1);
+    }
+  };
+  int h0 = threadIdx.y / p.block_tokens;
+  load(h0);
   for (int i = tid; i < here * half; i += threads) {
     const int j = i / half;
     long long at = 0;
@@ -124,12 +124,16 @@ __global__ void __launch_bounds__(V > 1 ? 256 : 512) rotary_kernel(const RotaryP
     s_turn[i] = cs;
   }
   __syncthreads();
-  for (int unit = threadIdx.y;;) {
+  float2 cs[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) cs[j] = rotates ? s_turn[mine * half + threadIdx.x * V + j] : make_float2(1.f, 0.f);
+  while (h0 < heads) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (!out[i]) continue;
+      const int h = h0 + i * step;
+      if (!moves(h)) continue;
+      T* out = (h < p.Hq ? q_out : k_out) + (long long)h * p.D;
       if (rotates) {
-        const float2* cs = s_turn + token[i] * half + threadIdx.x * V;
         float x[V], y[V], u[V], v[V];
         a[i].get(x);
         b[i].get(y);
@@ -151,34 +155,33 @@ __global__ void __launch_bounds__(V > 1 ? 256 : 512) rotary_kernel(const RotaryP
         a[i].set(u);
         b[i].set(v);
       }
-      a[i].store(out[i] + at0);
-      if (two) b[i].store(out[i] + at1);
+      a[i].store(out + at0);
+      if (two) b[i].store(out + at1);
     }
-    unit += kAhead * blockDim.y;
-    if (unit >= units) break;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(unit + i * blockDim.y, i);
+    h0 += kAhead * step;
+    load(h0);
   }
 }
 
 template <typename T, int V>
 cudaError_t launch(RotaryParams p, cudaStream_t stream) {
   const int half = p.R / 2, heads = p.Hq + p.Hk;
-  const int x = half / V + (p.D - p.R + 2 * V - 1) / (2 * V);
-  int y = kRotaryThreads / x;
-  if (y < 1) y = 1;
-  // a few tokens a block, so that each thread makes about one turn, but no fewer than two blocks an SM
-  long long tokens = kRotaryThreads / half;
+  const int x = half / V + (p.D - p.R + 2 * V - 1) / (2 * V), rows = kRotaryThreads / x > 1 ? kRotaryThreads / x : 1;
+  // a thread has about kAhead heads, the block as many tokens as that leaves room for; but for fewer
+  // tokens than two blocks an SM would have, a token a block with all its rows of threads
+  int step = (heads + kAhead - 1) / kAhead;
+  if (step > rows || p.tokens < 2 * kSms) step = rows < heads ? rows : heads;
+  long long tokens = rows / step;
   if (tokens > p.tokens / (2 * kSms)) tokens = p.tokens / (2 * kSms);
   if (tokens < 1) tokens = 1;
   p.block_tokens = (int)tokens;
-  if (y > tokens * heads) y = (int)tokens * heads;
   const long long grid = (p.tokens + tokens - 1) / tokens;
   const size_t smem = (size_t)tokens * half * sizeof(float2);
+  const dim3 block(x, (unsigned)(tokens * step));
   if (p.interleaved)
-    rotary_kernel<T, V, true><<<(unsigned)grid, dim3(x, y), smem, stream>>>(p);
+    rotary_kernel<T, V, true><<<(unsigned)grid, block, smem, stream>>>(p);
   else
-    rotary_kernel<T, V, false><<<(unsigned)grid, dim3(x, y), smem, stream>>>(p);
+    rotary_kernel<T, V, false><<<(unsigned)grid, block, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
