@@ -14,6 +14,9 @@
 // read once, dx and dg written once: HBM bandwidth bounds it.  Where s = 0 (a = 1 exactly) the weight
 // has no derivative; its share is left out.
 //
+// A product that goes on into a sum is written as one operation: the compiler joins packed ones of its own, in
+// one kernel and not in another, and the same call on other alignments would have other last bits.
+//
 // drate is summed by threads over their tokens, then over warps, blocks and rows in a fixed order.
 #pragma once
 
@@ -24,7 +27,8 @@ namespace {
 
 // Two rounds' tiles: three would leave two blocks an SM instead of three.
 constexpr int kMinBlocks = kGlrBwdBlocks, kStages = 2, kRun = kGlrBwdRun, kWarps = kGlrBwdWarps;
-constexpr int kTile = kRun * kWarps * 64;  // of a tensor's tokens in shared memory
+template <typename T, bool kGeneral>
+constexpr int kTileOf = kRun * kWarps * kPitch<T, kGeneral>;  // of a tensor's tokens in shared memory
 
 // lambda of a sequence's last token without what comes from behind: dy + dhT
 __device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end, int t, long long c, bool c0,
@@ -33,11 +37,11 @@ __device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end
   return add2(dy, load_f32(p.dhT + (long long)sequence_of(p.cu, p.N, end, t) * p.D + c, p.vec, c0, c1));
 }
 
-template <typename T, int kGate, int kNorm, bool kPacked>
+template <typename T, int kGate, int kNorm, bool kGeneral>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) glr_bwd_kernel(const GlrParams p) {
-  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][tokens][64 channels]
+  constexpr int kTile = kTileOf<T, kGeneral>;
+  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][tokens][64 channels and padding]
   __shared__ ulonglong2 s_ahead[2][kWarps][32], s_back[2][kWarps][32];
-  __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
   volatile int* const dead = &s_dead;
@@ -57,17 +61,24 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   const unsigned unit = blockIdx.x / K;
   const long long row = unit / p.tiles;
   const int tile = (int)(unit - (unsigned)row * p.tiles);
-  const bool vec = p.vec;
+  const bool vec = !kGeneral || p.vec;
   const long long c = (long long)tile * 64 + 2 * lane;
   const bool c0 = c < p.D, c1 = c + 1 < p.D;
-  const unsigned end = kPacked ? min(max(p.cu[p.N], 0), p.T) : p.T;
+  const Places at = places<kGeneral>(vec, c0, c1);
+  __shared__ int32_t s_cu[kGeneral ? kBorders : 1];
+  const bool packed = kGeneral && p.cu;
+  const int32_t* cu = kGeneral ? take_borders(p, s_cu) : nullptr;
+  const unsigned end = packed ? min(max(p.cu[p.N], 0), p.T) : p.T;
   const unsigned span = warps * kRun, round = K * span;
   const unsigned rounds = end ? (end - 1) / round + 1 : 0;
   const f32x2 rate = kGate == GLR_RATE ? load_f32(p.rate + c, vec, c0, c1) : 0ull;
-  f32x2 carry = !kPacked && p.dhT ? load_f32(p.dhT + row * p.D + c, vec, c0, c1) : 0ull;
+  f32x2 carry = !packed && p.dhT ? load_f32(p.dhT + row * p.D + c, vec, c0, c1) : 0ull;
   f32x2 drate = 0ull;
 
   T* tiles = reinterpret_cast<T*>(s_tiles);
+  // behind them, of a cluster: [2][K blocks][32]
+  ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 3 * kTile);
+  const bool odd = kGeneral && sizeof(T) == 2 && p.piece == 2;
   const int cols = (int)min(64ll, p.D - (long long)tile * 64);
   const auto fetch = [&](unsigned r) {  // round r, counted from the last tokens, into its stage
     if (r < rounds) {
@@ -78,7 +89,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       for (int k = 0; k < 3; ++k, to += kTile) {
         const void* from = k == 0 ? p.x : k == 1 ? p.g : p.dy;
         const long long stride = k == 0 ? p.x_stride : k == 1 ? p.g_stride : p.dy_stride;
-        copy_tile(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
+        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
                   p.piece);
       }
     }
@@ -103,62 +114,83 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     cp_async_wait<0>();
     __syncthreads();
     fetch(r + 1);
-    const T* xs = tiles + r % kStages * (3 * kTile) + warp * kRun * 64;
+    const T* xs = tiles + r % kStages * (3 * kTile) + warp * kRun * kPitch<T, kGeneral>;
     const T *gs = xs + kTile, *ds = gs + kTile;
     const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist
-    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t, kRun) : 0u;
+    const unsigned xsodd = odd && n ? odd_rows(static_cast<const T*>(p.x) + (row * p.T + t) * p.x_stride + tile * 64ll, p.x_stride) : 0u;
+    const unsigned gsodd = odd && n ? odd_rows(static_cast<const T*>(p.g) + (row * p.T + t) * p.g_stride + tile * 64ll, p.g_stride) : 0u;
+    const unsigned dsodd = odd && n ? odd_rows(static_cast<const T*>(p.dy) + (row * p.T + t) * p.dy_stride + tile * 64ll, p.dy_stride) : 0u;
+    const unsigned borders = packed && n ? borders_of(cu, p.N, (int)end, (int)t, kRun) : 0u;
     f32x2 h = before;
     if (r + 1 < rounds) before = state_before(t - round);
+    // A run of as many tokens as there can be without a border is worked on without any check between them.
+    const bool plain = n == kRun && !(kGeneral && borders);
     f32x2 a[kRun], s[kRun];
-    f32x2 A = dup2(1.f), H = 0ull;
+    f32x2 A = dup2(1.f), H = 0ull, M = 0ull;
     bool cut = false;
+    if (plain) {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      gate2<kGate, kNorm>(pair_at(gs, i, lane), rate, a[i], s[i]);
-      const f32x2 x = pair_at(xs, i, lane), b = kNorm == GLR_NONE ? x : mul2(s[i], x);
-      if (kPacked && borders >> i & 1) {
-        f32x2 first = 0ull;
-        if (p.h0 && i < n)
-          first = load_f32(p.h0 + (long long)sequence_of(p.cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
-        H = fma2(a[i], first, b);
-        cut = true;
-      } else {
-        H = fma2(a[i], H, b);
+      for (int i = 0; i < kRun; ++i) {
+        gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s[i]);
+        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
+        H = fma2(a[i], H, kNorm == GLR_NONE ? x : mul2(s[i], x));
         A = mul2(A, a[i]);
       }
-    }
-    s_ahead[turn][warp][lane] = make_ulonglong2(kPacked && cut ? 0ull : at_least_tiny(A), H);
-    // backwards: m before these tokens from m behind them; tokens that do not exist pass it on
-    const bool same = !kPacked && n == kRun;  // (then the decays' product is the one forwards)
-    if (!same) A = dup2(1.f);
-    f32x2 M = 0ull;
-    cut = false;
+      A = at_least_tiny(A);
+      s_ahead[turn][warp][lane] = make_ulonglong2(A, H);
+      // backwards: m before these tokens from m behind them
+      f32x2 lam = pair_at<kGeneral>(ds, kRun - 1, lane, dsodd);
 #pragma unroll
-    for (int i = kRun - 1; i >= 0; --i) {
-      const f32x2 dy = pair_at(ds, i, lane);
-      if (i >= n) {
-        a[i] = dup2(1.f);
-      } else if (kPacked && borders >> (i + 1) & 1) {
-        M = mul2(a[i], with_last(p, dy, (int)end, (int)t + i, c, c0, c1));
-        cut = true;
-        continue;
+      for (int i = kRun - 2; i >= 0; --i) lam = fma2(a[i + 1], lam, pair_at<kGeneral>(ds, i, lane, dsodd));
+      M = mul2(a[0], lam);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s[i]);
+        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd), b = kNorm == GLR_NONE ? x : mul2(s[i], x);
+        if (kGeneral && borders >> i & 1) {
+          f32x2 first = 0ull;
+          if (p.h0 && i < n)
+            first = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
+          H = fma2(a[i], first, b);
+          cut = true;
+        } else {
+          H = fma2(a[i], H, b);
+          A = mul2(A, a[i]);
+        }
       }
-      M = mul2(a[i], add2(dy, M));
-      if (!same) A = mul2(A, a[i]);
+      s_ahead[turn][warp][lane] = make_ulonglong2(cut ? 0ull : at_least_tiny(A), H);
+      // (tokens that do not exist pass m on)
+      A = dup2(1.f);
+      cut = false;
+      f32x2 lam = 0ull;
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) {
+        const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
+        lam = i + 1 < kRun ? fma2(a[(i + 1) % kRun], lam, dy) : dy;
+        if (i >= n) {
+          a[i] = dup2(1.f);
+        } else if (kGeneral && borders >> (i + 1) & 1) {
+          lam = with_last(p, dy, (int)end, (int)t + i, c, c0, c1);
+          cut = true;
+        }
+        A = mul2(A, a[i]);
+      }
+      M = mul2(a[0], lam);
+      A = cut ? 0ull : at_least_tiny(A);
     }
-    A = kPacked && cut ? 0ull : at_least_tiny(A);
     s_back[turn][warp][lane] = make_ulonglong2(A, M);
     __syncthreads();
     for (int w = warp / kChunkWarps * kChunkWarps; w < warp; ++w) {
       const ulonglong2 v = s_ahead[turn][w][lane];
-      h = through<kPacked>(v.x, v.y, h);
+      h = through<kGeneral>(v.x, v.y, h);
     }
     f32x2 sA = dup2(1.f), sM = 0ull;
     const auto lead = [&](int from, int to) {  // warps from - 1 down to `to`
 #pragma unroll 4
       for (int w = from - 1; w >= to; --w) {
         const ulonglong2 v = s_back[turn][w][lane];
-        follow<kPacked>(sA, sM, v.x, v.y);
+        follow<kGeneral>(sA, sM, v.x, v.y);
       }
     };
     lead(warps, warp + 1);
@@ -167,15 +199,15 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     f32x2 m = carry;
     if (K > 1) {
       if (!*dead) {
-        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], k, sA, sM);
+        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sA, sM);
       }
       wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
       f32x2 now = carry;
       const auto pass = [&](int from, int to) {
 #pragma unroll 4
         for (int k = from - 1; k >= to; --k) {
-          const ulonglong2 v = s_rank[turn][k][lane];
-          now = through<kPacked>(v.x, v.y, now);
+          const ulonglong2 v = s_rank[(turn * K + k) * 32 + lane];
+          now = through<kGeneral>(v.x, v.y, now);
         }
       };
       pass((int)K, (int)rank + 1);
@@ -183,33 +215,14 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       pass((int)rank + 1, 0);
       carry = now;
     } else {
-      carry = through<kPacked>(sA, sM, carry);
+      carry = through<kGeneral>(sA, sM, carry);
     }
-    m = through<kPacked>(A, M, m);
-    f32x2 hp[kRun];  // the state before each token
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      if (kPacked && borders >> i & 1) {
-        h = 0ull;
-        if (p.h0 && i < n)
-          h = load_f32(p.h0 + (long long)sequence_of(p.cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
-      }
-      hp[i] = h;
-      const f32x2 x = pair_at(xs, i, lane);
-      h = fma2(a[i], h, kNorm == GLR_NONE ? x : mul2(s[i], x));
-    }
+    m = through<kGeneral>(A, M, m);
     T* dx = static_cast<T*>(p.dx) + (row * p.T + t + kRun) * p.D + c;
     T* dg = static_cast<T*>(p.dg) + (row * p.T + t + kRun) * p.D + c;
-#pragma unroll
-    for (int i = kRun - 1; i >= 0; --i) {
-      dx -= p.D, dg -= p.D;
-      if (i >= n) continue;
-      const f32x2 x = pair_at(xs, i, lane), dy = pair_at(ds, i, lane);
-      const f32x2 lam = kPacked && borders >> (i + 1) & 1 ? with_last(p, dy, (int)end, (int)t + i, c, c0, c1)
-                                                          : add2(dy, m);
-      Raw2<T> o;
-      o.set(kNorm == GLR_NONE ? lam : mul2(s[i], lam));
-      o.store(dx, vec, c0, c1);
+    f32x2 hp[kRun], lam = 0ull;  // the state before each token; lambda
+    const auto token = [&](int i, f32x2 x) {
+      store_out<kGeneral>(dx, kNorm == GLR_NONE ? lam : mul2(s[i], lam), at);
       // dL / (a lambda): h_{t-1} and the weight's share
       f32x2 slope = hp[i];
       if (kNorm == GLR_LINEAR) slope = fma2(x, dup2(-1.f), slope);
@@ -223,22 +236,56 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
         float g0, g1, sig0, sig1, rest0, rest1;
         unpack2(s[i], rest0, rest1);
         if (kGate == GLR_RATE || kNorm != GLR_LINEAR) {
-          unpack2(pair_at(gs, i, lane), g0, g1);
+          unpack2(pair_at<kGeneral>(gs, i, lane, gsodd), g0, g1);
           sigmoid_of(g0, sig0, rest0);
           sigmoid_of(g1, sig1, rest1);
         }
         if (kGate == GLR_RATE) {
-          d = mul2(d, pack2(sig0, sig1));
-          drate = add2(drate, d);
-          d = mul2(d, rate);
+          drate = fma2(d, pack2(sig0, sig1), drate);
+          d = mul2(mul2(d, pack2(sig0, sig1)), rate);
         }
         d = mul2(d, pack2(rest0, rest1));
       }
-      o.set(d);
-      o.store(dg, vec, c0, c1);
-      if (kPacked ? borders >> i & 1 : t + i == 0) {
-        if (p.dh0) {
-          const long long q = kPacked ? sequence_of(p.cu, p.N, (int)end, (int)t + i) : row;
+      store_out<kGeneral>(dg, d, at);
+    };
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        hp[i] = h;
+        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
+        h = fma2(a[i], h, kNorm == GLR_NONE ? x : mul2(s[i], x));
+      }
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) {
+        dx -= p.D, dg -= p.D;
+        const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
+        lam = i + 1 == kRun ? add2(dy, m) : fma2(a[(i + 1) % kRun], lam, dy);
+        token(i, pair_at<kGeneral>(xs, i, lane, xsodd));
+      }
+      if (p.dh0 && !packed && t == 0) store_f32(p.dh0 + row * p.D + c, m, vec, c0, c1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (kGeneral && borders >> i & 1) {
+          h = 0ull;
+          if (p.h0 && i < n)
+            h = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
+        }
+        hp[i] = h;
+        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
+        h = fma2(a[i], h, kNorm == GLR_NONE ? x : mul2(s[i], x));
+      }
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) {
+        dx -= p.D, dg -= p.D;
+        if (i >= n) continue;
+        const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
+        lam = kGeneral && borders >> (i + 1) & 1 ? with_last(p, dy, (int)end, (int)t + i, c, c0, c1)
+              : i + 1 == n                       ? add2(dy, m)
+                                                 : fma2(a[(i + 1) % kRun], lam, dy);
+        token(i, pair_at<kGeneral>(xs, i, lane, xsodd));
+        if (p.dh0 && (packed ? (borders >> i & 1) != 0 : t + i == 0)) {
+          const long long q = packed ? sequence_of(cu, p.N, (int)end, (int)t + i) : row;
           store_f32(p.dh0 + q * p.D + c, m, vec, c0, c1);
         }
       }
@@ -257,7 +304,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     }
   }
   if (!p.dh0) return;
-  if (!kPacked) {
+  if (!packed) {
     if (rounds == 0 && rank == 0 && warp == 0) store_f32(p.dh0 + row * p.D + c, carry, vec, c0, c1);
     return;
   }
@@ -268,20 +315,21 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   }
 }
 
-template <auto kKernel, typename T>
+template <auto kKernel, typename T, bool kGeneral>
 cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
-  const size_t smem = kStages * 3 * kTile * sizeof(T);
+  const size_t smem = kStages * 3 * kTileOf<T, kGeneral> * sizeof(T);
   const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
   cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
   if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
-  if (e == cudaSuccess) e = launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, smem);
+  if (e == cudaSuccess) e = launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, glr_smem(smem, p.cluster));
   if (e != cudaSuccess || !p.drate) return e;
   return launch_column_sums(p.partial, p.drate, nullptr, (p.cu ? 1 : p.N) * p.cluster, p.D, stream);
 }
 template <typename T, int kGate, int kNorm>
 cudaError_t launch(const GlrParams& p, cudaStream_t stream) {
-  return p.cu ? launch_prompt<glr_bwd_kernel<T, kGate, kNorm, true>, T>(p, stream)
-              : launch_prompt<glr_bwd_kernel<T, kGate, kNorm, false>, T>(p, stream);
+  // packed rows, and rows that are not aligned to pairs
+  return p.cu || !p.vec || p.piece == 2 ? launch_prompt<glr_bwd_kernel<T, kGate, kNorm, true>, T, true>(p, stream)
+              : launch_prompt<glr_bwd_kernel<T, kGate, kNorm, false>, T, false>(p, stream);
 }
 template <typename T, int kGate>
 cudaError_t launch_gate(const GlrParams& p, cudaStream_t stream) {

@@ -10,8 +10,8 @@
 // follow each other in time, and so do the blocks of a cluster.
 #pragma once
 
-#include <stdlib.h>
 #include <atomic>
+#include <type_traits>
 
 #include "cluster.cuh"
 #include "layer_common.cuh"
@@ -86,72 +86,131 @@ __device__ __forceinline__ void store_f32(float* p, f32x2 x, bool vec, bool c0, 
   r.v = x;
   r.store(p, vec, c0, c1);
 }
-// A tile's pair in shared memory, tokens of 64 channels.
-template <typename T>
-__device__ __forceinline__ f32x2 pair_at(const T* tile, int token, int lane) {
+// The pair of an output: rows of the plain kernels are aligned to pairs, of the general ones one of two ways, each
+// store under its own condition (a branch would keep the tokens' arithmetic apart).
+struct Places {
+  bool pair, first, second;
+};
+template <bool kGeneral>
+__device__ __forceinline__ Places places(bool vec, bool c0, bool c1) {
+  return {c0 && (!kGeneral || vec), c0 && !vec, c1 && !vec};
+}
+template <bool kGeneral, typename T>
+__device__ __forceinline__ void store_out(T* p, f32x2 x, const Places& at) {
+  Raw2<T> o;
+  o.set(x);
+  if (at.pair) o.store(p, true, true, true);
+  if (kGeneral) {
+    if (at.first) o.store(p, false, true, false);
+    if (at.second) o.store(p, false, false, true);
+  }
+}
+// Tiles lie in shared memory as tokens of 64 channels, `pitch` elements apart.  Rows of bf16 that are not
+// aligned to pairs (odd rows) lie one element further on: bit i of their mask is token i's.
+template <typename T, bool kGeneral>
+constexpr int kPitch = kGeneral && sizeof(T) == 2 ? 72 : 64;
+template <bool kGeneral, typename T>
+__device__ __forceinline__ f32x2 pair_at(const T* tile, int token, int lane, unsigned odd) {
+  const T* q = tile + token * kPitch<T, kGeneral> + 2 * lane;
   Raw2<T> r;
-  r.load(tile + token * 64 + 2 * lane, true, true, true);
+  r.load(q, true, true, true);
+  if constexpr (kGeneral && sizeof(T) == 2) {
+    Raw2<T> next;
+    next.load(q + 2, true, true, true);
+    r.v = __funnelshift_r(r.v, next.v, odd >> token & 1 ? 16 : 0);
+  }
   return r.get();
+}
+// The mask for the tokens from `row` (the first one's address) on.
+__device__ __forceinline__ unsigned odd_rows(const void* row, long long stride) {
+  const unsigned first = (unsigned)(reinterpret_cast<uintptr_t>(row) >> 1) & 1u;
+  return stride & 1 ? (first ? 0x55555555u : 0xaaaaaaaau) : 0u - first;
 }
 
 // ---- tiles on their way into shared memory ---------------------------------------------------
-// A tile of `tokens` rows of 64 channels from src, `cols` of which exist: zeros for rows
-// from `rows` on and for channels that do not exist.
+// A tile of `tokens` rows of 64 channels from src, `cols` of which exist: zeros for rows from `rows` on and for
+// channels that do not exist.
 //
 // 16 bytes an asynchronous copy where rows are made of, and aligned to, them.  The others are apart from
 // the kernels' loop, and not inlined: they are rare, and the loop is to stay in the instruction cache.
-template <typename T>
+template <int kPitch, typename T>
 __device__ __forceinline__ void copy_wide(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
   constexpr int kCols = 16 / (int)sizeof(T), kPieces = 64 / kCols;
   const int row0 = threadIdx.x / kPieces, col = threadIdx.x % kPieces * kCols, step = blockDim.x / kPieces;
   const T* from = src + row0 * stride + col;
   const long long by = step * stride;
-  tile += row0 * 64 + col;
+  tile += row0 * kPitch + col;
 #pragma unroll 4
   for (int row = row0; row < tokens; row += step) {
     const bool ok = col < cols && row < rows;
     cp_async16(tile, ok ? from : src, ok);
     from += by;
-    tile += step * 64;
+    tile += step * kPitch;
   }
 }
-// 4 bytes an asynchronous copy.
-template <typename T>
+__device__ __forceinline__ void cp_async4(void* to, const void* from, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(ok ? 4 : 0)
+               : "memory");
+}
+// 4 bytes an asynchronous copy, a row a warp: with a row's place known to the whole warp and several rows
+// unrolled, its instructions keep ahead of its latency (a word a thread, by one count over the tile: 2.5
+// times the kernel's time).
+template <int kPitch, typename T>
 __device__ __noinline__ void copy_words(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
-  constexpr int kCols = 4 / (int)sizeof(T), kPieces = 64 / kCols;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < tokens * kPieces; i += blockDim.x) {
-    const int row = i / kPieces, col = i % kPieces * kCols;
+  constexpr int kCols = 4 / (int)sizeof(T);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const int col = lane * kCols;
+  const T* from = src + warp * stride + col;
+  T* to = tile + warp * kPitch + col;
+  const long long by = warps * stride;
+#pragma unroll 8
+  for (int row = warp; row < tokens; row += warps, from += by, to += warps * kPitch) {
     const bool ok = col < cols && row < rows;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(tile + row * 64 + col)),
-                 "l"(ok ? src + row * stride + col : src), "r"(ok ? 4 : 0)
-                 : "memory");
+    cp_async4(to, ok ? from : src, ok);
+    if (kCols == 1) {
+      const bool more = col + 32 < cols && row < rows;
+      cp_async4(to + 32, more ? from + 32 : src, more);
+    }
   }
 }
-// Odd rows of bf16: plain loads, 16 under way at a time.
-static __device__ __noinline__ void copy_halves(uint16_t* tile, const uint16_t* src, long long stride, int rows,
-                                                int tokens, int cols) {
-  for (int i = threadIdx.x; i < tokens * 64; i += 16 * blockDim.x) {
-    uint16_t v[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int at = i + k * blockDim.x, row = at / 64, c = at % 64;
-      v[k] = row < rows && c < cols ? src[row * stride + c] : (uint16_t)0;
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int at = i + k * blockDim.x;
-      if (at < tokens * 64) tile[at] = v[k];
-    }
+// Odd rows of bf16 so, 4 aligned bytes a copy: those of a row that begins between two words lie one element
+// further on.  A word that is only half the row's is a plain load of that half.
+template <int kPitch>
+__device__ __noinline__ void copy_odd(uint16_t* tile, const uint16_t* src, long long stride, int rows, int tokens,
+                                      int cols) {
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const unsigned odd = odd_rows(src, stride);
+  const uint16_t* none = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(src) & ~3ull);
+  const uint16_t* from = src + warp * stride + 2 * lane;
+  uint16_t* to = tile + warp * kPitch + 2 * lane;
+  const long long by = warps * stride;
+#pragma unroll 4
+  for (int row = warp; row < tokens; row += warps, from += by, to += warps * kPitch) {
+    const int shift = odd >> (row & 31) & 1, last = row < rows ? cols : 0;
+    const auto word = [&](int at) {  // columns at, at + 1 into elements at + shift, at + shift + 1
+      const bool first = at >= 0 && at < last, second = at + 1 < last;
+      if (first == second) {
+        cp_async4(to + (at + shift - 2 * lane), first ? from + (at - 2 * lane) : none, first);
+      } else {
+        to[at + shift - 2 * lane] = first ? from[at - 2 * lane] : (uint16_t)0;
+        to[at + shift - 2 * lane + 1] = second ? from[at + 1 - 2 * lane] : (uint16_t)0;
+      }
+    };
+    word(2 * lane - shift);
+    if (lane == 0 && shift) word(63);
   }
 }
 // piece: bytes that rows are made of and aligned to
-template <typename T>
+template <bool kGeneral, typename T>
 __device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, int rows, int tokens, int cols,
                                           int piece) {
-  if (piece == 16) copy_wide(tile, src, stride, rows, tokens, cols);
-  else if (sizeof(T) == 4 || piece == 4) copy_words(tile, src, stride, rows, tokens, cols);
-  else copy_halves(reinterpret_cast<uint16_t*>(tile), reinterpret_cast<const uint16_t*>(src), stride, rows, tokens, cols);
+  constexpr int kP = kPitch<T, kGeneral>;
+  if (piece == 16)
+    copy_wide<kP>(tile, src, stride, rows, tokens, cols);
+  else if (!kGeneral || sizeof(T) == 4 || piece == 4)
+    copy_words<kP>(tile, src, stride, rows, tokens, cols);
+  else
+    copy_odd<kP>(reinterpret_cast<uint16_t*>(tile), reinterpret_cast<const uint16_t*>(src), stride, rows, tokens, cols);
 }
 
 // ---- gates -------------------------------------------------------------------------------
@@ -171,23 +230,26 @@ __device__ __forceinline__ f32x2 each(f32x2 x, F f) {
 // packed ones would need each of them in a pair of registers (8 x 2048 x 2560 training: 180 us packed,
 // GATES_US as they are).
 
-// e^u - 1 for |u| < 1/2: u times the polynomial of degree 6 with the least relative error there
-// (3.0e-9, by Remez's exchange; 1.2e-7 with the roundings).
-__device__ __forceinline__ float expm1_small(float u) {
+// Every rounding is written out (the compiler may join others in one kernel and not in another: a token's
+// gate is to have the same bits in all of them).
+
+// (e^u - 1) / u for |u| < 1/2: the polynomial of degree 6 with the least relative error there (3.0e-9, by
+// Remez's exchange; 1.2e-7 with the roundings).
+__device__ __forceinline__ float expm1_over(float u) {
   float r = 0.000198411915f;
   r = fmaf(r, u, 0.00139973243f);
   r = fmaf(r, u, 0.00833363459f);
   r = fmaf(r, u, 0.0416653194f);
   r = fmaf(r, u, 0.166666627f);
   r = fmaf(r, u, 0.50000006f);
-  r = fmaf(r, u, 1.f);
-  return r * u;
+  return fmaf(r, u, 1.f);
 }
+__device__ __forceinline__ float exp_of(float x) { return ex2(__fmul_rn(kLog2e, x)); }
 // sigmoid(g) and 1 - sigmoid(g), each to its last digits: with e = e^-g and q = 1 / (1 + e) they are q and
 // e q, but what is nearer to 1 is 1 less the other.
 __device__ __forceinline__ void sigmoid_of(float g, float& sig, float& rest) {
-  const float e = ex2(-kLog2e * g), q = rcp(1.f + e);
-  const float less = e < 1.f ? e * q : q, more = 1.f - less;
+  const float e = exp_of(-g), q = rcp(__fadd_rn(1.f, e));
+  const float less = e < 1.f ? __fmul_rn(e, q) : q, more = __fsub_rn(1.f, less);
   sig = e < 1.f ? more : less;
   rest = e < 1.f ? less : more;
 }
@@ -200,11 +262,11 @@ __device__ __forceinline__ void gate_of(float g, float rate, float& a, float& s)
   if (kGate == GLR_SIGMOID) {
     sigmoid_of(g, a, left);
   } else {
-    const float log = kGate == GLR_LOG ? g : rate * rcp(1.f + ex2(-kLog2e * g));
-    const float e = ex2(kLog2e * log), small = expm1_small(log);
+    const float log = kGate == GLR_LOG ? g : __fmul_rn(rate, rcp(__fadd_rn(1.f, exp_of(-g))));
+    const float e = exp_of(log), over = expm1_over(log);
     const bool near = fabsf(log) < 0.5f;
-    a = near ? 1.f + small : e;
-    if (kNorm != GLR_NONE) left = near ? -small : 1.f - e;
+    a = near ? fmaf(over, log, 1.f) : e;
+    if (kNorm != GLR_NONE) left = near ? -__fmul_rn(over, log) : __fsub_rn(1.f, e);
   }
   s = kNorm == GLR_NONE ? 1.f : kNorm == GLR_LINEAR ? left : sqrt_ftz(fmaf(left, a, left));
 }
@@ -269,6 +331,13 @@ __device__ __forceinline__ int first_border_above(const int32_t* cu, int N, int 
   }
   return (int)lo;
 }
+// The table, in shared memory where it fits: a search takes three reads, one after the other.
+constexpr int kBorders = 512;
+__device__ __forceinline__ const int32_t* take_borders(const GlrParams& p, int32_t* table) {
+  if (!p.cu || p.N >= kBorders) return p.cu;
+  for (int i = threadIdx.x; i <= p.N; i += blockDim.x) table[i] = p.cu[i];
+  return table;  // (complete after the block's next barrier)
+}
 // The sequence that holds token v.  (Not inlined: the loops over a thread's tokens are unrolled.)
 static __device__ __noinline__ int sequence_of(const int32_t* cu, int N, int end, int v) {
   return min(max(first_border_above(cu, N, end, v) - 1, 0), N - 1);
@@ -292,13 +361,14 @@ static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int
 // for run at once, which depends on the size (of 256 threads at two blocks an SM, 36 clusters of 8 but only
 // 14 of 14 fit this GPU).  The size with the fewest rounds over all waves of clusters is taken.  The GPU is
 // asked once for each kernel and size.
+inline size_t glr_smem(size_t tiles, int blocks) { return tiles + (blocks > 1 ? blocks * 1024 : 0); }
 template <auto kKernel>
-cudaError_t choose_cluster(GlrParams* p, unsigned threads, size_t smem, long long spans) {
+cudaError_t choose_cluster(GlrParams* p, unsigned threads, size_t tiles, long long spans) {
   static std::atomic<int> room[kGlrMaxCluster + 1];
   const long long units = glr_units(*p);
   long long best = -1;
-  const int force = getenv("GLR_K") ? atoi(getenv("GLR_K")) : 0;
   for (int k = 1; k <= kGlrMaxCluster && (k == 1 || k <= spans); ++k) {
+    const size_t smem = glr_smem(tiles, k);
     int n = room[k].load(std::memory_order_relaxed);
     if (!n) {
       cudaError_t e = allow_clusters(kKernel, k, smem);
@@ -317,7 +387,7 @@ cudaError_t choose_cluster(GlrParams* p, unsigned threads, size_t smem, long lon
     if (n < 0) continue;
     // (a wave's start costs about two rounds)
     const long long cost = ((units + n - 1) / n) * ((spans + k - 1) / k + 2);
-    if (best < 0 || cost < best || k == force) best = k == force ? 0 : cost, p->cluster = k;
+    if (best < 0 || cost < best) best = cost, p->cluster = k;
   }
   return best < 0 ? cudaErrorInvalidConfiguration : cudaSuccess;
 }

@@ -17,13 +17,14 @@ namespace gdn {
 namespace {
 
 constexpr int kMinBlocks = kGlrFwdBlocks, kStages = 2, kRun = kGlrFwdRun, kWarps = kGlrFwdWarps;
-constexpr int kTile = kRun * kWarps * 64;  // of a tensor's tokens in shared memory
+template <typename T, bool kGeneral>
+constexpr int kTileOf = kRun * kWarps * kPitch<T, kGeneral>;  // of a tensor's tokens in shared memory
 
-template <typename T, int kGate, int kNorm, bool kPacked>
+template <typename T, int kGate, int kNorm, bool kGeneral>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) glr_fwd_kernel(const GlrParams p) {
-  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][tokens][64 channels]
+  constexpr int kTile = kTileOf<T, kGeneral>;
+  extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][tokens][64 channels and padding]
   __shared__ ulonglong2 s_warp[2][kWarps][32];
-  __shared__ ulonglong2 s_rank[2][kGlrMaxCluster][32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
   volatile int* const dead = &s_dead;
@@ -43,16 +44,23 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   const unsigned unit = blockIdx.x / K;
   const long long row = unit / p.tiles;
   const int tile = (int)(unit - (unsigned)row * p.tiles);
-  const bool vec = p.vec;
+  const bool vec = !kGeneral || p.vec;
   const long long c = (long long)tile * 64 + 2 * lane;
   const bool c0 = c < p.D, c1 = c + 1 < p.D;
-  const unsigned end = kPacked ? min(max(p.cu[p.N], 0), p.T) : p.T;
+  const Places at = places<kGeneral>(vec, c0, c1);
+  __shared__ int32_t s_cu[kGeneral ? kBorders : 1];
+  const bool packed = kGeneral && p.cu;
+  const int32_t* cu = kGeneral ? take_borders(p, s_cu) : nullptr;
+  const unsigned end = packed ? min(max(p.cu[p.N], 0), p.T) : p.T;
   const unsigned span = warps * kRun, round = K * span;
   const unsigned rounds = end ? (end - 1) / round + 1 : 0;
   const f32x2 rate = kGate == GLR_RATE ? load_f32(p.rate + c, vec, c0, c1) : 0ull;
-  f32x2 carry = !kPacked && p.h0 ? load_f32(p.h0 + row * p.D + c, vec, c0, c1) : 0ull;
+  f32x2 carry = !packed && p.h0 ? load_f32(p.h0 + row * p.D + c, vec, c0, c1) : 0ull;
 
   T* tiles = reinterpret_cast<T*>(s_tiles);
+  // behind them, of a cluster: [2][K blocks][32]
+  ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 2 * kTile);
+  const bool odd = kGeneral && sizeof(T) == 2 && p.piece == 2;
   const int cols = (int)min(64ll, p.D - (long long)tile * 64);
   const auto fetch = [&](unsigned r) {  // round r into its stage
     if (r < rounds) {
@@ -63,7 +71,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       for (int k = 0; k < 2; ++k, to += kTile) {
         const void* from = k ? p.g : p.x;
         const long long stride = k ? p.g_stride : p.x_stride;
-        copy_tile(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
+        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
                   p.piece);
       }
     }
@@ -81,33 +89,41 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     cp_async_wait<0>();
     __syncthreads();
     fetch(r + 1);
-    const T* xs = tiles + r % kStages * (2 * kTile) + warp * kRun * 64;
+    const T* xs = tiles + r % kStages * (2 * kTile) + warp * kRun * kPitch<T, kGeneral>;
     const T* gs = xs + kTile;
     const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist
-    const unsigned borders = kPacked && n ? borders_of(p.cu, p.N, (int)end, (int)t, kRun) : 0u;
+    const unsigned xsodd = odd && n ? odd_rows(static_cast<const T*>(p.x) + (row * p.T + t) * p.x_stride + tile * 64ll, p.x_stride) : 0u;
+    const unsigned gsodd = odd && n ? odd_rows(static_cast<const T*>(p.g) + (row * p.T + t) * p.g_stride + tile * 64ll, p.g_stride) : 0u;
+    const unsigned borders = packed && n ? borders_of(cu, p.N, (int)end, (int)t, kRun) : 0u;
+    // A run of as many tokens as there can be without a border is worked on without any check between them.
+    const bool plain = n == kRun && !(kGeneral && borders);
     f32x2 a[kRun], b[kRun];
     f32x2 A = dup2(1.f), H = 0ull;
     bool cut = false;
+    const auto reduce = [&](auto plain) {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      f32x2 s;
-      gate2<kGate, kNorm>(pair_at(gs, i, lane), rate, a[i], s);
-      b[i] = pair_at(xs, i, lane);
-      if (kNorm != GLR_NONE) b[i] = mul2(s, b[i]);
-      if (kPacked && borders >> i & 1) {
-        if (p.h0 && i < n) {
-          const long long q = sequence_of(p.cu, p.N, (int)end, (int)t + i);
-          b[i] = fma2(a[i], load_f32(p.h0 + q * p.D + c, vec, c0, c1), b[i]);
+      for (int i = 0; i < kRun; ++i) {
+        f32x2 s;
+        gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s);
+        b[i] = pair_at<kGeneral>(xs, i, lane, xsodd);
+        if (kNorm != GLR_NONE) b[i] = mul2(s, b[i]);
+        if (!decltype(plain)::value && kGeneral && borders >> i & 1) {
+          if (p.h0 && i < n) {
+            const long long q = sequence_of(cu, p.N, (int)end, (int)t + i);
+            b[i] = fma2(a[i], load_f32(p.h0 + q * p.D + c, vec, c0, c1), b[i]);
+          }
+          H = b[i];
+          cut = true;
+        } else {
+          H = fma2(a[i], H, b[i]);
+          A = mul2(A, a[i]);
         }
-        H = b[i];
-        cut = true;
-      } else {
-        H = fma2(a[i], H, b[i]);
-        A = mul2(A, a[i]);
       }
-    }
+    };
+    if (!kGeneral || plain) reduce(std::true_type{});
+    else reduce(std::false_type{});
     // (behind the last token nothing is read from h: what zeros make of the gates there does not matter)
-    A = kPacked && cut ? 0ull : at_least_tiny(A);
+    A = kGeneral && cut ? 0ull : at_least_tiny(A);
     s_warp[turn][warp][lane] = make_ulonglong2(A, H);
     __syncthreads();
     // all the warps' stretches in order; (A, H) becomes what lies before this warp's
@@ -116,7 +132,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
 #pragma unroll 4
       for (int w = from; w < to; ++w) {
         const ulonglong2 v = s_warp[turn][w][lane];
-        follow<kPacked>(sA, sH, v.x, v.y);
+        follow<kGeneral>(sA, sH, v.x, v.y);
       }
     };
     lead(0, warp);
@@ -125,15 +141,15 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     if (K > 1) {
       lead(warp, warps);
       if (!*dead) {
-        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[turn][rank][lane], &s_bar[turn], k, sA, sH);
+        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sA, sH);
       }
       wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
       f32x2 now = carry;
       const auto pass = [&](unsigned from, unsigned to) {
 #pragma unroll 4
         for (unsigned k = from; k < to; ++k) {
-          const ulonglong2 v = s_rank[turn][k][lane];
-          now = through<kPacked>(v.x, v.y, now);
+          const ulonglong2 v = s_rank[(turn * K + k) * 32 + lane];
+          now = through<kGeneral>(v.x, v.y, now);
         }
       };
       pass(0, rank);
@@ -142,31 +158,28 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       carry = now;
     } else {
       lead(warp, warps);
-      carry = through<kPacked>(sA, sH, carry);
+      carry = through<kGeneral>(sA, sH, carry);
     }
-    h = through<kPacked>(A, H, h);
+    h = through<kGeneral>(A, H, h);
     if (p.states && t % kGlrChunk == 0 && n)
       store_f32(p.states + (row * p.chunks + t / kGlrChunk) * p.D + c, h, vec, c0, c1);
-    if (!kPacked && n == kRun && t + kRun != end) {
+    if (plain) {
       T* to = y;
 #pragma unroll
       for (int i = 0; i < kRun; ++i, to += p.D) {
         h = fma2(a[i], h, b[i]);
-        Raw2<T> o;
-        o.set(h);
-        o.store(to, vec, c0, c1);
+        store_out<kGeneral>(to, h, at);
       }
+      if (p.hT && !packed && t + kRun == end) store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
     } else {  // the last tokens of sequences among them, or fewer tokens
       T* to = y;
 #pragma unroll
       for (int i = 0; i < kRun; ++i, to += p.D) {
         if (i >= n) break;
-        h = kPacked && borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
-        Raw2<T> o;
-        o.set(h);
-        o.store(to, vec, c0, c1);
-        if (p.hT && (kPacked ? (borders >> (i + 1) & 1) != 0 : t + i + 1 == end)) {
-          const long long q = kPacked ? sequence_of(p.cu, p.N, (int)end, (int)t + i) : row;
+        h = kGeneral && borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
+        store_out<kGeneral>(to, h, at);
+        if (p.hT && (packed ? (borders >> (i + 1) & 1) != 0 : t + i + 1 == end)) {
+          const long long q = packed ? sequence_of(cu, p.N, (int)end, (int)t + i) : row;
           store_f32(p.hT + q * p.D + c, h, vec, c0, c1);
         }
       }
@@ -176,7 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   cp_async_wait<0>();
   if (K > 1) cluster_sync();  // no block leaves before its neighbours have sent what they send
   if (!p.hT || p.hT == p.h0) return;
-  if (!kPacked) {  // no token at all
+  if (!packed) {  // no token at all
     if (rounds == 0 && rank == 0 && warp == 0) store_f32(p.hT + row * p.D + c, carry, vec, c0, c1);
     return;
   }
@@ -207,13 +220,14 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrParams p) {
   store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
 }
 
-template <auto kKernel, typename T>
+template <auto kKernel, typename T, bool kGeneral>
 cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
-  const size_t smem = kStages * 2 * kTile * sizeof(T);
+  const size_t smem = kStages * 2 * kTileOf<T, kGeneral> * sizeof(T);
   const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
   cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
   if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
-  return e == cudaSuccess ? launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, smem) : e;
+  if (e != cudaSuccess) return e;
+  return launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, glr_smem(smem, p.cluster));
 }
 template <typename T, int kGate, int kNorm>
 cudaError_t launch(const GlrParams& p, bool step, cudaStream_t stream) {
@@ -221,8 +235,9 @@ cudaError_t launch(const GlrParams& p, bool step, cudaStream_t stream) {
     glr_step_kernel<T, kGate, kNorm><<<(unsigned)(((long long)p.N * p.tiles + 3) / 4), 128, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  return p.cu ? launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true>, T>(p, stream)
-              : launch_prompt<glr_fwd_kernel<T, kGate, kNorm, false>, T>(p, stream);
+  // packed rows, and rows that are not aligned to pairs
+  return p.cu || !p.vec || p.piece == 2 ? launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true>, T, true>(p, stream)
+              : launch_prompt<glr_fwd_kernel<T, kGate, kNorm, false>, T, false>(p, stream);
 }
 template <typename T, int kGate>
 cudaError_t launch_gate(const GlrParams& p, bool step, cudaStream_t stream) {

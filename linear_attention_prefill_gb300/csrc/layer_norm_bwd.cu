@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1) ln_bwd_kernel(const LnParams p) {
       for (int j = 0; j < 4; ++j) {
         const f32x2 uw = mul2(u[i][j], w[i][j]);
         ss = fma2(r[i][j], r[i][j], ss);
-        su = add2(su, uw);
+        su = fma2(u[i][j], w[i][j], su);
         sx = fma2(uw, r[i][j], sx);
       }
       v[0] += both(ss), v[1] += both(su), v[2] += both(sx);
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) ln_bwd_ring_kernel(const LnParams p,
         r[k][j] = add2(r[k][j], mean);
         const f32x2 uw = mul2(u[k][j], w[j]);
         ss = fma2(r[k][j], r[k][j], ss);
-        su = add2(su, uw);
+        su = fma2(u[k][j], w[j], su);
         sx = fma2(uw, r[k][j], sx);
       }
       if (here) q[4 * k] = both(ss), q[4 * k + 1] = both(su), q[4 * k + 2] = both(sx);

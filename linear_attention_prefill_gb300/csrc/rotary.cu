@@ -32,17 +32,33 @@ struct Piece {
   union {
     Word word;
     T e[V];
+    uint32_t pair[V * sizeof(T) < 4 ? 1 : V * sizeof(T) / 4];
   };
   __device__ __forceinline__ Piece() {}
   __device__ __forceinline__ void load(const T* p) { word = *reinterpret_cast<const Word*>(p); }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Word*>(p) = word; }
+  // (pairs of bf16 as halves of a register)
   __device__ __forceinline__ void get(float (&o)[V]) const {
+    if constexpr (sizeof(T) == 2 && V > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = to_f32(e[i]);
+      for (int i = 0; i < V / 2; ++i) {
+        o[2 * i] = __uint_as_float(pair[i] << 16);
+        o[2 * i + 1] = __uint_as_float(pair[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = to_f32(e[i]);
+    }
   }
   __device__ __forceinline__ void set(const float (&o)[V]) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) from_f32(e + i, o[i]);
+      for (int i = 0; i < V / 2; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pair[i]) : "f"(o[2 * i + 1]), "f"(o[2 * i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) from_f32(e + i, o[i]);
+    }
   }
 };
 
@@ -63,7 +79,7 @@ __device__ __forceinline__ bool position_of(const RotaryParams& p, long long tok
     n = lo;
     first = p.cu[lo];
   } else {
-    n = token / p.T;
+    n = (unsigned)token / (unsigned)p.T;  // (tokens fit 31 bits)
     first = n * p.T;
   }
   *at = token - first + (p.offsets ? p.offsets[n] : 0);
@@ -73,7 +89,7 @@ __device__ __forceinline__ bool position_of(const RotaryParams& p, long long tok
 // blockDim.x threads of a head: R / 2 / V of them have V pairs each, the others 2 V columns that are
 // passed through.  blockDim.y is the block's tokens times some heads of each: a thread stays with its
 // token, whose cosines and sines it keeps, and takes every so many of its heads, kAhead loads ahead.
-constexpr int kRotaryThreads = 256, kAhead = 4, kMinBlocks = 3;
+constexpr int kRotaryThreads = 128, kAhead = 4, kMinBlocks = 6;
 template <typename T, int V, bool kNext>
 __global__ void __launch_bounds__(V > 1 ? 256 : 512, V > 1 ? kMinBlocks : 1) rotary_kernel(const RotaryParams p) {
   extern __shared__ __align__(16) float2 s_turn[];  // [tokens of the block][R / 2]: m cos, m sin
