@@ -31,10 +31,10 @@ template <typename T, bool kGeneral>
 constexpr int kTileOf = kRun * kWarps * kPitch<T, kGeneral>;  // of a tensor's tokens in shared memory
 
 // lambda of a sequence's last token without what comes from behind: dy + dhT
-__device__ __forceinline__ f32x2 with_last(const GlrParams& p, f32x2 dy, int end, int t, long long c, bool c0,
+__device__ __forceinline__ f32x2 with_last(const GlrParams& p, const int32_t* cu, f32x2 dy, int end, int t, long long c, bool c0,
                                            bool c1) {
   if (!p.dhT) return dy;
-  return add2(dy, load_f32(p.dhT + (long long)sequence_of(p.cu, p.N, end, t) * p.D + c, p.vec, c0, c1));
+  return add2(dy, load_f32(p.dhT + (long long)sequence_of(cu, p.N, end, t) * p.D + c, p.vec, c0, c1));
 }
 
 template <typename T, int kGate, int kNorm, bool kGeneral>
@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 3 * kTile);
   const bool odd = kGeneral && sizeof(T) == 2 && p.piece == 2;
   const int cols = (int)min(64ll, p.D - (long long)tile * 64);
+  const long long tokens = packed ? p.T : (long long)p.N * p.T;
   const auto fetch = [&](unsigned r) {  // round r, counted from the last tokens, into its stage
     if (r < rounds) {
       const unsigned first = (rounds - 1 - r) * round + rank * span;
@@ -89,8 +90,8 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       for (int k = 0; k < 3; ++k, to += kTile) {
         const void* from = k == 0 ? p.x : k == 1 ? p.g : p.dy;
         const long long stride = k == 0 ? p.x_stride : k == 1 ? p.g_stride : p.dy_stride;
-        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
-                  p.piece);
+        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span,
+                             cols, p.piece, from, (tokens - 1) * stride + p.D);
       }
     }
     cp_async_commit();
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
         if (i >= n) {
           a[i] = dup2(1.f);
         } else if (kGeneral && borders >> (i + 1) & 1) {
-          lam = with_last(p, dy, (int)end, (int)t + i, c, c0, c1);
+          lam = with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1);
           cut = true;
         }
         A = mul2(A, a[i]);
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
         dx -= p.D, dg -= p.D;
         if (i >= n) continue;
         const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
-        lam = kGeneral && borders >> (i + 1) & 1 ? with_last(p, dy, (int)end, (int)t + i, c, c0, c1)
+        lam = kGeneral && borders >> (i + 1) & 1 ? with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1)
               : i + 1 == n                       ? add2(dy, m)
                                                  : fma2(a[(i + 1) % kRun], lam, dy);
         token(i, pair_at<kGeneral>(xs, i, lane, xsodd));

@@ -174,10 +174,12 @@ __device__ __noinline__ void copy_words(T* tile, const T* src, long long stride,
   }
 }
 // Odd rows of bf16 so, 4 aligned bytes a copy: those of a row that begins between two words lie one element
-// further on.  A word that is only half the row's is a plain load of that half.
+// further on.  A word that the row shares with a neighbour is copied whole, what is not the row's is not read
+// from the tile; only a word that would reach out of the operand (from `begin` to `end`) is a plain load of
+// its half.
 template <int kPitch>
 __device__ __noinline__ void copy_odd(uint16_t* tile, const uint16_t* src, long long stride, int rows, int tokens,
-                                      int cols) {
+                                      int cols, const uint16_t* begin, const uint16_t* end) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   const unsigned odd = odd_rows(src, stride);
   const uint16_t* none = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(src) & ~3ull);
@@ -186,31 +188,33 @@ __device__ __noinline__ void copy_odd(uint16_t* tile, const uint16_t* src, long 
   const long long by = warps * stride;
 #pragma unroll 4
   for (int row = warp; row < tokens; row += warps, from += by, to += warps * kPitch) {
-    const int shift = odd >> (row & 31) & 1, last = row < rows ? cols : 0;
-    const auto word = [&](int at) {  // columns at, at + 1 into elements at + shift, at + shift + 1
-      const bool first = at >= 0 && at < last, second = at + 1 < last;
-      if (first == second) {
-        cp_async4(to + (at + shift - 2 * lane), first ? from + (at - 2 * lane) : none, first);
-      } else {
-        to[at + shift - 2 * lane] = first ? from[at - 2 * lane] : (uint16_t)0;
-        to[at + shift - 2 * lane + 1] = second ? from[at + 1 - 2 * lane] : (uint16_t)0;
+    const int shift = odd >> (row & 31) & 1;
+    const auto word = [&](const uint16_t* w, uint16_t* at, int col) {  // column col is the word's first
+      const bool wanted = row < rows && col < cols, inside = w >= begin && w + 2 <= end;
+      cp_async4(at, wanted && inside ? w : none, wanted && inside);
+      if (wanted && !inside) {
+        if (w >= begin) at[0] = w[0];
+        else at[1] = w[1];
       }
     };
-    word(2 * lane - shift);
-    if (lane == 0 && shift) word(63);
+    word(from - shift, to, 2 * lane - shift);
+    if (lane == 0 && shift) word(from + 63, to + 64, 63);
   }
 }
-// piece: bytes that rows are made of and aligned to
+// piece: bytes that rows are made of and aligned to; begin, end: the operand
 template <bool kGeneral, typename T>
 __device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, int rows, int tokens, int cols,
-                                          int piece) {
+                                          int piece, const void* begin, long long length) {
   constexpr int kP = kPitch<T, kGeneral>;
-  if (piece == 16)
+  if (piece == 16) {
     copy_wide<kP>(tile, src, stride, rows, tokens, cols);
-  else if (!kGeneral || sizeof(T) == 4 || piece == 4)
+  } else if (!kGeneral || sizeof(T) == 4 || piece == 4) {
     copy_words<kP>(tile, src, stride, rows, tokens, cols);
-  else
-    copy_odd<kP>(reinterpret_cast<uint16_t*>(tile), reinterpret_cast<const uint16_t*>(src), stride, rows, tokens, cols);
+  } else {
+    const uint16_t* first = static_cast<const uint16_t*>(begin);
+    copy_odd<kP>(reinterpret_cast<uint16_t*>(tile), reinterpret_cast<const uint16_t*>(src), stride, rows, tokens, cols,
+                 first, first + length);
+  }
 }
 
 // ---- gates -------------------------------------------------------------------------------

@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 2 * kTile);
   const bool odd = kGeneral && sizeof(T) == 2 && p.piece == 2;
   const int cols = (int)min(64ll, p.D - (long long)tile * 64);
+  const long long tokens = packed ? p.T : (long long)p.N * p.T;
   const auto fetch = [&](unsigned r) {  // round r into its stage
     if (r < rounds) {
       const unsigned first = r * round + rank * span;
@@ -71,8 +72,8 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       for (int k = 0; k < 2; ++k, to += kTile) {
         const void* from = k ? p.g : p.x;
         const long long stride = k ? p.g_stride : p.x_stride;
-        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span, cols,
-                  p.piece);
+        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span,
+                             cols, p.piece, from, (tokens - 1) * stride + p.D);
       }
     }
     cp_async_commit();
