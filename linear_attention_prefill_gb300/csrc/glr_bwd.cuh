@@ -124,61 +124,61 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     const unsigned borders = packed && n ? borders_of(cu, p.N, (int)end, (int)t, kRun) : 0u;
     f32x2 h = before;
     if (r + 1 < rounds) before = state_before(t - round);
-    // A run of as many tokens as there can be without a border is worked on without any check between them.
-    const bool plain = n == kRun && !(kGeneral && borders);
+    // One border among the run's tokens, and fewer tokens than a run has, are dealt with by selects, as
+    // forwards: with the state that the border's sequence starts from, and the gradient that the one
+    // before it ends with.
+    const int border = kGeneral && borders ? __ffs(borders) - 1 : 2 * kRun;
+    const bool many = kGeneral && (borders & (borders - 1)) != 0;
+    const bool full = !kGeneral && n == kRun;
+    f32x2 start = 0ull, finish = 0ull;
+    if (kGeneral && border < n && p.h0)
+      start = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + border) * p.D + c, vec, c0, c1);
+    if (kGeneral && border > 0 && border <= n && p.dhT)
+      finish = load_f32(p.dhT + (long long)sequence_of(cu, p.N, (int)end, (int)t + border - 1) * p.D + c, vec, c0, c1);
     f32x2 a[kRun], s[kRun];
-    f32x2 A = dup2(1.f), H = 0ull, M = 0ull;
-    bool cut = false;
-    if (plain) {
+    f32x2 A = dup2(1.f), H = 0ull, M = 0ull, lam = 0ull;
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s[i]);
-        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
-        H = fma2(a[i], H, kNorm == GLR_NONE ? x : mul2(s[i], x));
-        A = mul2(A, a[i]);
-      }
-      A = at_least_tiny(A);
-      s_ahead[turn][warp][lane] = make_ulonglong2(A, H);
+    for (int i = 0; i < kRun; ++i) {
+      gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s[i]);
+      const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
+      H = fma2(a[i], kGeneral ? pick(i == border, start, H) : H, kNorm == GLR_NONE ? x : mul2(s[i], x));
+      if (!full) a[i] = pick(i < n, a[i], dup2(1.f));  // (tokens that do not exist pass m on)
+      A = mul2(A, a[i]);
+    }
+    A = at_least_tiny(A);
+    if (!(kGeneral && many)) {
+      s_ahead[turn][warp][lane] = make_ulonglong2(kGeneral && border < kRun ? 0ull : A, H);
       // backwards: m before these tokens from m behind them
-      f32x2 lam = pair_at<kGeneral>(ds, kRun - 1, lane, dsodd);
 #pragma unroll
-      for (int i = kRun - 2; i >= 0; --i) lam = fma2(a[i + 1], lam, pair_at<kGeneral>(ds, i, lane, dsodd));
+      for (int i = kRun - 1; i >= 0; --i) {
+        const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
+        const bool ends = kGeneral && i + 1 == border;
+        if (i + 1 == kRun) lam = kGeneral ? add2(dy, pick(ends, finish, 0ull)) : dy;
+        else lam = fma2(kGeneral ? pick(ends, dup2(1.f), a[(i + 1) % kRun]) : a[(i + 1) % kRun],
+                        kGeneral ? pick(ends, finish, lam) : lam, dy);
+      }
       M = mul2(a[0], lam);
+      if (kGeneral && border > 0 && border <= kRun) A = 0ull;
     } else {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
-        gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s[i]);
-        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd), b = kNorm == GLR_NONE ? x : mul2(s[i], x);
-        if (kGeneral && borders >> i & 1) {
-          f32x2 first = 0ull;
-          if (p.h0 && i < n)
-            first = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
-          H = fma2(a[i], first, b);
-          cut = true;
-        } else {
-          H = fma2(a[i], H, b);
-          A = mul2(A, a[i]);
-        }
+        const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
+        f32x2 from = H;
+        if (borders >> i & 1)
+          from = p.h0 && i < n ? load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, vec,
+                                          c0, c1)
+                               : 0ull;
+        H = fma2(a[i], from, kNorm == GLR_NONE ? x : mul2(s[i], x));
       }
-      s_ahead[turn][warp][lane] = make_ulonglong2(cut ? 0ull : at_least_tiny(A), H);
-      // (tokens that do not exist pass m on)
-      A = dup2(1.f);
-      cut = false;
-      f32x2 lam = 0ull;
+      s_ahead[turn][warp][lane] = make_ulonglong2(0ull, H);
 #pragma unroll
       for (int i = kRun - 1; i >= 0; --i) {
         const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
         lam = i + 1 < kRun ? fma2(a[(i + 1) % kRun], lam, dy) : dy;
-        if (i >= n) {
-          a[i] = dup2(1.f);
-        } else if (kGeneral && borders >> (i + 1) & 1) {
-          lam = with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1);
-          cut = true;
-        }
-        A = mul2(A, a[i]);
+        if (i < n && borders >> (i + 1) & 1) lam = with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1);
       }
       M = mul2(a[0], lam);
-      A = cut ? 0ull : at_least_tiny(A);
+      A = 0ull;
     }
     s_back[turn][warp][lane] = make_ulonglong2(A, M);
     __syncthreads();
@@ -221,9 +221,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     m = through<kGeneral>(A, M, m);
     T* dx = static_cast<T*>(p.dx) + (row * p.T + t + kRun) * p.D + c;
     T* dg = static_cast<T*>(p.dg) + (row * p.T + t + kRun) * p.D + c;
-    f32x2 hp[kRun], lam = 0ull;  // the state before each token; lambda
-    const auto token = [&](int i, f32x2 x) {
-      store_out<kGeneral>(dx, kNorm == GLR_NONE ? lam : mul2(s[i], lam), at);
+    f32x2 hp[kRun];  // the state before each token
+    const auto token = [&](int i, f32x2 x, bool some) {
+      if (some) store_out<kGeneral>(dx, kNorm == GLR_NONE ? lam : mul2(s[i], lam), at);
       // dL / (a lambda): h_{t-1} and the weight's share
       f32x2 slope = hp[i];
       if (kNorm == GLR_LINEAR) slope = fma2(x, dup2(-1.f), slope);
@@ -242,32 +242,56 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
           sigmoid_of(g1, sig1, rest1);
         }
         if (kGate == GLR_RATE) {
-          drate = fma2(d, pack2(sig0, sig1), drate);
+          drate = fma2(some ? d : 0ull, pack2(sig0, sig1), drate);
           d = mul2(mul2(d, pack2(sig0, sig1)), rate);
         }
         d = mul2(d, pack2(rest0, rest1));
       }
-      store_out<kGeneral>(dg, d, at);
+      if (some) store_out<kGeneral>(dg, d, at);
     };
-    if (plain) {
+    if (!(kGeneral && many)) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
-        hp[i] = h;
+        hp[i] = kGeneral ? pick(i == border, start, h) : h;
         const f32x2 x = pair_at<kGeneral>(xs, i, lane, xsodd);
-        h = fma2(a[i], h, kNorm == GLR_NONE ? x : mul2(s[i], x));
+        h = fma2(a[i], hp[i], kNorm == GLR_NONE ? x : mul2(s[i], x));
       }
+      // the gradient of the state that a sequence starts from
+      const int first = packed ? border : t == 0 ? 0 : 2 * kRun;
+      f32x2 of_start = 0ull;
+      if (full) {
 #pragma unroll
-      for (int i = kRun - 1; i >= 0; --i) {
-        dx -= p.D, dg -= p.D;
-        const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
-        lam = i + 1 == kRun ? add2(dy, m) : fma2(a[(i + 1) % kRun], lam, dy);
-        token(i, pair_at<kGeneral>(xs, i, lane, xsodd));
+        for (int i = kRun - 1; i >= 0; --i) {
+          dx -= p.D, dg -= p.D;
+          const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
+          lam = i + 1 == kRun ? add2(dy, m) : fma2(a[(i + 1) % kRun], lam, dy);
+          token(i, pair_at<kGeneral>(xs, i, lane, xsodd), true);
+        }
+        of_start = m;
+      } else {
+        const f32x2 behind = m;
+        m = 0ull;
+        lam = 0ull;
+#pragma unroll
+        for (int i = kRun - 1; i >= 0; --i) {
+          dx -= p.D, dg -= p.D;
+          const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
+          // what comes from the next token: nothing but `finish` at a border, m from behind the run's last
+          const bool ends = kGeneral && i + 1 == border, last = i + 1 == n;
+          const f32x2 by = i + 1 < kRun ? pick(ends || last, dup2(1.f), a[(i + 1) % kRun]) : dup2(1.f);
+          lam = fma2(by, pick(ends, finish, pick(last, behind, lam)), dy);
+          token(i, pair_at<kGeneral>(xs, i, lane, xsodd), i < n);
+          of_start = pick(i == first, m, of_start);
+        }
       }
-      if (p.dh0 && !packed && t == 0) store_f32(p.dh0 + row * p.D + c, m, vec, c0, c1);
+      if (p.dh0 && first < n) {
+        const long long q = packed ? sequence_of(cu, p.N, (int)end, (int)t + first) : row;
+        store_f32(p.dh0 + q * p.D + c, of_start, vec, c0, c1);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
-        if (kGeneral && borders >> i & 1) {
+        if (borders >> i & 1) {
           h = 0ull;
           if (p.h0 && i < n)
             h = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
@@ -281,14 +305,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
         dx -= p.D, dg -= p.D;
         if (i >= n) continue;
         const f32x2 dy = pair_at<kGeneral>(ds, i, lane, dsodd);
-        lam = kGeneral && borders >> (i + 1) & 1 ? with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1)
-              : i + 1 == n                       ? add2(dy, m)
-                                                 : fma2(a[(i + 1) % kRun], lam, dy);
-        token(i, pair_at<kGeneral>(xs, i, lane, xsodd));
-        if (p.dh0 && (packed ? (borders >> i & 1) != 0 : t + i == 0)) {
-          const long long q = packed ? sequence_of(cu, p.N, (int)end, (int)t + i) : row;
-          store_f32(p.dh0 + q * p.D + c, m, vec, c0, c1);
-        }
+        lam = borders >> (i + 1) & 1 ? with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1)
+              : i + 1 == n           ? add2(dy, m)
+                                     : fma2(a[(i + 1) % kRun], lam, dy);
+        token(i, pair_at<kGeneral>(xs, i, lane, xsodd), true);
+        if (p.dh0 && borders >> i & 1)
+          store_f32(p.dh0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, m, vec, c0, c1);
       }
     }
   }

@@ -360,6 +360,14 @@ static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int
   return bits;
 }
 
+// a where `take`, else b
+__device__ __forceinline__ f32x2 pick(bool take, f32x2 a, f32x2 b) {
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(take ? a0 : b0, take ? a1 : b1);
+}
+
 // ---- launches --------------------------------------------------------------------------------
 // Blocks of a cluster: they go on together through a row's `spans`, and as many clusters as there is room
 // for run at once, which depends on the size (of 256 threads at two blocks an SM, 36 clusters of 8 but only

@@ -96,35 +96,42 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     const unsigned xsodd = odd && n ? odd_rows(static_cast<const T*>(p.x) + (row * p.T + t) * p.x_stride + tile * 64ll, p.x_stride) : 0u;
     const unsigned gsodd = odd && n ? odd_rows(static_cast<const T*>(p.g) + (row * p.T + t) * p.g_stride + tile * 64ll, p.g_stride) : 0u;
     const unsigned borders = packed && n ? borders_of(cu, p.N, (int)end, (int)t, kRun) : 0u;
-    // A run of as many tokens as there can be without a border is worked on without any check between them.
-    const bool plain = n == kRun && !(kGeneral && borders);
+    // The first border among the run's tokens (a sequence starts there, or the last one ended before it), and
+    // the state that it starts from.  One border, and fewer tokens than a run has, are dealt with by
+    // selects: branches between the tokens would keep their arithmetic apart (8 x 2048 x 2560 training: 172 us
+    // for 142).  Runs with more borders are rare.
+    const int border = kGeneral && borders ? __ffs(borders) - 1 : 2 * kRun;
+    const bool many = kGeneral && (borders & (borders - 1)) != 0;
+    f32x2 start = 0ull;
+    if (kGeneral && border < n && p.h0)
+      start = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + border) * p.D + c, vec, c0, c1);
     f32x2 a[kRun], b[kRun];
     f32x2 A = dup2(1.f), H = 0ull;
-    bool cut = false;
-    const auto reduce = [&](auto plain) {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      f32x2 s;
+      gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s);
+      b[i] = pair_at<kGeneral>(xs, i, lane, xsodd);
+      if (kNorm != GLR_NONE) b[i] = mul2(s, b[i]);
+      H = fma2(a[i], kGeneral ? pick(i == border, start, H) : H, b[i]);
+      A = mul2(A, a[i]);
+    }
+    if (kGeneral && many) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
-        f32x2 s;
-        gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s);
-        b[i] = pair_at<kGeneral>(xs, i, lane, xsodd);
-        if (kNorm != GLR_NONE) b[i] = mul2(s, b[i]);
-        if (!decltype(plain)::value && kGeneral && borders >> i & 1) {
-          if (p.h0 && i < n) {
-            const long long q = sequence_of(cu, p.N, (int)end, (int)t + i);
-            b[i] = fma2(a[i], load_f32(p.h0 + q * p.D + c, vec, c0, c1), b[i]);
-          }
+        if (borders >> i & 1) {
+          f32x2 first = 0ull;
+          if (p.h0 && i < n)
+            first = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, vec, c0, c1);
+          b[i] = fma2(a[i], first, b[i]);
           H = b[i];
-          cut = true;
         } else {
           H = fma2(a[i], H, b[i]);
-          A = mul2(A, a[i]);
         }
       }
-    };
-    if (!kGeneral || plain) reduce(std::true_type{});
-    else reduce(std::false_type{});
+    }
     // (behind the last token nothing is read from h: what zeros make of the gates there does not matter)
-    A = kGeneral && cut ? 0ull : at_least_tiny(A);
+    A = kGeneral && border < kRun ? 0ull : at_least_tiny(A);
     s_warp[turn][warp][lane] = make_ulonglong2(A, H);
     __syncthreads();
     // all the warps' stretches in order; (A, H) becomes what lies before this warp's
@@ -164,25 +171,35 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     h = through<kGeneral>(A, H, h);
     if (p.states && t % kGlrChunk == 0 && n)
       store_f32(p.states + (row * p.chunks + t / kGlrChunk) * p.D + c, h, vec, c0, c1);
-    if (plain) {
-      T* to = y;
+    T* to = y;
+    if (!kGeneral && n == kRun) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i, to += p.D) {
         h = fma2(a[i], h, b[i]);
         store_out<kGeneral>(to, h, at);
       }
-      if (p.hT && !packed && t + kRun == end) store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
-    } else {  // the last tokens of sequences among them, or fewer tokens
-      T* to = y;
+      if (p.hT && t + kRun == end) store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
+    } else if (!many) {
+      const int last = packed ? border : t + n == end ? n : 0;  // (the token before it ends its sequence)
+      f32x2 final = 0ull;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i, to += p.D) {
+        h = fma2(a[i], kGeneral ? pick(i == border, start, h) : h, b[i]);
+        if (i < n) store_out<kGeneral>(to, h, at);
+        final = pick(i + 1 == last, h, final);
+      }
+      if (p.hT && last > 0 && last <= n) {
+        const long long q = packed ? sequence_of(cu, p.N, (int)end, (int)t + last - 1) : row;
+        store_f32(p.hT + q * p.D + c, final, vec, c0, c1);
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < kRun; ++i, to += p.D) {
         if (i >= n) break;
-        h = kGeneral && borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
+        h = borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
         store_out<kGeneral>(to, h, at);
-        if (p.hT && (packed ? (borders >> (i + 1) & 1) != 0 : t + i + 1 == end)) {
-          const long long q = packed ? sequence_of(cu, p.N, (int)end, (int)t + i) : row;
-          store_f32(p.hT + q * p.D + c, h, vec, c0, c1);
-        }
+        if (p.hT && borders >> (i + 1) & 1)
+          store_f32(p.hT + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, h, vec, c0, c1);
       }
     }
     y += (long long)round * p.D;
