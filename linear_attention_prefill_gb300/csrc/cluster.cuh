@@ -69,7 +69,8 @@ __device__ __forceinline__ void wait_for_ranks(uint64_t* bar, unsigned parity, u
   }
 }
 
-// A launch in clusters of `blocks` (1: none) neighbouring blocks, with `smem` bytes of dynamic memory.
+// A launch in clusters of `blocks` (1: none) neighbouring blocks, with `smem` bytes of dynamic memory.  `most`:
+// what any launch of the kernel takes, allowed for all of them (another thread may launch it with more).
 template <typename Kernel>
 cudaError_t allow_clusters(Kernel kernel, unsigned blocks, size_t smem) {
   cudaError_t e = cudaSuccess;
@@ -96,8 +97,8 @@ struct ClusterConfig {
 };
 template <typename Kernel, typename Params>
 cudaError_t launch_clusters(Kernel kernel, unsigned grid, unsigned threads, unsigned blocks, const Params& p,
-                            cudaStream_t stream, size_t smem = 0) {
-  const cudaError_t e = allow_clusters(kernel, blocks, smem);
+                            cudaStream_t stream, size_t smem = 0, size_t most = 0) {
+  const cudaError_t e = allow_clusters(kernel, blocks, most);
   if (e != cudaSuccess) return e;
   const ClusterConfig c(grid, threads, blocks, smem, stream);
   return cudaLaunchKernelEx(&c.cfg, kernel, p);

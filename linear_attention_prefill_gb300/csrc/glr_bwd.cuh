@@ -344,7 +344,8 @@ cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
   const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
   cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
   if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
-  if (e == cudaSuccess) e = launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, glr_smem(smem, p.cluster));
+  if (e == cudaSuccess) e = launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream,
+                         glr_smem(smem, p.cluster), glr_smem(smem, kGlrMaxCluster));
   if (e != cudaSuccess || !p.drate) return e;
   return launch_column_sums(p.partial, p.drate, nullptr, (p.cu ? 1 : p.N) * p.cluster, p.D, stream);
 }

@@ -230,10 +230,8 @@ __device__ __forceinline__ f32x2 each(f32x2 x, F f) {
   return pack2(f(a), f(b));
 }
 
-// The gates are computed channel by channel: their constants are operands of scalar instructions, while
-// packed ones would need each of them in a pair of registers (8 x 2048 x 2560 training: 180 us packed,
-// GATES_US as they are).
-
+// The gates are computed channel by channel: their constants are operands of scalar instructions.
+//
 // Every rounding is written out (the compiler may join others in one kernel and not in another: a token's
 // gate is to have the same bits in all of them).
 
@@ -383,7 +381,7 @@ cudaError_t choose_cluster(GlrParams* p, unsigned threads, size_t tiles, long lo
     const size_t smem = glr_smem(tiles, k);
     int n = room[k].load(std::memory_order_relaxed);
     if (!n) {
-      cudaError_t e = allow_clusters(kKernel, k, smem);
+      cudaError_t e = allow_clusters(kKernel, k, glr_smem(tiles, kGlrMaxCluster));
       if (e != cudaSuccess) return e;
       const ClusterConfig c(k, threads, k, smem, nullptr);
       if (k == 1) {

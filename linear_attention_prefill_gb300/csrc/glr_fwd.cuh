@@ -245,7 +245,8 @@ cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
   cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
   if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
   if (e != cudaSuccess) return e;
-  return launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream, glr_smem(smem, p.cluster));
+  return launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream,
+                         glr_smem(smem, p.cluster), glr_smem(smem, kGlrMaxCluster));
 }
 template <typename T, int kGate, int kNorm>
 cudaError_t launch(const GlrParams& p, bool step, cudaStream_t stream) {

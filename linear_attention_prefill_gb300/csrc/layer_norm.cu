@@ -183,7 +183,7 @@ template <typename T, int kRows>
 cudaError_t launch_ring(LnParams p, const LnRing& shape, cudaStream_t stream) {
   const auto kernel = ln_fwd_ring_kernel<T, kRows>;
   const int threads = (p.D / 8 + 31) / 32 * 32, smem = shape.slots * shape.slot_bytes;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnRingBytes);
   if (e == cudaSuccess) e = device_error_word(&p.err);
   if (e != cudaSuccess) return e;
   const long long most = (long long)shape.blocks * kSms;

@@ -89,9 +89,9 @@ __device__ __forceinline__ bool position_of(const RotaryParams& p, long long tok
 // blockDim.x threads of a head: R / 2 / V of them have V pairs each, the others 2 V columns that are
 // passed through.  blockDim.y is the block's tokens times some heads of each: a thread stays with its
 // token, whose cosines and sines it keeps, and takes every so many of its heads, kAhead loads ahead.
-constexpr int kRotaryThreads = 128, kAhead = 4, kMinBlocks = 6;
+constexpr int kRotaryThreads = 128, kAhead = 4;
 template <typename T, int V, bool kNext>
-__global__ void __launch_bounds__(V > 1 ? 256 : 512, V > 1 ? kMinBlocks : 1) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(V > 1 ? 256 : 512, V > 1 ? 3 : 1) rotary_kernel(const RotaryParams p) {
   extern __shared__ __align__(16) float2 s_turn[];  // [tokens of the block][R / 2]: m cos, m sin
   const int half = p.R / 2, pairs = half / V;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
