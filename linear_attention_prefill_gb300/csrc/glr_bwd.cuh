@@ -48,16 +48,6 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (known to be the warp's)
   const unsigned K = p.cluster, rank = K > 1 ? cluster_rank() : 0;
-  if (K > 1) {
-    if (threadIdx.x == 0) {
-      mbar_init(&s_bar[0], 1);
-      mbar_init(&s_bar[1], 1);
-      mbar_fence_init();
-      s_dead = 0;
-    }
-    __syncwarp();
-    cluster_arrive();
-  }
   const unsigned unit = blockIdx.x / K;
   const long long row = unit / p.tiles;
   const int tile = (int)(unit - (unsigned)row * p.tiles);
@@ -75,6 +65,16 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   f32x2 carry = !packed && p.dhT ? load_f32(p.dhT + row * p.D + c, vec, c0, c1) : 0ull;
   f32x2 drate = 0ull;
 
+  if (K > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(&s_bar[0], 1);
+      mbar_init(&s_bar[1], 1);
+      mbar_fence_init();
+      s_dead = 0;
+    }
+    __syncwarp();
+    cluster_arrive();
+  }
   T* tiles = reinterpret_cast<T*>(s_tiles);
   // behind them, of a cluster: [2][K blocks][32]
   ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 3 * kTile);

@@ -31,16 +31,6 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (known to be the warp's)
   const unsigned K = p.cluster, rank = K > 1 ? cluster_rank() : 0;
-  if (K > 1) {
-    if (threadIdx.x == 0) {
-      mbar_init(&s_bar[0], 1);
-      mbar_init(&s_bar[1], 1);
-      mbar_fence_init();
-      s_dead = 0;
-    }
-    __syncwarp();
-    cluster_arrive();
-  }
   const unsigned unit = blockIdx.x / K;
   const long long row = unit / p.tiles;
   const int tile = (int)(unit - (unsigned)row * p.tiles);
@@ -57,6 +47,17 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   const f32x2 rate = kGate == GLR_RATE ? load_f32(p.rate + c, vec, c0, c1) : 0ull;
   f32x2 carry = !packed && p.h0 ? load_f32(p.h0 + row * p.D + c, vec, c0, c1) : 0ull;
 
+  // (the state is read before the others hear of this block: the last token's block may write it in place)
+  if (K > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(&s_bar[0], 1);
+      mbar_init(&s_bar[1], 1);
+      mbar_fence_init();
+      s_dead = 0;
+    }
+    __syncwarp();
+    cluster_arrive();
+  }
   T* tiles = reinterpret_cast<T*>(s_tiles);
   // behind them, of a cluster: [2][K blocks][32]
   ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 2 * kTile);
