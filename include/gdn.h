@@ -345,7 +345,9 @@ gdn_status kda_recurrent_step(const void* q, const void* k, const void* v, const
  * ---- The layer around the forwards -------------------------------------------------
  *
  * The operators a linear-attention layer runs before and after gdn_chunk_fwd,
- * kda_chunk_fwd and ssd_chunk_fwd, and the Mamba-1 member of the family.  The
+ * kda_chunk_fwd and ssd_chunk_fwd, the Mamba-1 member of the family, and the
+ * gated linear recurrence; the last and layer norm and rotary positions with
+ * their gradients.  The
  * pages name the projection side only as fused operators ("Empowering Hybrid
  * Attention Models on NPUs", §7 Implementation); the formulas are the
  * published ones of these layers.  The conventions at the top hold, except:
@@ -528,7 +530,8 @@ gdn_status gdn_rms_norm_fwd_e4m3_f32(const float* x, const float* w, const float
  *
  *   dx, dg   [tokens, D] bf16;  drate [D] fp32, exactly with rate;  dh0 [N, D] fp32 or NULL
  *
- * The states come from fp32 throughout, never from rounded y; sums are fp32 in a fixed order.  With
+ * The states come from fp32 throughout, never from rounded y; sums are fp32 in an order fixed by the
+ * sizes (drate's by the rows' alignment, too: rows on narrow accesses are cut otherwise in time).  With
  * .._SQRT the weight has no derivative at a_t = 1; its share of dg is left out there.  The rate's
  * gradient needs gdn_glr_chunk_bwd_workspace_size(...) bytes (0: none), as the S6 scan's workspace.
  */

@@ -148,58 +148,67 @@ __device__ __forceinline__ void copy_wide(T* tile, const T* src, long long strid
     tile += step * kPitch;
   }
 }
-__device__ __forceinline__ void cp_async4(void* to, const void* from, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(ok ? 4 : 0)
-               : "memory");
+__device__ __forceinline__ void cp_async4(void* to, const void* from, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(bytes) : "memory");
 }
-// 4 bytes an asynchronous copy, a row a warp: with a row's place known to the whole warp and several rows
-// unrolled, its instructions keep ahead of its latency (a word a thread, by one count over the tile: 2.5
-// times the kernel's time).
+template <int kPitch, typename T>
+__device__ __forceinline__ void clear_rows(T* tile, int from, int to) {
+  unsigned* words = reinterpret_cast<unsigned*>(tile);
+  constexpr int kWords = kPitch * (int)sizeof(T) / 4;
+  for (int i = from * kWords + threadIdx.x; i < to * kWords; i += blockDim.x) words[i] = 0u;
+}
+// 4 bytes an asynchronous copy, a row a warp, nothing but pointers that move on in the loop over the rows
+// that exist: a block has few warps, so what counts is the length of the chain of instructions.
 template <int kPitch, typename T>
 __device__ __noinline__ void copy_words(T* tile, const T* src, long long stride, int rows, int tokens, int cols) {
   constexpr int kCols = 4 / (int)sizeof(T);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  const int col = lane * kCols;
-  const T* from = src + warp * stride + col;
+  const int col = lane * kCols, have = min(rows, tokens);
+  const int some = col < cols ? 4 : 0, more = col + 32 < cols ? 4 : 0;
+  const T* from = src + warp * stride + (some ? col : 0);
   T* to = tile + warp * kPitch + col;
   const long long by = warps * stride;
 #pragma unroll 8
-  for (int row = warp; row < tokens; row += warps, from += by, to += warps * kPitch) {
-    const bool ok = col < cols && row < rows;
-    cp_async4(to, ok ? from : src, ok);
-    if (kCols == 1) {
-      const bool more = col + 32 < cols && row < rows;
-      cp_async4(to + 32, more ? from + 32 : src, more);
-    }
+  for (int row = warp; row < have; row += warps, from += by, to += warps * kPitch) {
+    cp_async4(to, from, some);
+    if (kCols == 1) cp_async4(to + 32, more ? from + 32 : from, more);
   }
+  clear_rows<kPitch>(tile, have, tokens);
 }
 // Odd rows of bf16 so, 4 aligned bytes a copy: those of a row that begins between two words lie one element
-// further on.  A word that the row shares with a neighbour is copied whole, what is not the row's is not read
-// from the tile; only a word that would reach out of the operand (from `begin` to `end`) is a plain load of
-// its half.
+// further on.  A word that the row shares with a neighbour is copied whole, what is not the row's is not
+// stored from the tile; the operand's first and last row (from `begin` to `end`), whose words may reach out of
+// it, go by elements.  Every other row of a warp begins alike.
 template <int kPitch>
 __device__ __noinline__ void copy_odd(uint16_t* tile, const uint16_t* src, long long stride, int rows, int tokens,
                                       int cols, const uint16_t* begin, const uint16_t* end) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  const int have = min(rows, tokens);
   const unsigned odd = odd_rows(src, stride);
-  const uint16_t* none = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(src) & ~3ull);
-  const uint16_t* from = src + warp * stride + 2 * lane;
-  uint16_t* to = tile + warp * kPitch + 2 * lane;
-  const long long by = warps * stride;
-#pragma unroll 4
-  for (int row = warp; row < tokens; row += warps, from += by, to += warps * kPitch) {
-    const int shift = odd >> (row & 31) & 1;
-    const auto word = [&](const uint16_t* w, uint16_t* at, int col) {  // column col is the word's first
-      const bool wanted = row < rows && col < cols, inside = w >= begin && w + 2 <= end;
-      cp_async4(at, wanted && inside ? w : none, wanted && inside);
-      if (wanted && !inside) {
-        if (w >= begin) at[0] = w[0];
-        else at[1] = w[1];
-      }
-    };
-    word(from - shift, to, 2 * lane - shift);
-    if (lane == 0 && shift) word(from + 63, to + 64, 63);
+  const auto shift_of = [&](int row) { return (int)(odd >> (row & 31) & 1u); };
+  const int lo = src == begin ? 1 : 0;
+  const int hi = have > 0 && src + (have - 1) * stride + cols >= end ? have - 1 : have;
+  const long long by = 2 * warps * stride;
+#pragma unroll 1
+  for (int j = 0; j < 2; ++j) {
+    int row = warp + j * warps;
+    const int shift = shift_of(row), some = 2 * lane - shift < cols ? 4 : 0;
+    const uint16_t* from = src + row * stride + (some ? 2 * lane - shift : shift);
+    uint16_t* to = tile + row * kPitch + 2 * lane;
+    if (row < lo) row += 2 * warps, from += by, to += 2 * warps * kPitch;
+#pragma unroll 8
+    for (; row < hi; row += 2 * warps, from += by, to += 2 * warps * kPitch) cp_async4(to, from, some);
   }
+  if (cols == 64)  // the 33rd words
+    for (int row = lo + threadIdx.x; row < hi; row += blockDim.x)
+      if (shift_of(row)) cp_async4(tile + row * kPitch + 64, src + row * stride + 63, 4);
+  const auto by_elements = [&](int row) {
+    for (int col = threadIdx.x; col < cols; col += blockDim.x)
+      tile[row * kPitch + shift_of(row) + col] = src[row * stride + col];
+  };
+  if (lo > 0 && have > 0) by_elements(0);
+  if (hi < have && hi >= lo) by_elements(hi);
+  clear_rows<kPitch>(tile, have, tokens);
 }
 // piece: bytes that rows are made of and aligned to; begin, end: the operand
 template <bool kGeneral, typename T>
