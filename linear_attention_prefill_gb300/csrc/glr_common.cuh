@@ -86,35 +86,35 @@ __device__ __forceinline__ void store_f32(float* p, f32x2 x, bool vec, bool c0, 
   r.v = x;
   r.store(p, vec, c0, c1);
 }
-// The pair of an output: rows of the plain kernels are aligned to pairs, of the general ones one of two ways, each
-// store under its own condition (a branch would keep the tokens' arithmetic apart).
+// The pair of an output: a kernel of narrow rows stores in one of two ways, each under its own condition
+// (a branch would keep the tokens' arithmetic apart).
 struct Places {
   bool pair, first, second;
 };
-template <bool kGeneral>
+template <bool kNarrow>
 __device__ __forceinline__ Places places(bool vec, bool c0, bool c1) {
-  return {c0 && (!kGeneral || vec), c0 && !vec, c1 && !vec};
+  return {c0 && (!kNarrow || vec), c0 && !vec, c1 && !vec};
 }
-template <bool kGeneral, typename T>
+template <bool kNarrow, typename T>
 __device__ __forceinline__ void store_out(T* p, f32x2 x, const Places& at) {
   Raw2<T> o;
   o.set(x);
   if (at.pair) o.store(p, true, true, true);
-  if (kGeneral) {
+  if (kNarrow) {
     if (at.first) o.store(p, false, true, false);
     if (at.second) o.store(p, false, false, true);
   }
 }
 // Tiles lie in shared memory as tokens of 64 channels, `pitch` elements apart.  Rows of bf16 that are not
 // aligned to pairs (odd rows) lie one element further on: bit i of their mask is token i's.
-template <typename T, bool kGeneral>
-constexpr int kPitch = kGeneral && sizeof(T) == 2 ? 72 : 64;
-template <bool kGeneral, typename T>
+template <typename T, bool kNarrow>
+constexpr int kPitch = kNarrow && sizeof(T) == 2 ? 72 : 64;
+template <bool kNarrow, typename T>
 __device__ __forceinline__ f32x2 pair_at(const T* tile, int token, int lane, unsigned odd) {
-  const T* q = tile + token * kPitch<T, kGeneral> + 2 * lane;
+  const T* q = tile + token * kPitch<T, kNarrow> + 2 * lane;
   Raw2<T> r;
   r.load(q, true, true, true);
-  if constexpr (kGeneral && sizeof(T) == 2) {
+  if constexpr (kNarrow && sizeof(T) == 2) {
     Raw2<T> next;
     next.load(q + 2, true, true, true);
     r.v = __funnelshift_r(r.v, next.v, odd >> token & 1 ? 16 : 0);
@@ -211,13 +211,13 @@ __device__ __noinline__ void copy_odd(uint16_t* tile, const uint16_t* src, long 
   clear_rows<kPitch>(tile, have, tokens);
 }
 // piece: bytes that rows are made of and aligned to; begin, end: the operand
-template <bool kGeneral, typename T>
+template <bool kNarrow, typename T>
 __device__ __forceinline__ void copy_tile(T* tile, const T* src, long long stride, int rows, int tokens, int cols,
                                           int piece, const void* begin, long long length) {
-  constexpr int kP = kPitch<T, kGeneral>;
+  constexpr int kP = kPitch<T, kNarrow>;
   if (piece == 16) {
     copy_wide<kP>(tile, src, stride, rows, tokens, cols);
-  } else if (!kGeneral || sizeof(T) == 4 || piece == 4) {
+  } else if (!kNarrow || sizeof(T) == 4 || piece == 4) {
     copy_words<kP>(tile, src, stride, rows, tokens, cols);
   } else {
     const uint16_t* first = static_cast<const uint16_t*>(begin);

@@ -6,9 +6,13 @@
 // until the state before them is known.  In a round the blocks of a cluster take 64 tokens each of
 // the same 64 channels: every thread reduces its 16 tokens to (A, H), the warps exchange these through
 // shared memory and the blocks through each other's, and a second walk over the 16 tokens, now
-// from the right state, writes y.  Tiles arrive by asynchronous copies, two rounds ahead.
+// from the right state, writes y.  Tiles arrive by asynchronous copies, one round ahead.
 //
 // State, products and sums are fp32; y is rounded once.
+//
+// 65536 x 2560 in bf16 takes 254 us, 4.0 TB/s: instruction issue bounds it (60 % of its slots) at 14 warps an SM,
+// which cannot hide all of the exchange.  16 tokens a thread is what 128 registers hold, and four
+// blocks of four warps an SM; with 8 tokens the rounds were twice as many and the time longer.
 #pragma once
 
 #include "glr_common.cuh"
@@ -17,12 +21,13 @@ namespace gdn {
 namespace {
 
 constexpr int kMinBlocks = kGlrFwdBlocks, kStages = 2, kRun = kGlrFwdRun, kWarps = kGlrFwdWarps;
-template <typename T, bool kGeneral>
-constexpr int kTileOf = kRun * kWarps * kPitch<T, kGeneral>;  // of a tensor's tokens in shared memory
+template <typename T, bool kNarrow>
+constexpr int kTileOf = kRun * kWarps * kPitch<T, kNarrow>;  // of a tensor's tokens in shared memory
 
-template <typename T, int kGate, int kNorm, bool kGeneral>
+// kGeneral: borders between tokens (packed rows); kNarrow: rows that are not aligned to pairs
+template <typename T, int kGate, int kNorm, bool kGeneral, bool kNarrow>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) glr_fwd_kernel(const GlrParams p) {
-  constexpr int kTile = kTileOf<T, kGeneral>;
+  constexpr int kTile = kTileOf<T, kNarrow>;
   extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][tokens][64 channels and padding]
   __shared__ ulonglong2 s_warp[2][kWarps][32];
   __shared__ uint64_t s_bar[2];
@@ -34,10 +39,10 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   const unsigned unit = blockIdx.x / K;
   const long long row = unit / p.tiles;
   const int tile = (int)(unit - (unsigned)row * p.tiles);
-  const bool vec = !kGeneral || p.vec;
+  const bool vec = !kNarrow || p.vec;
   const long long c = (long long)tile * 64 + 2 * lane;
   const bool c0 = c < p.D, c1 = c + 1 < p.D;
-  const Places at = places<kGeneral>(vec, c0, c1);
+  const Places at = places<kNarrow>(vec, c0, c1);
   __shared__ int32_t s_cu[kGeneral ? kBorders : 1];
   const bool packed = kGeneral && p.cu;
   const int32_t* cu = kGeneral ? take_borders(p, s_cu) : nullptr;
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   T* tiles = reinterpret_cast<T*>(s_tiles);
   // behind them, of a cluster: [2][K blocks][32]
   ulonglong2* const s_rank = reinterpret_cast<ulonglong2*>(tiles + kStages * 2 * kTile);
-  const bool odd = kGeneral && sizeof(T) == 2 && p.piece == 2;
+  const bool odd = kNarrow && sizeof(T) == 2 && p.piece == 2;
   const int cols = (int)min(64ll, p.D - (long long)tile * 64);
   const long long tokens = packed ? p.T : (long long)p.N * p.T;
   const auto fetch = [&](unsigned r) {  // round r into its stage
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       for (int k = 0; k < 2; ++k, to += kTile) {
         const void* from = k ? p.g : p.x;
         const long long stride = k ? p.g_stride : p.x_stride;
-        copy_tile<kGeneral>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span,
+        copy_tile<kNarrow>(to, static_cast<const T*>(from) + (row * p.T + first) * stride + tile * 64ll, stride, left, span,
                              cols, p.piece, from, (tokens - 1) * stride + p.D);
       }
     }
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     cp_async_wait<0>();
     __syncthreads();
     fetch(r + 1);
-    const T* xs = tiles + r % kStages * (2 * kTile) + warp * kRun * kPitch<T, kGeneral>;
+    const T* xs = tiles + r % kStages * (2 * kTile) + warp * kRun * kPitch<T, kNarrow>;
     const T* gs = xs + kTile;
     const int n = t < end ? (int)min(end - t, (unsigned)kRun) : 0;  // tokens that exist
     const unsigned xsodd = odd && n ? odd_rows(static_cast<const T*>(p.x) + (row * p.T + t) * p.x_stride + tile * 64ll, p.x_stride) : 0u;
@@ -99,8 +104,8 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     const unsigned borders = packed && n ? borders_of(cu, p.N, (int)end, (int)t, kRun) : 0u;
     // The first border among the run's tokens (a sequence starts there, or the last one ended before it), and
     // the state that it starts from.  One border, and fewer tokens than a run has, are dealt with by
-    // selects: branches between the tokens would keep their arithmetic apart (8 x 2048 x 2560 training: 172 us
-    // for 142).  Runs with more borders are rare.
+    // selects: branches between the tokens would keep their arithmetic apart (the gradient of 8 x 2048 x 2560
+    // took 172 us so, 147 now).  Runs with more borders are rare.
     const int border = kGeneral && borders ? __ffs(borders) - 1 : 2 * kRun;
     const bool many = kGeneral && (borders & (borders - 1)) != 0;
     f32x2 start = 0ull;
@@ -111,8 +116,8 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       f32x2 s;
-      gate2<kGate, kNorm>(pair_at<kGeneral>(gs, i, lane, gsodd), rate, a[i], s);
-      b[i] = pair_at<kGeneral>(xs, i, lane, xsodd);
+      gate2<kGate, kNorm>(pair_at<kNarrow>(gs, i, lane, gsodd), rate, a[i], s);
+      b[i] = pair_at<kNarrow>(xs, i, lane, xsodd);
       if (kNorm != GLR_NONE) b[i] = mul2(s, b[i]);
       H = fma2(a[i], kGeneral ? pick(i == border, start, H) : H, b[i]);
       A = mul2(A, a[i]);
@@ -173,11 +178,11 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     if (p.states && t % kGlrChunk == 0 && n)
       store_f32(p.states + (row * p.chunks + t / kGlrChunk) * p.D + c, h, vec, c0, c1);
     T* to = y;
-    if (!kGeneral && n == kRun) {
+    if (n == kRun && !borders) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i, to += p.D) {
         h = fma2(a[i], h, b[i]);
-        store_out<kGeneral>(to, h, at);
+        store_out<kNarrow>(to, h, at);
       }
       if (p.hT && t + kRun == end) store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
     } else if (!many) {
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
 #pragma unroll
       for (int i = 0; i < kRun; ++i, to += p.D) {
         h = fma2(a[i], kGeneral ? pick(i == border, start, h) : h, b[i]);
-        if (i < n) store_out<kGeneral>(to, h, at);
+        if (i < n) store_out<kNarrow>(to, h, at);
         final = pick(i + 1 == last, h, final);
       }
       if (p.hT && last > 0 && last <= n) {
@@ -198,7 +203,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       for (int i = 0; i < kRun; ++i, to += p.D) {
         if (i >= n) break;
         h = borders >> i & 1 ? b[i] : fma2(a[i], h, b[i]);
-        store_out<kGeneral>(to, h, at);
+        store_out<kNarrow>(to, h, at);
         if (p.hT && borders >> (i + 1) & 1)
           store_f32(p.hT + (long long)sequence_of(cu, p.N, (int)end, (int)t + i) * p.D + c, h, vec, c0, c1);
       }
@@ -239,9 +244,9 @@ __global__ void __launch_bounds__(128) glr_step_kernel(const GlrParams p) {
   store_f32(p.hT + row * p.D + c, h, vec, c0, c1);
 }
 
-template <auto kKernel, typename T, bool kGeneral>
+template <auto kKernel, typename T, bool kNarrow>
 cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
-  const size_t smem = kStages * 2 * kTileOf<T, kGeneral> * sizeof(T);
+  const size_t smem = kStages * 2 * kTileOf<T, kNarrow> * sizeof(T);
   const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
   cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
   if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
@@ -255,9 +260,11 @@ cudaError_t launch(const GlrParams& p, bool step, cudaStream_t stream) {
     glr_step_kernel<T, kGate, kNorm><<<(unsigned)(((long long)p.N * p.tiles + 3) / 4), 128, 0, stream>>>(p);
     return cudaGetLastError();
   }
-  // packed rows, and rows that are not aligned to pairs
-  return p.cu || !p.vec || p.piece == 2 ? launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true>, T, true>(p, stream)
-              : launch_prompt<glr_fwd_kernel<T, kGate, kNorm, false>, T, false>(p, stream);
+  // each has the borders' arithmetic or the odd rows' only where it needs it (packed rows of pairs, 2560 x 32768
+  // bf16 forwards: 179 us, 200 with the arithmetic of odd rows)
+  if (!p.vec || p.piece == 2) return launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true, true>, T, true>(p, stream);
+  return p.cu ? launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true, false>, T, false>(p, stream)
+              : launch_prompt<glr_fwd_kernel<T, kGate, kNorm, false, false>, T, false>(p, stream);
 }
 template <typename T, int kGate>
 cudaError_t launch_gate(const GlrParams& p, bool step, cudaStream_t stream) {

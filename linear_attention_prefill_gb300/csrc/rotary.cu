@@ -7,8 +7,8 @@
 // modulo 2^64 is the angle modulo one turn, exactly, at any position; of an fp32 angle at position
 // 2^20 only 4 bits behind the point would be left.  A block takes a few tokens: it makes their
 // cosines and sines once, a pair a thread, and walks all heads of q and k with them, in one launch.
-// The first loads are under way meanwhile.  HBM bandwidth bounds it: every element crosses once each
-// way.  Products are fp32, rounded once.
+// The first loads are under way meanwhile.  Every element crosses HBM once each way; loads in flight bound it
+// (q and k of 4096 tokens, 16 heads of 128 in bf16: 16 us, 4.2 TB/s).  Products are fp32, rounded once.
 #include "layer_common.cuh"
 #include "layer_internal.h"
 
