@@ -140,18 +140,19 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     if (kGeneral && border > 0 && border <= n && p.dhT)
       finish = load_f32(p.dhT + (long long)sequence_of(cu, p.N, (int)end, (int)t + border - 1) * p.D + c, vec, c0, c1);
     f32x2 a[kRun], s[kRun];
-    f32x2 A = dup2(1.f), H = 0ull, M = 0ull, lam = 0ull;
+    f32x2 P = dup2(kWhole), H = 0ull, M = 0ull, lam = 0ull;
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       gate2<kGate, kNorm>(pair_at<kNarrow>(gs, i, lane, gsodd), rate, a[i], s[i]);
       const f32x2 x = pair_at<kNarrow>(xs, i, lane, xsodd);
       H = fma2(a[i], kGeneral ? pick(i == border, start, H) : H, kNorm == GLR_NONE ? x : mul2(s[i], x));
       if (!full) a[i] = pick(i < n, a[i], dup2(1.f));  // (tokens that do not exist pass m on)
-      A = mul2(A, a[i]);
+      P = mul2(P, a[i]);
     }
-    A = at_least_tiny(A);
+    // a border among the tokens, or behind them, cuts what goes on from them; many of them both ways
+    const bool apart = kGeneral && border < kRun, apart_back = kGeneral && (many || (border > 0 && border <= kRun));
+    P = at_least(P);
     if (!(kGeneral && many)) {
-      s_ahead[turn][warp][lane] = make_ulonglong2(kGeneral && border < kRun ? 0ull : A, H);
       // backwards: m before these tokens from m behind them
 #pragma unroll
       for (int i = kRun - 1; i >= 0; --i) {
@@ -162,7 +163,6 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
                         kGeneral ? pick(ends, finish, lam) : lam, dy);
       }
       M = mul2(a[0], lam);
-      if (kGeneral && border > 0 && border <= kRun) A = 0ull;
     } else {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
@@ -174,7 +174,6 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
                                : 0ull;
         H = fma2(a[i], from, kNorm == GLR_NONE ? x : mul2(s[i], x));
       }
-      s_ahead[turn][warp][lane] = make_ulonglong2(0ull, H);
 #pragma unroll
       for (int i = kRun - 1; i >= 0; --i) {
         const f32x2 dy = pair_at<kNarrow>(ds, i, lane, dsodd);
@@ -182,47 +181,38 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
         if (i < n && borders >> (i + 1) & 1) lam = with_last(p, cu, dy, (int)end, (int)t + i, c, c0, c1);
       }
       M = mul2(a[0], lam);
-      A = 0ull;
     }
-    s_back[turn][warp][lane] = make_ulonglong2(A, M);
+    s_ahead[turn][warp][lane] = make_ulonglong2(apart ? 0ull : P, H);
+    s_back[turn][warp][lane] = make_ulonglong2(apart_back ? 0ull : P, M);
     __syncthreads();
     for (int w = warp / kChunkWarps * kChunkWarps; w < warp; ++w) {
       const ulonglong2 v = s_ahead[turn][w][lane];
       h = through<kGeneral>(v.x, v.y, h);
     }
-    f32x2 sA = dup2(1.f), sM = 0ull;
-    const auto lead = [&](int from, int to) {  // warps from - 1 down to `to`
-#pragma unroll 4
-      for (int w = from - 1; w >= to; --w) {
-        const ulonglong2 v = s_back[turn][w][lane];
-        follow<kGeneral>(sA, sM, v.x, v.y);
-      }
-    };
-    lead(warps, warp + 1);
-    A = sA, M = sM;
-    lead(warp + 1, 0);
+    // the warps behind this one, last to first; (P, M) becomes what lies behind this warp's
+    f32x2 sP = dup2(kWhole), sM = 0ull;
+    ulonglong2 runs[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) runs[w] = w < warps ? s_back[turn][w][lane] : make_ulonglong2(dup2(kWhole), 0ull);
+#pragma unroll
+    for (int w = kWarps - 1; w >= 0; --w) {
+      if (w == warp) P = sP, M = sM;
+      follow<kGeneral>(sP, sM, runs[w].x, runs[w].y);
+    }
     f32x2 m = carry;
     if (K > 1) {
+      const f32x2 sent = to_send<kGeneral>(sP);
       if (!*dead) {
-        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sA, sM);
+        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sent, sM);
       }
       wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
-      f32x2 now = carry;
-      const auto pass = [&](int from, int to) {
-#pragma unroll 4
-        for (int k = from - 1; k >= to; --k) {
-          const ulonglong2 v = s_rank[(turn * K + k) * 32 + lane];
-          now = through<kGeneral>(v.x, v.y, now);
-        }
-      };
-      pass((int)K, (int)rank + 1);
-      m = now;
-      pass((int)rank + 1, 0);
-      carry = now;
+      // (the last block first)
+      const ulonglong2 v = pass_blocks<kGeneral>(carry, s_rank + (turn * K + K - 1) * 32 + lane, -32, (int)(K - 1 - rank), (int)K);
+      m = v.x, carry = v.y;
     } else {
-      carry = through<kGeneral>(sA, sM, carry);
+      carry = through<kGeneral>(sP, sM, carry);
     }
-    m = through<kGeneral>(A, M, m);
+    m = through<kGeneral>(P, M, m);
     T* dx = static_cast<T*>(p.dx) + (row * p.T + t + kRun) * p.D + c;
     T* dg = static_cast<T*>(p.dg) + (row * p.T + t + kRun) * p.D + c;
     f32x2 hp[kRun];  // the state before each token

@@ -19,8 +19,6 @@
 
 namespace gdn {
 
-constexpr float kTiny = 1.17549435e-38f;  // 2^-126
-
 // ---- two channels of a row ---------------------------------------------------------------
 // Channels 2 lane, 2 lane + 1 of a warp's 64: in one access where rows are aligned to pairs (vec).
 template <typename T>
@@ -292,36 +290,95 @@ __device__ __forceinline__ void gate2(f32x2 g, f32x2 rate, f32x2& a, f32x2& s) {
   s = pack2(s0, s1);
 }
 
+// a where `take`, else b
+__device__ __forceinline__ f32x2 pick(bool take, f32x2 a, f32x2 b) {
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(take ? a0 : b0, take ? a1 : b1);
+}
+
 // ---- stretches of time ---------------------------------------------------------------------
-// A product of decays that underflows stays at 2^-126: an infinite state before it stays infinite,
-// as it does token by token, and of finite ones nothing is left either way.  A = 0 is a border: what
-// lies behind it sees nothing from before, not even infinities.
-__device__ __forceinline__ f32x2 at_least_tiny(f32x2 a) {
-  return each(a, [](float v) { return fmaxf(v, kTiny); });
+// A stretch maps the state h before it to A h + H.  Its product of decays A is held 2^108 times as large (P): by
+// itself it underflows within a few tokens of closed gates, and a state near fp32's largest would come out of it
+// wrong by up to 4.  P keeps all its digits down to A = 2^-234, and what its roundings below that make of any finite
+// state is less than 2^-129, below fp32's normal numbers.  P stays at 2^-149 or above: an infinite state stays
+// infinite, as it does token by token, and of finite ones less than 2^-128 is left.  P = 0 (A = 0) is a border: what
+// lies behind it sees nothing from before, not even infinities.  (Decays, at most 1; a product above 2^20 would
+// overflow.)
+constexpr float kWhole = 0x1p108f, kLeast = 0x1p-149f;  // P of no tokens; of an underflown product
+__device__ __forceinline__ f32x2 at_least(f32x2 P) {
+  return each(P, [](float v) { return fmaxf(v, kLeast); });
 }
-template <bool kBorders>
-__device__ __forceinline__ f32x2 through(f32x2 A, f32x2 H, f32x2 h) {  // A h + H
-  if (!kBorders) return fma2(A, h, H);
-  float a0, a1, b0, b1, r0, r1;
-  unpack2(A, a0, a1);
+// H behind a border (P or A = 0), else r
+__device__ __forceinline__ f32x2 unless_border(f32x2 P, f32x2 H, f32x2 r) {
+  float p0, p1, b0, b1, r0, r1;
+  unpack2(P, p0, p1);
   unpack2(H, b0, b1);
-  unpack2(fma2(A, h, H), r0, r1);
-  return pack2(a0 == 0.f ? b0 : r0, a1 == 0.f ? b1 : r1);
+  unpack2(r, r0, r1);
+  return pack2(p0 == 0.f ? b0 : r0, p1 == 0.f ? b1 : r1);
 }
-// (A, H) followed by (B, G)
+// A x is (f x) k with f = min(P, 1), k = max(P, 1) / 2^108.  One of them is a power of two, 1 for P from 1 on (the
+// same bits as of A), and neither step underflows before the result does.
+struct Factors {
+  f32x2 f, k;
+};
+__device__ __forceinline__ Factors factors(f32x2 P) {
+  return {each(P, [](float v) { return fminf(v, 1.f); }),
+          mul2(each(P, [](float v) { return fmaxf(v, 1.f); }), dup2(1.f / kWhole))};
+}
 template <bool kBorders>
-__device__ __forceinline__ void follow(f32x2& A, f32x2& H, f32x2 B, f32x2 G) {
-  H = through<kBorders>(B, G, H);
-  const f32x2 product = at_least_tiny(mul2(A, B));
-  if (!kBorders) {
-    A = product;
-    return;
+__device__ __forceinline__ f32x2 through(f32x2 P, f32x2 H, f32x2 h) {  // A h + H
+  const Factors a = factors(P);
+  const f32x2 r = fma2(mul2(a.f, h), a.k, H);
+  return kBorders ? unless_border(P, H, r) : r;
+}
+// (P, H) followed by (Q, G)
+template <bool kBorders>
+__device__ __forceinline__ void follow(f32x2& P, f32x2& H, f32x2 Q, f32x2 G) {
+  const Factors b = factors(Q);
+  H = through<kBorders>(Q, G, H);
+  const f32x2 product = at_least(mul2(mul2(b.f, P), b.k));
+  P = kBorders ? unless_border(P, 0ull, unless_border(Q, 0ull, product)) : product;
+}
+
+// What a block of a cluster sends of its stretch: A, or -P of a lane's two channels if one of them is deep, P < 1,
+// which 64 tokens rarely are.  The receivers go through all as if none were, and again if a sign says so (the
+// factors of all for all made 65536 x 2560 7 % slower).
+template <bool kBorders>
+__device__ __forceinline__ f32x2 to_send(f32x2 P) {
+  float p0, p1;
+  unpack2(P, p0, p1);
+  const bool deep = fminf(p0, p1) < 1.f && !(kBorders && P == 0ull);
+  return mul2(P, dup2(deep ? -1.f : 1.f / kWhole));
+}
+// The states before the block after `first` others of the cluster's, and behind all of them, from h before them.
+template <bool kBorders>
+__device__ __forceinline__ ulonglong2 pass_blocks(f32x2 h, const ulonglong2* sent, int step, int first, int blocks) {
+  const f32x2 h0 = h;
+  unsigned signs = 0u;
+  const auto some = [&](int from, int to) {
+#pragma unroll 4
+    for (int k = from; k < to; ++k) {
+      const ulonglong2 v = sent[k * step];
+      signs |= (unsigned)(v.x >> 32);
+      const f32x2 r = fma2(v.x, h, v.y);
+      h = kBorders ? unless_border(v.x, v.y, r) : r;
+    }
+  };
+  some(0, first);
+  f32x2 before = h;
+  some(first, blocks);
+  if ((int)signs < 0) {
+    h = h0;
+#pragma unroll 1
+    for (int k = 0; k < blocks; ++k, sent += step) {
+      const ulonglong2 v = *sent;
+      before = pick(k == first, h, before);
+      h = through<kBorders>(mul2(v.x, dup2((long long)v.x < 0 ? -1.f : kWhole)), v.y, h);
+    }
   }
-  float a0, a1, b0, b1, p0, p1;
-  unpack2(A, a0, a1);
-  unpack2(B, b0, b1);
-  unpack2(product, p0, p1);
-  A = pack2(a0 == 0.f || b0 == 0.f ? 0.f : p0, a1 == 0.f || b1 == 0.f ? 0.f : p1);
+  return make_ulonglong2(before, h);
 }
 
 // ---- sequence borders of a packed row ------------------------------------------------------
@@ -365,14 +422,6 @@ static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int
     m = first_border_above(cu, N, end, b);
   }
   return bits;
-}
-
-// a where `take`, else b
-__device__ __forceinline__ f32x2 pick(bool take, f32x2 a, f32x2 b) {
-  float a0, a1, b0, b1;
-  unpack2(a, a0, a1);
-  unpack2(b, b0, b1);
-  return pack2(take ? a0 : b0, take ? a1 : b1);
 }
 
 // ---- launches --------------------------------------------------------------------------------

@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   constexpr int kTile = kTileOf<T, kNarrow>;
   extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g][tokens][64 channels and padding]
   __shared__ ulonglong2 s_warp[2][kWarps][32];
+  __shared__ ulonglong2 s_state[32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
   volatile int* const dead = &s_dead;
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     if (kGeneral && border < n && p.h0)
       start = load_f32(p.h0 + (long long)sequence_of(cu, p.N, (int)end, (int)t + border) * p.D + c, vec, c0, c1);
     f32x2 a[kRun], b[kRun];
-    f32x2 A = dup2(1.f), H = 0ull;
+    f32x2 P = dup2(kWhole), H = 0ull;
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       f32x2 s;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       b[i] = pair_at<kNarrow>(xs, i, lane, xsodd);
       if (kNorm != GLR_NONE) b[i] = mul2(s, b[i]);
       H = fma2(a[i], kGeneral ? pick(i == border, start, H) : H, b[i]);
-      A = mul2(A, a[i]);
+      P = mul2(P, a[i]);
     }
     if (kGeneral && many) {
 #pragma unroll
@@ -137,44 +138,34 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       }
     }
     // (behind the last token nothing is read from h: what zeros make of the gates there does not matter)
-    A = kGeneral && border < kRun ? 0ull : at_least_tiny(A);
-    s_warp[turn][warp][lane] = make_ulonglong2(A, H);
+    s_warp[turn][warp][lane] = make_ulonglong2(kGeneral && border < kRun ? 0ull : at_least(P), H);
     __syncthreads();
-    // all the warps' stretches in order; (A, H) becomes what lies before this warp's
-    f32x2 sA = dup2(1.f), sH = 0ull;
-    const auto lead = [&](int from, int to) {
-#pragma unroll 4
-      for (int w = from; w < to; ++w) {
-        const ulonglong2 v = s_warp[turn][w][lane];
-        follow<kGeneral>(sA, sH, v.x, v.y);
-      }
-    };
-    lead(0, warp);
-    A = sA, H = sH;
+    // all the warps' stretches in order; (P, H) becomes what lies before this warp's
+    f32x2 sP = dup2(kWhole), sH = 0ull;
+    ulonglong2 runs[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) runs[w] = w < warps ? s_warp[turn][w][lane] : make_ulonglong2(dup2(kWhole), 0ull);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) P = sP, H = sH;
+      follow<kGeneral>(sP, sH, runs[w].x, runs[w].y);
+    }
     f32x2 h = carry;
     if (K > 1) {
-      lead(warp, warps);
+      const f32x2 sent = to_send<kGeneral>(sP);
       if (!*dead) {
-        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sA, sH);
+        for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sent, sH);
       }
-      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
-      f32x2 now = carry;
-      const auto pass = [&](unsigned from, unsigned to) {
-#pragma unroll 4
-        for (unsigned k = from; k < to; ++k) {
-          const ulonglong2 v = s_rank[(turn * K + k) * 32 + lane];
-          now = through<kGeneral>(v.x, v.y, now);
-        }
-      };
-      pass(0, rank);
-      h = now;
-      pass(rank, K);
-      carry = now;
+      if (warp == 0) {  // (one warp for all: fewer instructions, and fewer waits)
+        wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
+        s_state[lane] = pass_blocks<kGeneral>(carry, s_rank + turn * K * 32 + lane, 32, (int)rank, (int)K);
+      }
+      __syncthreads();
+      h = s_state[lane].x, carry = s_state[lane].y;
     } else {
-      lead(warp, warps);
-      carry = through<kGeneral>(sA, sH, carry);
+      carry = through<kGeneral>(sP, sH, carry);
     }
-    h = through<kGeneral>(A, H, h);
+    h = through<kGeneral>(P, H, h);
     if (p.states && t % kGlrChunk == 0 && n)
       store_f32(p.states + (row * p.chunks + t / kGlrChunk) * p.D + c, h, vec, c0, c1);
     T* to = y;
