@@ -336,7 +336,7 @@ template <auto kKernel, typename T, bool kNarrow>
 cudaError_t launch_prompt(GlrParams p, cudaStream_t stream) {
   const size_t smem = kStages * 3 * kTileOf<T, kNarrow> * sizeof(T);
   const int warps = p.T > kRun * (kWarps - 1) ? kWarps : p.T > kRun ? (p.T - 1) / kRun + 1 : 1;
-  cudaError_t e = choose_cluster<kKernel>(&p, 32 * warps, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
+  cudaError_t e = choose_cluster<kKernel, 32 * kWarps>(&p, smem, ((long long)p.T + kRun * kWarps - 1) / (kRun * kWarps));
   if (e == cudaSuccess && p.cluster > 1) e = device_error_word(&p.err);
   if (e == cudaSuccess) e = launch_clusters(kKernel, glr_grid(p), 32 * warps, p.cluster, p, stream,
                          glr_smem(smem, p.cluster), glr_smem(smem, kGlrMaxCluster));

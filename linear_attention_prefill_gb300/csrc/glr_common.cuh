@@ -428,22 +428,25 @@ static __device__ __noinline__ unsigned borders_of(const int32_t* cu, int N, int
 // Blocks of a cluster: they go on together through a row's `spans`, and as many clusters as there is room
 // for run at once, which depends on the size (of 256 threads at two blocks an SM, 36 clusters of 8 but only
 // 14 of 14 fit this GPU).  The size with the fewest rounds over all waves of clusters is taken.  The GPU is
-// asked once for each kernel and size.
+// asked once for each kernel and size: rows of more than one span have blocks of kThreads threads, the others one
+// block of however many.
 inline size_t glr_smem(size_t tiles, int blocks) { return tiles + (blocks > 1 ? blocks * 1024 : 0); }
-template <auto kKernel>
-cudaError_t choose_cluster(GlrParams* p, unsigned threads, size_t tiles, long long spans) {
+template <auto kKernel, unsigned kThreads>
+cudaError_t choose_cluster(GlrParams* p, size_t tiles, long long spans) {
   static std::atomic<int> room[kGlrMaxCluster + 1];
   const long long units = glr_units(*p);
   long long best = -1;
-  for (int k = 1; k <= kGlrMaxCluster && (k == 1 || k <= spans); ++k) {
+  p->cluster = 1;
+  if (spans <= 1) return cudaSuccess;
+  for (int k = 1; k <= kGlrMaxCluster && k <= spans; ++k) {
     const size_t smem = glr_smem(tiles, k);
     int n = room[k].load(std::memory_order_relaxed);
     if (!n) {
       cudaError_t e = allow_clusters(kKernel, k, glr_smem(tiles, kGlrMaxCluster));
       if (e != cudaSuccess) return e;
-      const ClusterConfig c(k, threads, k, smem, nullptr);
+      const ClusterConfig c(k, kThreads, k, smem, nullptr);
       if (k == 1) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, threads, smem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, kThreads, smem);
         n *= kSms;
       } else {
         e = cudaOccupancyMaxActiveClusters(&n, kKernel, &c.cfg);
