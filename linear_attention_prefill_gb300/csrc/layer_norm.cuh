@@ -8,6 +8,7 @@
 #pragma once
 
 #include <atomic>
+#include <cstddef>
 
 #include "cluster.cuh"
 #include "layer_common.cuh"
@@ -18,10 +19,11 @@ namespace gdn {
 // Sums over the block of kCount (1, 2, 4 or 8) values a thread.  Lanes halve the values that they go on
 // with at each step: 8 values take 9 shuffles, not 40, and as many again over the warps' sums.  `turn`
 // alternates, and the shared memory with it, so that one barrier a sum is enough.
-struct LnShared {
+struct alignas(16) LnShared {
   float warp[2][8][32];
-  float rank[2][4][4];
+  float rank[2][4][4];  // (written by 16 bytes)
 };
+static_assert(alignof(LnShared) % 16 == 0 && offsetof(LnShared, rank) % 16 == 0, "stores of 16 bytes into `rank`");
 template <int kCount>
 __device__ __forceinline__ float scatter_sums(float (&v)[kCount], int lane) {  // the lane's one of them
   int off = 16;
