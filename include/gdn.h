@@ -673,6 +673,8 @@ gdn_status gdn_device_status(gdn_stream_t stream);
  * Returns GDN_OK once enqueued.
  */
 gdn_status gdn_selftest_expired_wait(long long limit_cycles, gdn_stream_t stream);
+/* The same of two blocks of a cluster that wait for each other's sums, which neither sends. */
+gdn_status gdn_selftest_expired_cluster_wait(long long limit_cycles, gdn_stream_t stream);
 
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status s);

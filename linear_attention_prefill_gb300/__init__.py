@@ -11,7 +11,7 @@ rotary positions (layer.py).
 """
 from .binding import (GdnError, HostPipeline, chain_kind, gdn_chunk_fwd, gdn_chunk_fwd_host, gdn_chunk_fwd_prologue,
                       gdn_chunk_fwd_workspace_size, gdn_recurrent_step_prologue,
-                      gdn_device_status, gdn_recurrent_step, gdn_selftest_expired_wait,
+                      gdn_device_status, gdn_recurrent_step, gdn_selftest_expired_cluster_wait, gdn_selftest_expired_wait,
                       kda_chunk_fwd, kda_chunk_fwd_workspace_size, kda_recurrent_step,
                       load_library, ssd_chunk_fwd, ssd_recurrent_step, status_string)
 from .layer import (gdn_glr_chunk_bwd, gdn_glr_chunk_bwd_workspace_size, gdn_glr_chunk_fwd,
@@ -22,7 +22,8 @@ from .layer import (gdn_glr_chunk_bwd, gdn_glr_chunk_bwd_workspace_size, gdn_glr
 
 __all__ = ["GdnError", "HostPipeline", "chain_kind", "gdn_chunk_fwd", "gdn_chunk_fwd_host", "gdn_chunk_fwd_prologue",
            "gdn_chunk_fwd_workspace_size", "gdn_recurrent_step_prologue",
-           "gdn_device_status", "gdn_recurrent_step", "gdn_selftest_expired_wait", "load_library",
+           "gdn_device_status", "gdn_recurrent_step", "gdn_selftest_expired_cluster_wait", "gdn_selftest_expired_wait",
+           "load_library",
            "kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_recurrent_step",
            "ssd_chunk_fwd", "ssd_recurrent_step", "status_string", "gdn_rms_norm_fwd",
            "gdn_s6_chunk_fwd", "gdn_s6_chunk_fwd_workspace_size", "gdn_s6_recurrent_step",

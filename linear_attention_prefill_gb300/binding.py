@@ -66,6 +66,7 @@ SIGNATURES = {
     "kda_recurrent_step": (_I, _STEP_ARGS),
     "gdn_device_status": (_I, [_P]),
     "gdn_selftest_expired_wait": (_I, [ctypes.c_longlong, _P]),
+    "gdn_selftest_expired_cluster_wait": (_I, [ctypes.c_longlong, _P]),
     "gdn_status_string": (ctypes.c_char_p, [_I]),
     "gdn_last_error": (ctypes.c_char_p, []),
     "gdn_abi_version": (_I, []),
@@ -412,6 +413,12 @@ def gdn_selftest_expired_wait(limit_cycles: int = 1 << 20, stream=None):
     """Enqueue the timeout-path diagnostic (a bounded wait that is bound to expire)."""
     dev = torch.device("cuda", torch.cuda.current_device())
     _check(load_library().gdn_selftest_expired_wait(int(limit_cycles), _stream_handle(stream, dev)))
+
+
+def gdn_selftest_expired_cluster_wait(limit_cycles: int = 1 << 20, stream=None):
+    """The same of two blocks of a cluster that wait for each other."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    _check(load_library().gdn_selftest_expired_cluster_wait(int(limit_cycles), _stream_handle(stream, dev)))
 
 
 def gdn_device_status(stream=None):

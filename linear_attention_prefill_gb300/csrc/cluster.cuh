@@ -45,9 +45,10 @@ __device__ __forceinline__ void send_to_rank(void* local, uint64_t* bar, unsigne
                "l"(a), "l"(b), "r"(its)
                : "memory");
 }
-// Wait for phase `parity` of `bar`, whose bytes come from the cluster; gives up after about a second and
-// records that, and from then on (`dead`) no wait of the block lasts.
-__device__ __forceinline__ void wait_for_ranks(uint64_t* bar, unsigned parity, unsigned* err, volatile int* dead) {
+// Wait for phase `parity` of `bar`, whose bytes come from the cluster; gives up after `limit` cycles (about a
+// second) and records that, and from then on (`dead`) no wait of the block lasts.
+__device__ __forceinline__ void wait_for_ranks(uint64_t* bar, unsigned parity, unsigned* err, volatile int* dead,
+                                               long long limit = 1ll << 31) {
   const auto done = [&] {
     unsigned ok;
     asm volatile(
@@ -61,10 +62,21 @@ __device__ __forceinline__ void wait_for_ranks(uint64_t* bar, unsigned parity, u
   if (done()) return;
   const long long t0 = clock64();
   while (!done()) {
-    if (*dead || clock64() - t0 > (1ll << 31)) {
+    if (*dead || clock64() - t0 > limit) {
       if (!*dead) record_error(err, kErrWaitTimeout);
       *dead = 1;
       return;
+    }
+  }
+}
+// The end of a block that exchanges so: no block leaves before its neighbours have sent what they send.  To one
+// that has given up a wait some of that may be on its way still; it takes microseconds, and half a millisecond is
+// waited.
+__device__ __forceinline__ void leave_ranks(volatile int* dead) {
+  cluster_sync();
+  if (*dead) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1ll << 20)) {
     }
   }
 }

@@ -9,6 +9,7 @@
 
 #include "../../include/gdn.h"
 #include "abi_common.h"
+#include "cluster.cuh"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
 #include "layer_internal.h"
@@ -48,6 +49,24 @@ __global__ void selftest_expired_wait_kernel(unsigned* err, long long limit) {
   }
   __syncwarp();
   if (threadIdx.x == 0) mbar_wait_limit(&bar, 0, err, limit);
+}
+
+// The same of blocks of a cluster that expect each other's bytes, none of which are sent: both give up, and leave
+// as the kernels' blocks do.
+__global__ void selftest_expired_cluster_wait_kernel(unsigned* err, long long limit) {
+  __shared__ uint64_t bar;
+  __shared__ int s_dead;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    mbar_fence_init();
+    s_dead = 0;
+  }
+  __syncwarp();
+  cluster_sync();
+  if (threadIdx.x == 0) mbar_expect_tx(&bar, 2 * 32 * 16);
+  wait_for_ranks(&bar, 0, err, &s_dead, limit);
+  __syncwarp();
+  leave_ranks(&s_dead);
 }
 
 // Input check of an _ex call: every log-decay g <= 0 and finite (with the fused
@@ -612,6 +631,17 @@ gdn_status gdn_selftest_expired_wait(long long limit_cycles, gdn_stream_t stream
       err, limit_cycles);
   e = cudaGetLastError();
   return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the expired-wait self-test");
+}
+
+gdn_status gdn_selftest_expired_cluster_wait(long long limit_cycles, gdn_stream_t stream) {
+  if (limit_cycles < 0 || limit_cycles > (1ll << 31))
+    return fail(GDN_ERR_INVALID_ARG, "limit_cycles=%lld must be in [0, 2^31]", limit_cycles);
+  unsigned* err = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&err), gdn::g_device_error);
+  if (e != cudaSuccess) return cuda_fail(e, "locating the device error word");
+  const gdn::ClusterConfig c(2, 32, 2, 0, reinterpret_cast<cudaStream_t>(stream));
+  e = cudaLaunchKernelEx(&c.cfg, gdn::selftest_expired_cluster_wait_kernel, err, limit_cycles);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e, "launching the expired-cluster-wait self-test");
 }
 
 gdn_status gdn_device_status(gdn_stream_t stream) {

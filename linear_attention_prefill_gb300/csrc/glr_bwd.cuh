@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     }
   }
   cp_async_wait<0>();
-  if (K > 1) cluster_sync();  // no block leaves before its neighbours have sent what they send
+  if (K > 1) leave_ranks(dead);
   if (kGate == GLR_RATE) {  // the block's sum, its warps in order
     __syncthreads();
     f32x2* sum = reinterpret_cast<f32x2*>(&s_ahead[0][0][0]);

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     y += (long long)round * p.D;
   }
   cp_async_wait<0>();
-  if (K > 1) cluster_sync();  // no block leaves before its neighbours have sent what they send
+  if (K > 1) leave_ranks(dead);
   if (!p.hT || p.hT == p.h0) return;
   if (!packed) {  // no token at all
     if (rounds == 0 && rank == 0 && warp == 0) store_f32(p.hT + row * p.D + c, carry, vec, c0, c1);
