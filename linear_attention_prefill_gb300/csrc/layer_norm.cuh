@@ -193,14 +193,14 @@ inline int ln_blocks(int D) {
 // As many blocks as are resident together, each takes its rows in turn.  The GPU is asked once for each kernel
 // and block.
 template <auto kKernel>
-cudaError_t ln_resident(int threads, size_t smem, int* blocks) {
+cudaError_t ln_resident(int threads, int* blocks) {
   static std::atomic<int> known[33];
-  int n = smem ? 0 : known[threads / 32].load(std::memory_order_relaxed);
+  int n = known[threads / 32].load(std::memory_order_relaxed);
   if (!n) {
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, threads, smem);
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, threads, 0);
     if (e != cudaSuccess) return e;
     if (n < 1) n = 1;
-    if (!smem) known[threads / 32].store(n, std::memory_order_relaxed);
+    known[threads / 32].store(n, std::memory_order_relaxed);
   }
   *blocks = n;
   return cudaSuccess;
@@ -208,7 +208,7 @@ cudaError_t ln_resident(int threads, size_t smem, int* blocks) {
 template <auto kKernel>
 cudaError_t ln_grid(const LnParams& p, int G, int threads, unsigned* grid) {
   int resident = 0;
-  const cudaError_t e = ln_resident<kKernel>(threads, 0, &resident);
+  const cudaError_t e = ln_resident<kKernel>(threads, &resident);
   const long long per_block = G ? threads / G : 1, units = (p.rows + per_block - 1) / per_block;
   const long long most = (long long)resident * kSms / p.blocks;
   *grid = (unsigned)((units < most ? units : most) * p.blocks);
