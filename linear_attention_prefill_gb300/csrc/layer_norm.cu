@@ -200,7 +200,11 @@ cudaError_t launch_t(const LnParams& p, cudaStream_t stream) {
   if (p.D <= 256) return launch<T, kWhole, 32, 1>(p, stream);
   if (p.D <= 512) return launch<T, kWhole, 32, 2>(p, stream);
   if (kWhole && p.blocks == 1 && p.rows >= kLnRingRows) {
-    const LnRing shape = ln_ring<T>(p, p.residual ? 2 : 1);
+    // Two blocks an SM up to 704 threads together in bf16, 640 in fp32, whose rows leave the ring fewer places: 16332 x
+    // 2568 takes 56 us in bf16 with two and 82 with one, 14894 x 2816 64 and 75, 8166 x 2568 in fp32 62 and 56.
+    const LnRing shape = ln_ring<T>(p, p.residual ? 2 : 1, ln_blocks(p.D, sizeof(T) == 2 ? 704 : 640));
+    // Two rows a sum where two more are on their way meanwhile.  Two and one in bf16: 64 and 73 us of 65536 x 640, 57
+    // and 67 of 20480 x 2048, 55 and 62 of 8192 x 5120; 65 and 59 of 40960 x 1024, 64 and 58 of 6826 x 6144.
     if (shape.slots >= 4) return launch_ring<T, 2>(p, shape, stream);
     return launch_ring<T, 1>(p, shape, stream);
   }

@@ -183,11 +183,14 @@ __device__ __forceinline__ float both(f32x2 v) {
 }
 __device__ __forceinline__ float sum8(const f32x2 (&v)[4]) { return both(add2(add2(v[0], v[1]), add2(v[2], v[3]))); }
 
-// Blocks an SM for rows of a block: about 640 threads together.  It is by the row's length alone: how rows are
-// dealt out to blocks decides the order of the parameters' gradients.
-inline int ln_blocks(int D) {
+// Blocks an SM for rows of a block: about `most` threads together, 640 in the gradient.  There it is by the row's
+// length alone: how rows are dealt out to blocks decides the order of the parameters' gradients.  The gradient in
+// bf16 with 640, 1024 and 320 threads: 65.7, 75.9 and 105 us of 40960 x 1024, 65.2, 77.0 and 95.9 of 16384 x 2560, 97.4,
+// 100.3 and 97.4 of 16332 x 2568 (one block, two, one), 71.9, 75.1 and 71.9 of 10240 x 4096.  (ln_partials: the most
+// blocks of any length on either side of 2560.)
+inline int ln_blocks(int D, int most = 640) {
   const int threads = (D / 8 + 31) / 32 * 32;
-  return threads > 320 ? 1 : 640 / threads > 8 ? 8 : 640 / threads;
+  return threads > most / 2 ? 1 : most / threads > 8 ? 8 : most / threads;
 }
 
 // As many blocks as are resident together, each takes its rows in turn.  The GPU is asked once for each kernel
@@ -221,12 +224,16 @@ constexpr int kLnRingBytes = 208 * 1024, kLnRingSlots = 16;
 struct LnRing {
   int slots, slot_bytes, blocks;  // of a block, of a row, of an SM
 };
-constexpr long long kLnRingRows = 4 * kSms;  // rows for which it pays: every block has a few
+// Rows for which it pays: every block has a few.  With and without the ring in bf16, forward and gradient: 304 x 2560
+// 4.3 and 3.8, 8.4 and 8.9 us; 608 x 2560 4.8 and 4.8, 8.9 and 10.9; 1216 x 2560 6.3 and 6.7, 10.4 and 15.0; 304 x 5120 4.8
+// and 4.8, 10.9 and 12.5; 1216 x 5120 9.9 and 10.9, 17.6 and 25.3; 8192 x 5120 54.7 and 68.9, 68.0 and 150.  (Forwards
+// at some widths the rows in registers are as fast: 40960 x 1024 65 and 56, 20480 x 2048 57 and 57.)
+constexpr long long kLnRingRows = 4 * kSms;
 template <typename T>
-LnRing ln_ring(const LnParams& p, int tensors) {
+LnRing ln_ring(const LnParams& p, int tensors, int blocks) {
   LnRing r;
   r.slot_bytes = p.D * (int)sizeof(T) * tensors;
-  r.blocks = ln_blocks(p.D);
+  r.blocks = blocks;
   r.slots = kLnRingBytes / r.blocks / r.slot_bytes;  // (two rows at least)
   if (r.slots > 8) r.slots = 8;
   return r;

@@ -272,9 +272,12 @@ cudaError_t launch_t(const LnParams& p, cudaStream_t stream) {
   if (p.D <= 256) return launch<T, kWhole, 32, 1, kParams>(p, stream);
   if (p.D <= 512) return launch<T, kWhole, 32, 2, kParams>(p, stream);
   if (kWhole && p.blocks == 1 && p.rows >= kLnRingRows) {
-    const LnRing shape = ln_ring<T>(p, p.residual ? 3 : 2);
-    // two rows take 88 registers: up to 640 threads have them
+    const LnRing shape = ln_ring<T>(p, p.residual ? 3 : 2, ln_blocks(p.D));
+    // Two rows take 90 registers, which 640 threads have; 704 have 80 (8192 x 5120 compiled so takes 76 us for 68), wider
+    // rows fewer.  Two and one in bf16: 65 and 77 us of 16384 x 2560, 68 and 82 of 8192 x 5120, 81 and 87 of 8179 x 5128,
+    // 79 and 81 of 7447 x 5632.
     if (shape.slots >= 4 && p.D <= 8 * 640) return launch_ring<T, 2, kParams, 640>(p, shape, stream);
+    if (shape.slots >= 4 && p.D <= 8 * 704) return launch_ring<T, 2, kParams, 704>(p, shape, stream);
     return launch_ring<T, 1, kParams, 1024>(p, shape, stream);
   }
   if (p.slice <= 8 * 512) return launch<T, kWhole, 0, 1, kParams, 512>(p, stream);
