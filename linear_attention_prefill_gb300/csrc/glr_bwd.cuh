@@ -14,7 +14,7 @@
 // read once, dx and dg written once.  Where s = 0 (a = 1 exactly) the weight has no derivative; its
 // share is left out.
 //
-// 8 x 2048 x 2560 in bf16 with rate and sqrt takes 147 us, 2.9 TB/s, bound by instruction issue (63 % of its slots)
+// 8 x 2048 x 2560 in bf16 with rate and sqrt takes 146 us, 2.9 TB/s, bound by instruction issue (64 % of its slots)
 // at 12 warps an SM: 168 registers hold 16 tokens' decays, weights and states.
 //
 // A product that goes on into a sum is written as one operation: the compiler joins packed ones of its own, in
@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
   constexpr int kTile = kTileOf<T, kNarrow>;
   extern __shared__ __align__(16) unsigned char s_tiles[];  // [stages][x, g, dy][tokens][64 channels and padding]
   __shared__ ulonglong2 s_ahead[2][kWarps][32], s_back[2][kWarps][32];
+  __shared__ ulonglong2 s_state[32];
   __shared__ uint64_t s_bar[2];
   __shared__ int s_dead;
   volatile int* const dead = &s_dead;
@@ -205,10 +206,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       if (!*dead) {
         for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sent, sM);
       }
-      wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
-      // (the last block first)
-      const ulonglong2 v = pass_blocks<kGeneral>(carry, s_rank + (turn * K + K - 1) * 32 + lane, -32, (int)(K - 1 - rank), (int)K);
-      m = v.x, carry = v.y;
+      if (warp == 0) {  // (one warp for all, the last block first)
+        wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
+        s_state[lane] = pass_blocks<kGeneral>(carry, s_rank + (turn * K + K - 1) * 32 + lane, -32, (int)(K - 1 - rank), (int)K);
+      }
+      __syncthreads();
+      m = s_state[lane].x, carry = s_state[lane].y;
     } else {
       carry = through<kGeneral>(sP, sM, carry);
     }

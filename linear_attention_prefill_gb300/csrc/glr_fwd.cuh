@@ -10,7 +10,7 @@
 //
 // State, products and sums are fp32; y is rounded once.
 //
-// 65536 x 2560 in bf16 takes 254 us, 4.0 TB/s: instruction issue bounds it (60 % of its slots) at 14 warps an SM,
+// 65536 x 2560 in bf16 takes 256 us, 3.9 TB/s: instruction issue bounds it (60 % of its slots) at 14 warps an SM,
 // which cannot hide all of the exchange.  16 tokens a thread is what 128 registers hold, and four
 // blocks of four warps an SM; with 8 tokens the rounds were twice as many and the time longer.
 #pragma once
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
     // The first border among the run's tokens (a sequence starts there, or the last one ended before it), and
     // the state that it starts from.  One border, and fewer tokens than a run has, are dealt with by
     // selects: branches between the tokens would keep their arithmetic apart (the gradient of 8 x 2048 x 2560
-    // took 172 us so, 147 now).  Runs with more borders are rare.
+    // took 172 us so, 146 now).  Runs with more borders are rare.
     const int border = kGeneral && borders ? __ffs(borders) - 1 : 2 * kRun;
     const bool many = kGeneral && (borders & (borders - 1)) != 0;
     f32x2 start = 0ull;
@@ -156,7 +156,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? kMinBlocks : 1) 
       if (!*dead) {
         for (unsigned k = warp; k < K; k += warps) send_to_rank(&s_rank[(turn * K + rank) * 32 + lane], &s_bar[turn], k, sent, sH);
       }
-      if (warp == 0) {  // (one warp for all: fewer instructions, and fewer waits)
+      // One warp for all: fewer instructions.  In graphs 65536 x 2560 takes 254 us, 265 by every warp, the gradient of
+      // 10007 x 1111 108 and 110.
+      if (warp == 0) {
         wait_for_ranks(&s_bar[turn], r >> 1 & 1, p.err, dead);
         s_state[lane] = pass_blocks<kGeneral>(carry, s_rank + turn * K * 32 + lane, 32, (int)rank, (int)K);
       }
@@ -252,7 +254,7 @@ cudaError_t launch(const GlrParams& p, bool step, cudaStream_t stream) {
     return cudaGetLastError();
   }
   // each has the borders' arithmetic or the odd rows' only where it needs it (packed rows of pairs, 2560 x 32768
-  // bf16 forwards: 179 us, 200 with the arithmetic of odd rows)
+  // bf16 forwards, log gate and 1 - a: 180 us, 200 with the arithmetic of odd rows)
   if (!p.vec || p.piece == 2) return launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true, true>, T, true>(p, stream);
   return p.cu ? launch_prompt<glr_fwd_kernel<T, kGate, kNorm, true, false>, T, false>(p, stream)
               : launch_prompt<glr_fwd_kernel<T, kGate, kNorm, false, false>, T, false>(p, stream);
