@@ -526,14 +526,16 @@ gdn_status gdn_rms_norm_fwd_e4m3_f32(const float* x, const float* w, const float
  *
  * gdn_glr_chunk_bwd - the gradient.  x, g, rate, h0, gate, input_norm, cu_seqlens and states as in
  * (and from) the forward; dy [tokens, D] (dy_stride) and dhT [N, D] fp32 (or NULL) are the
- * gradients of y and hT.
+ * gradients of y and hT.  h0 is what it was before the forward: with cu_seqlens it is read, so that a forward in place
+ * (hT == h0) needs a copy of it.
  *
  *   dx, dg   [tokens, D] bf16;  drate [D] fp32, exactly with rate;  dh0 [N, D] fp32 or NULL
  *
  * The states come from fp32 throughout, never from rounded y; sums are fp32 in an order fixed by the
  * sizes (drate's by the rows' alignment, too: rows on narrow accesses are cut otherwise in time).  With
  * .._SQRT the weight has no derivative at a_t = 1; its share of dg is left out there.  The rate's
- * gradient needs gdn_glr_chunk_bwd_workspace_size(...) bytes (0: none), as the S6 scan's workspace.
+ * gradient needs gdn_glr_chunk_bwd_workspace_size(...) bytes (0: none), as the S6 scan's workspace: 4 D for each row and
+ * each 64 tokens of it, 16 of them at most.
  */
 enum { GDN_GLR_GATE_LOG = 0, GDN_GLR_GATE_SIGMOID = 1, GDN_GLR_GATE_RATE = 2 };
 enum { GDN_GLR_INPUT_PLAIN = 0, GDN_GLR_INPUT_LINEAR = 1, GDN_GLR_INPUT_SQRT = 2 };

@@ -228,7 +228,8 @@ def gdn_glr_chunk_bwd(dy, x, g, states, rate=None, h0=None, dhT=None, dx=None, d
 
     dy [B, T, D] (x's type, may be a slice) and dhT [N, D] fp32 (or None for zeros) are the gradients of
     y and hT; ``states`` is the forward's, the other inputs and the form are the same as there.
-    drate [D] fp32 is None without a rate, dh0 [N, D] fp32 None without h0 (unless given).
+    drate [D] fp32 is None without a rate, dh0 [N, D] fp32 None without h0 (unless given).  h0 is what it
+    was before the forward: with cu_seqlens it is read, so that a forward in place needs a copy of it.
     ``workspace``: a uint8 device tensor of at least gdn_glr_chunk_bwd_workspace_size bytes, or None for
     a fresh one where one is needed.
     """
